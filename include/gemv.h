@@ -7,6 +7,8 @@
  *   h = silu(A_gate·x) ⊙ (A_up·x)     gemv_gate_up_silu_*
  *   y = A·x for few, long rows        gemv_splitk_* (caller's workspace)
  *   y = scale ⊙ (Q·x), int8 Q         gemv_q8_f32 / gemv_q8_f16 / gemv_q8_bf16
+ *   e4m3, a scale per block of 128    gemv_fp8_quantise_*, gemv_fp8_* (any number of vectors)
+ *   a paged 8-bit key/value cache     gemv_kv_append_*, gemv_kv_attend_*
  *
  * The operation.  Output m is the dot product of row m of A with x (page
  * "SGEMV CUDA代码学习", section "问题定义: 一行一个点积": A is M×K, x is K×1,
@@ -260,6 +262,200 @@ gemv_status_t gemv_q8_f16(const int8_t *Q, int ldq, const float *scale,
 gemv_status_t gemv_q8_bf16(const int8_t *Q, int ldq, const float *scale,
                            const uint16_t *x, const float *bias, float *y,
                            int M, int K, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * 8-bit floating point with a scale for each block of 128.  Where gemv_q8_*
+ * halves the weight bytes with one scale a row, these hold weights and
+ * activations in e4m3 (the OCP format: 4 exponent and 3 mantissa bits, largest
+ * value 448, no infinities) with one fp32 scale for each 128 columns, so that
+ * a far larger value costs precision in its own block only, and both operands
+ * go to the matrix cores as they are.
+ * ------------------------------------------------------------------------ */
+#define GEMV_FP8_BLOCK 128
+
+/* Quantise X (rows x K, row-major with row stride ldx, of the element type in
+ * the name):
+ *
+ *   scale[r / block_rows, b] = max(amax / 448, 2^-126), amax = max |X| over
+ *                              block_rows rows and columns 128b .. 128b+127
+ *   Q = e4m3(X · (1 / scale)), to nearest even
+ *
+ * with the division, the reciprocal and the product in IEEE fp32.
+ *
+ * block_rows  1 (activations: a scale per row and 128 columns) or 128
+ *             (weights: a scale per 128 x 128 block).
+ * Q           rows x K e4m3 bytes, row stride ldq >= K (bytes K..ldq-1 of a
+ *             row are never written).
+ * scale       ceil(rows / block_rows) x ceil(K / 128) fp32, row stride
+ *             lds >= ceil(K / 128).
+ * A block that holds an infinity or a NaN gets an infinity or a NaN as its
+ * scale, and so reads as NaN; other blocks are not affected.  Q and scale
+ * must not overlap X or each other.
+ * Errors as for gemv_*: GEMV_ERROR_INVALID_VALUE for a negative size, a pitch
+ * that is too small, another block_rows, more than 65535·128 rows
+ * with block_rows 128, or a pointer that is NULL or not aligned to its element
+ * size.  rows == 0 or K == 0 enqueues nothing. */
+gemv_status_t gemv_fp8_quantise_f32(const float *X, int ldx, uint8_t *Q, int ldq,
+                                   float *scale, int lds, int rows, int K,
+                                   int block_rows, hipStream_t stream);
+gemv_status_t gemv_fp8_quantise_f16(const uint16_t *X, int ldx, uint8_t *Q, int ldq,
+                                   float *scale, int lds, int rows, int K,
+                                   int block_rows, hipStream_t stream);
+gemv_status_t gemv_fp8_quantise_bf16(const uint16_t *X, int ldx, uint8_t *Q, int ldq,
+                                   float *scale, int lds, int rows, int K,
+                                   int block_rows, hipStream_t stream);
+
+/* Y = W·X (+ bias added to every column) for e4m3 W and X with block scales:
+ *
+ *   Y[t, m] = Σ_b x_scale[t, b]·w_scale[m / 128, b]·Σ_{k in block b} W[m,k]·X[t,k] + bias[m]
+ *
+ * W        M x K e4m3 bytes, row stride ldw >= K; w_scale ceil(M / 128) x
+ *          ceil(K / 128) fp32, row stride ldws.
+ * X        nvec rows of K e4m3 bytes, row stride ldx >= K; x_scale nvec x
+ *          ceil(K / 128) fp32, row stride ldxs.  nvec is any number >= 0: one
+ *          decoded token, a batch of them, or a prompt.
+ * bias     M fp32 values, or NULL.
+ * Y        nvec rows of M values of the type in the name, row stride ldy >= M.
+ * A block's products are exact and are summed in fp32 on the matrix cores;
+ * its sum is scaled and added in fp32; the result is rounded to Y's type once.
+ * Results are deterministic, and a token's result does not depend on the other
+ * tokens' values.  16-byte aligned W and X with pitches and K of whole 16 bytes select
+ * the widest loads; any other layout works.
+ * Errors as for gemv_*.  M == 0 or nvec == 0 enqueues nothing; K == 0 writes
+ * the bias (or 0). */
+gemv_status_t gemv_fp8_f32(const uint8_t *W, int ldw, const float *w_scale,
+                          int ldws, const uint8_t *X, int ldx,
+                          const float *x_scale, int ldxs, const float *bias,
+                          float *Y, int ldy, int M, int K, int nvec,
+                          hipStream_t stream);
+gemv_status_t gemv_fp8_f16(const uint8_t *W, int ldw, const float *w_scale,
+                          int ldws, const uint8_t *X, int ldx,
+                          const float *x_scale, int ldxs, const float *bias,
+                          uint16_t *Y, int ldy, int M, int K, int nvec,
+                          hipStream_t stream);
+gemv_status_t gemv_fp8_bf16(const uint8_t *W, int ldw, const float *w_scale,
+                          int ldws, const uint8_t *X, int ldx,
+                          const float *x_scale, int ldxs, const float *bias,
+                          uint16_t *Y, int ldy, int M, int K, int nvec,
+                          hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * A paged key/value cache in 8 bits, with a scale for each block of tokens
+ * and head: the other half of a decode step, between the q/k/v projections
+ * and the output projection.
+ *
+ * The cache holds `pages` pages of page_size tokens.  A page is cut into
+ * blocks of GEMV_KV_BLOCK tokens; a block of one head has one fp32 scale for
+ * its keys and one for its values.  All memory is the caller's:
+ *
+ *   k        [pages][heads][page_size][dim] bytes
+ *   v        [pages][heads][page_size / 16][dim][16] bytes: the 16 tokens of
+ *            a block lie together for each dim, as the matrix cores read them
+ *   k_scale  [pages][heads][page_size / 16] fp32
+ *   v_scale  the same
+ *
+ * A value is its byte times its block's scale.  Bytes are int8 (-127..127) or
+ * e4m3.  A new cache needs no initial contents.
+ * ------------------------------------------------------------------------ */
+#define GEMV_KV_BLOCK 16
+
+typedef enum { GEMV_KV_INT8 = 0, GEMV_KV_E4M3 = 1 } gemv_kv_format_t;
+
+typedef struct {
+    int format;       /* gemv_kv_format_t */
+    int pages;        /* >= 1 */
+    int heads;        /* key/value heads, 1..65535 */
+    int page_size;    /* 16, 32, 64, 128 or 256 tokens */
+    int dim;          /* 64, 128 or 256 */
+    void *k, *v;      /* 16-byte aligned */
+    float *k_scale, *v_scale;
+} gemv_kv_cache_t;
+
+/* Which tokens a call is about.  Token j of sequence b lies in page
+ * table[b·table_pitch + j / page_size]; tokens past table_width pages, or in
+ * an entry outside 0..pages-1, are not there: they are not written and not
+ * seen.  seq_lens[b] is the sequence's length with the call's tokens; these
+ * are its last starts[b+1] - starts[b], in rows starts[b] .. starts[b+1]-1 of
+ * the call's matrices.  Rows from starts[sequences] on are padding, and are
+ * neither read nor written.  starts == NULL: every sequence has one row.
+ * All three arrays are device memory, read by the kernels only. */
+typedef struct {
+    int sequences;
+    const int *table;
+    int table_pitch, table_width; /* entries between rows, entries of a row */
+    const int *seq_lens;          /* [sequences] */
+    const int *starts;            /* [sequences + 1], ascending from 0, or NULL */
+} gemv_kv_batch_t;
+
+/* Write the keys and values of the batch's new tokens into the cache.  K and V
+ * are rows x heads x dim of the type in the name, ldk and ldv elements
+ * from row to row (so they may be columns of one wider matrix).
+ *
+ * Each block that gets tokens takes the smallest power of two s >= 2^-126 with
+ * |value| <= qmax·s for all its new values (qmax is 127 or 448), or the scale
+ * of its earlier tokens where that is larger; earlier tokens whose scale grows
+ * are rounded to the new one (in e4m3 that changes subnormals only).  A byte is
+ * value·(1/s), or earlier byte·(earlier scale / s), in IEEE fp32 and rounded to
+ * nearest even.  A block that gets an infinity or a NaN has the
+ * scale NaN and zero bytes, and reads as NaN until its first token is written
+ * again.  Bytes and scales behind a sequence's last token are left as they
+ * were.  Blocks that a call writes must belong to one sequence only (pages
+ * shared by several sequences are for reading).
+ * Errors: GEMV_ERROR_INVALID_VALUE for a cache or batch that is not as above,
+ * negative sizes, a pitch below heads·dim, rows != sequences without starts, a
+ * NULL or misaligned pointer. */
+gemv_status_t gemv_kv_append_f32(const gemv_kv_cache_t *cache, const float *K,
+                                int ldk, const float *V, int ldv, int rows,
+                                const gemv_kv_batch_t *batch,
+                                hipStream_t stream);
+gemv_status_t gemv_kv_append_f16(const gemv_kv_cache_t *cache, const uint16_t *K,
+                                int ldk, const uint16_t *V, int ldv, int rows,
+                                const gemv_kv_batch_t *batch,
+                                hipStream_t stream);
+gemv_status_t gemv_kv_append_bf16(const gemv_kv_cache_t *cache, const uint16_t *K,
+                                int ldk, const uint16_t *V, int ldv, int rows,
+                                const gemv_kv_batch_t *batch,
+                                hipStream_t stream);
+
+/* Attention of the batch's new tokens over the cache (which holds their own
+ * keys and values already):
+ *
+ *   O[i, h] = Σ_j softmax_j(scale·Q[i,h]·K[j, h/G])·V[j, h/G],  G = q_heads / heads
+ *
+ * over the tokens j that row i, at position p of its sequence, sees: j <= p
+ * and, where window > 0, also p - j < window or j < sinks (the first `sinks`
+ * tokens stay visible).  A row that sees no token gives 0.  Tokens that a row
+ * does not see do not affect it, whatever their blocks' scales.
+ *
+ * Q, O  rows x q_heads x dim of the type in the name, ldq and ldo elements
+ *       from row to row; O must not overlap the other arguments.
+ * scale finite; usually 1/sqrt(dim).
+ * workspace  device memory of at least gemv_kv_attend_workspace_size bytes,
+ *       16-byte aligned (may be NULL where that is 0); contract as for
+ *       gemv_splitk_*.
+ * Q and the cache's bytes enter the products exactly; scores, the softmax and
+ * its sums are fp32; a softmax weight is rounded to Q's type before it meets V,
+ * and the result once.  Deterministic: the order in which tokens are joined
+ * depends on the sizes only.
+ * Errors: as for gemv_kv_append_*, plus a q_heads that heads does not divide,
+ * rows·q_heads past 2^31 - 1, a negative window or sinks, a scale that is not
+ * finite, and a workspace that is too small. */
+gemv_status_t gemv_kv_attend_workspace_size(int q_heads, int heads, int dim,
+                                            int rows, int sequences,
+                                            int table_width, int page_size,
+                                            size_t *bytes);
+gemv_status_t gemv_kv_attend_f16(const gemv_kv_cache_t *cache, const uint16_t *Q,
+                                int ldq, uint16_t *O, int ldo, int q_heads,
+                                int rows, const gemv_kv_batch_t *batch,
+                                float scale, int window, int sinks,
+                                void *workspace, size_t workspace_bytes,
+                                hipStream_t stream);
+gemv_status_t gemv_kv_attend_bf16(const gemv_kv_cache_t *cache, const uint16_t *Q,
+                                int ldq, uint16_t *O, int ldo, int q_heads,
+                                int rows, const gemv_kv_batch_t *batch,
+                                float scale, int window, int sinks,
+                                void *workspace, size_t workspace_bytes,
+                                hipStream_t stream);
 
 /* ------------------------------------------------------------------------
  * Introspection and testing.  These do not change what the entry points

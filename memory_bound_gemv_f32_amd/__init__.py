@@ -9,12 +9,16 @@ Two levels:
 
 * the C ABI under the same names (``gemv_f32``, ``gemv_f16``, ``gemv_bf16``,
   ``gemv_batched_*``, ``gemv_multi_*``, ``gemv_gate_up_silu_*``,
-  ``gemv_splitk_*``, ``gemv_q8_*``, ``gemv_plan``, ``gemv_run_family``, ...), taking integer
-  addresses and returning the ``gemv_status_t`` code;
+  ``gemv_splitk_*``, ``gemv_q8_*``, ``gemv_fp8_*``, ``gemv_kv_*``, ``gemv_plan``,
+  ``gemv_run_family``, ...), taking integer addresses and returning the
+  ``gemv_status_t`` code;
 * tensor helpers ``gemv``, ``gemv_batched``, ``gemv_multi``,
   ``gemv_gate_up_silu``, ``gemv_splitk`` and ``gemv_q8`` that check dtype, shape,
   strides and device, call the matching entry point on
-  ``torch.cuda.current_stream()`` and raise ``GemvError`` on a failure code.
+  ``torch.cuda.current_stream()`` and raise ``GemvError`` on a failure code;
+  ``gemv_fp8_quantise`` and ``gemv_fp8`` (e4m3 with a scale per block of 128)
+  and ``gemv_kv_append`` and ``gemv_kv_attend`` (a paged 8-bit key/value cache,
+  ``KVCache``) do so on the current stream of their tensors' device.
 
 Layout of the tensor helpers: ``A`` is (M, K) with unit column stride and row
 stride ``lda = A.stride(0) >= K`` (so a column slice of a wider matrix works);
@@ -139,6 +143,43 @@ gemv_plan_splitk = _bind("gemv_plan_splitk", [_i, _i, _i, _i, _i, _vp, _vp, ctyp
 gemv_run_family = _bind("gemv_run_family", [_i, _i, _vp, _i, _vp, _vp, _vp, _i, _i, _i, _st])
 gemv_test_refused_launch = _bind("gemv_test_refused_launch", [_st])
 
+FP8_BLOCK = 128
+KV_BLOCK = 16
+KV_INT8, KV_E4M3 = 0, 1
+
+
+class KvCacheStruct(ctypes.Structure):
+    """gemv_kv_cache_t."""
+    _fields_ = [(name, ctypes.c_int) for name in ("format", "pages", "heads", "page_size", "dim")] + [
+        (name, ctypes.c_void_p) for name in ("k", "v", "k_scale", "v_scale")]
+
+
+class KvBatchStruct(ctypes.Structure):
+    """gemv_kv_batch_t."""
+    _fields_ = [("sequences", ctypes.c_int), ("table", ctypes.c_void_p),
+                ("table_pitch", ctypes.c_int), ("table_width", ctypes.c_int),
+                ("seq_lens", ctypes.c_void_p), ("starts", ctypes.c_void_p)]
+
+
+_cache_p, _batch_p = ctypes.POINTER(KvCacheStruct), ctypes.POINTER(KvBatchStruct)
+_quantise_args = [_vp, _i, _vp, _i, _vp, _i, _i, _i, _i, _st]
+gemv_fp8_quantise_f32 = _bind("gemv_fp8_quantise_f32", _quantise_args)
+gemv_fp8_quantise_f16 = _bind("gemv_fp8_quantise_f16", _quantise_args)
+gemv_fp8_quantise_bf16 = _bind("gemv_fp8_quantise_bf16", _quantise_args)
+_fp8_args = [_vp, _i, _vp, _i, _vp, _i, _vp, _i, _vp, _vp, _i, _i, _i, _i, _st]
+gemv_fp8_f32 = _bind("gemv_fp8_f32", _fp8_args)
+gemv_fp8_f16 = _bind("gemv_fp8_f16", _fp8_args)
+gemv_fp8_bf16 = _bind("gemv_fp8_bf16", _fp8_args)
+_append_args = [_cache_p, _vp, _i, _vp, _i, _i, _batch_p, _st]
+gemv_kv_append_f32 = _bind("gemv_kv_append_f32", _append_args)
+gemv_kv_append_f16 = _bind("gemv_kv_append_f16", _append_args)
+gemv_kv_append_bf16 = _bind("gemv_kv_append_bf16", _append_args)
+gemv_kv_attend_workspace_size = _bind("gemv_kv_attend_workspace_size",
+                                      [_i, _i, _i, _i, _i, _i, _i, ctypes.POINTER(_sz)])
+_attend_args = [_cache_p, _vp, _i, _vp, _i, _i, _i, _batch_p, ctypes.c_float, _i, _i, _vp, _sz, _st]
+gemv_kv_attend_f16 = _bind("gemv_kv_attend_f16", _attend_args)
+gemv_kv_attend_bf16 = _bind("gemv_kv_attend_bf16", _attend_args)
+
 EXPORTED = ("gemv_status_string", "gemv_last_hip_error",
             "gemv_last_hip_error_string", "gemv_f32", "gemv_f16", "gemv_bf16",
             "gemv_batched_f16", "gemv_batched_bf16", "gemv_multi_f32",
@@ -148,7 +189,11 @@ EXPORTED = ("gemv_status_string", "gemv_last_hip_error",
             "gemv_splitk_bf16", "gemv_splitk_noalloc", "gemv_q8_f32", "gemv_q8_f16", "gemv_q8_bf16",
             "gemv_q8_run_family", "gemv_plan_q8", "gemv_read_probe",
             "gemv_read_probe_variant", "gemv_plan",
-            "gemv_plan_splitk", "gemv_run_family", "gemv_test_refused_launch")
+            "gemv_plan_splitk", "gemv_run_family", "gemv_test_refused_launch",
+            "gemv_fp8_quantise_f32", "gemv_fp8_quantise_f16", "gemv_fp8_quantise_bf16",
+            "gemv_fp8_f32", "gemv_fp8_f16", "gemv_fp8_bf16", "gemv_kv_append_f32",
+            "gemv_kv_append_f16", "gemv_kv_append_bf16", "gemv_kv_attend_workspace_size",
+            "gemv_kv_attend_f16", "gemv_kv_attend_bf16")
 
 
 class GemvError(RuntimeError):
@@ -436,3 +481,259 @@ def gemv_gate_up_silu(A_gate, A_up, x, out=None, *, stream=None):
     if rc != GEMV_SUCCESS:
         raise GemvError(rc, fn.__name__)
     return h
+
+
+# ---------------------------------------------------------------------------
+# e4m3 with a scale per block of 128
+# ---------------------------------------------------------------------------
+
+def _on_device_of(t, fn, *args, stream=None):
+    """fn(*args, stream handle) with t's device current, on the given stream
+    or the current one of that device; raises on a failure code."""
+    torch = _torch()
+    dev = t.device.index
+    s = torch.cuda.current_stream(dev) if stream is None else stream
+    if dev == torch.cuda.current_device():
+        rc = fn(*args, int(s.cuda_stream))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, int(s.cuda_stream))
+    if rc != GEMV_SUCCESS:
+        raise GemvError(rc, fn.__name__)
+
+
+def _check_rows(t, name, device=None):
+    """(rows, columns, row stride) of a device matrix with unit column stride."""
+    if t.dim() != 2 or not t.is_cuda:
+        raise ValueError(f"{name} must be a 2-D device tensor")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have unit column stride")
+    pitch = t.stride(0) if rows > 1 and cols > 0 else cols
+    if pitch < cols:
+        raise ValueError(f"{name}'s row stride is smaller than its rows")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on another device")
+    return rows, cols, pitch
+
+
+def _e4m3(t, name):
+    torch = _torch()
+    if t.dtype not in (torch.float8_e4m3fn, torch.uint8):
+        raise TypeError(f"{name} must be float8_e4m3fn (or its bytes as uint8)")
+
+
+def _check_scale(scale, name, shape, device):
+    torch = _torch()
+    rows, cols, pitch = _check_rows(scale, name, device)
+    if scale.dtype != torch.float32 or (rows, cols) != shape:
+        raise ValueError(f"{name} must be a float32 tensor of shape {shape}")
+    return pitch
+
+
+def gemv_fp8_quantise(X, block_rows: int = 1, out=None, scale=None, *, stream=None):
+    """(Q, scale): X (rows, K) in float32, float16 or bfloat16 (unit column
+    stride) held in e4m3 with a float32 scale for every ``block_rows`` rows (1
+    for activations, 128 for weights) and 128 columns.  Q is float8_e4m3fn
+    (rows, K), scale (ceil(rows / block_rows), ceil(K / 128))."""
+    torch = _torch()
+    if block_rows not in (1, FP8_BLOCK):
+        raise ValueError("block_rows must be 1 or 128")
+    rows, K, ldx = _check_rows(X, "X")
+    dt = _dtype_name(X)
+    shape = (-(-rows // block_rows), -(-K // FP8_BLOCK))
+    if out is None:
+        out = torch.empty((rows, K), dtype=torch.float8_e4m3fn, device=X.device)
+    if scale is None:
+        scale = torch.empty(shape, dtype=torch.float32, device=X.device)
+    _e4m3(out, "out")
+    if _check_rows(out, "out", X.device)[:2] != (rows, K):
+        raise ValueError("out must have X's shape")
+    lds = _check_scale(scale, "scale", shape, X.device)
+    fn = {"f32": gemv_fp8_quantise_f32, "f16": gemv_fp8_quantise_f16, "bf16": gemv_fp8_quantise_bf16}[dt]
+    _on_device_of(X, fn, X.data_ptr(), ldx, out.data_ptr(),
+                  _check_rows(out, "out")[2], scale.data_ptr(), lds, rows, K, block_rows, stream=stream)
+    return out, scale
+
+
+def gemv_fp8(W, w_scale, X, x_scale, bias=None, out=None, *, out_dtype=None, stream=None):
+    """Y (nvec, M) = X @ W.T (+ bias) for e4m3 W (M, K) with w_scale
+    (ceil(M / 128), ceil(K / 128)) and e4m3 X (nvec, K) with x_scale (nvec,
+    ceil(K / 128)), as ``gemv_fp8_quantise`` gives them; any nvec.  Y is float32,
+    or ``out_dtype`` / out's dtype (float16, bfloat16); out may be a column
+    slice of a wider matrix."""
+    torch = _torch()
+    _e4m3(W, "W")
+    _e4m3(X, "X")
+    M, K, ldw = _check_rows(W, "W")
+    nvec, Kx, ldx = _check_rows(X, "X", W.device)
+    if Kx != K:
+        raise ValueError("W and X must have the same number of columns")
+    blocks = -(-K // FP8_BLOCK)
+    ldws = _check_scale(w_scale, "w_scale", (-(-M // FP8_BLOCK), blocks), W.device)
+    ldxs = _check_scale(x_scale, "x_scale", (nvec, blocks), W.device)
+    bias = _check_bias(bias, M, W.device)
+    if out is None:
+        out = torch.empty((nvec, M), dtype=torch.float32 if out_dtype is None else out_dtype, device=W.device)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError("out is not of out_dtype")
+    dt = _dtype_name(out)
+    rows, cols, ldy = _check_rows(out, "out", W.device)
+    if (rows, cols) != (nvec, M):
+        raise ValueError(f"out must be of shape {(nvec, M)}")
+    fn = {"f32": gemv_fp8_f32, "f16": gemv_fp8_f16, "bf16": gemv_fp8_bf16}[dt]
+    _on_device_of(W, fn, W.data_ptr(), ldw, w_scale.data_ptr(), ldws, X.data_ptr(),
+                  ldx, x_scale.data_ptr(), ldxs, bias.data_ptr() if bias is not None else None,
+                  out.data_ptr(), ldy, M, K, nvec, stream=stream)
+    return out
+
+
+# ---------------------------------------------------------------------------
+# a paged key/value cache in 8 bits
+# ---------------------------------------------------------------------------
+
+class KVCache:
+    """A paged key/value cache in int8 or e4m3 with a float32 scale per block
+    of 16 tokens and head, over the caller's tensors:
+
+    k (pages, heads, page_size, dim), v (pages, heads, page_size // 16, dim,
+    16), both int8 or both float8_e4m3fn; k_scale and v_scale (pages, heads,
+    page_size // 16) float32; all contiguous on one device.  ``KVCache.empty``
+    allocates them."""
+
+    def __init__(self, k, v, k_scale, v_scale):
+        torch = _torch()
+        if k.dim() != 4 or v.dim() != 5:
+            raise ValueError("k must be (pages, heads, page_size, dim) and v (pages, heads, page_size // 16, dim, 16)")
+        pages, heads, page_size, dim = k.shape
+        if page_size not in (16, 32, 64, 128, 256) or dim not in (64, 128, 256):
+            raise ValueError("page_size must be 16, 32, 64, 128 or 256 and dim 64, 128 or 256")
+        blocks = page_size // KV_BLOCK
+        if tuple(v.shape) != (pages, heads, blocks, dim, KV_BLOCK):
+            raise ValueError(f"v must be of shape {(pages, heads, blocks, dim, KV_BLOCK)}")
+        formats = {torch.int8: KV_INT8, torch.float8_e4m3fn: KV_E4M3}
+        if k.dtype not in formats or v.dtype != k.dtype:
+            raise TypeError("k and v must both be int8 or both float8_e4m3fn")
+        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if t.dtype != torch.float32 or tuple(t.shape) != (pages, heads, blocks):
+                raise ValueError(f"{name} must be a float32 tensor of shape {(pages, heads, blocks)}")
+        for t in (k, v, k_scale, v_scale):
+            if not t.is_cuda or not t.is_contiguous() or t.device != k.device:
+                raise ValueError("the cache's tensors must be contiguous on one device")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.pages, self.heads, self.page_size, self.dim = pages, heads, page_size, dim
+        self._struct = KvCacheStruct(formats[k.dtype], pages, heads, page_size, dim, k.data_ptr(),
+                                     v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr())
+
+    @classmethod
+    def empty(cls, pages: int, heads: int, dim: int, *, page_size: int = 64, dtype=None, device="cuda"):
+        """A cache in newly allocated memory (contents undefined); dtype int8
+        (the default) or float8_e4m3fn."""
+        torch = _torch()
+        dtype = torch.int8 if dtype is None else dtype
+        blocks = page_size // KV_BLOCK
+        scale = (pages, heads, blocks)
+        return cls(torch.empty((pages, heads, page_size, dim), dtype=dtype, device=device),
+                   torch.empty((pages, heads, blocks, dim, KV_BLOCK), dtype=dtype, device=device),
+                   torch.empty(scale, dtype=torch.float32, device=device),
+                   torch.empty(scale, dtype=torch.float32, device=device))
+
+
+def _kv_batch(cache, table, seq_lens, starts, rows):
+    torch = _torch()
+    sequences = table.shape[0] if table.dim() == 2 else -1
+    if (table.dim() != 2 or table.dtype != torch.int32 or (table.shape[1] > 1 and table.stride(1) != 1)
+            or (sequences > 1 and table.stride(0) < table.shape[1])):
+        raise ValueError("table must be an int32 (sequences, pages) tensor with unit column stride")
+    if seq_lens.dtype != torch.int32 or tuple(seq_lens.shape) != (sequences,) or not seq_lens.is_contiguous():
+        raise ValueError("seq_lens must be a contiguous int32 (sequences,) tensor")
+    if starts is None:
+        if rows != sequences:
+            raise ValueError("without starts every sequence has one row")
+    elif starts.dtype != torch.int32 or tuple(starts.shape) != (sequences + 1,) or not starts.is_contiguous():
+        raise ValueError("starts must be a contiguous int32 (sequences + 1,) tensor")
+    for t in (table, seq_lens, starts):
+        if t is not None and t.device != cache.k.device:
+            raise ValueError("table, seq_lens and starts must be on the cache's device")
+    return KvBatchStruct(sequences, table.data_ptr(), table.stride(0) if sequences > 1 else table.shape[1],
+                         table.shape[1], seq_lens.data_ptr(), starts.data_ptr() if starts is not None else None)
+
+
+def _check_heads(t, name, cache):
+    """(rows, heads, row stride) of a (rows, heads, dim) tensor whose rows may
+    be columns of a wider matrix."""
+    if t.dim() != 3 or t.shape[2] != cache.dim or t.device != cache.k.device:
+        raise ValueError(f"{name} must be (rows, heads, {cache.dim}) on the cache's device")
+    rows, heads, dim = t.shape
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
+        raise ValueError(f"{name}'s heads must lie one behind the other in a row")
+    pitch = t.stride(0) if rows > 1 else heads * dim
+    if pitch < heads * dim:
+        raise ValueError(f"{name}'s row stride is smaller than its rows")
+    return rows, heads, pitch
+
+
+def gemv_kv_append(cache, K, V, table, seq_lens, starts=None, *, stream=None):
+    """Write the new tokens' keys and values, K and V (rows, heads, dim) in
+    float32, float16 or bfloat16, into the cache.
+
+    table (sequences, pages) int32 names each sequence's pages, seq_lens
+    (sequences,) int32 its length with the new tokens; its new tokens are the
+    last ones, in rows starts[b] .. starts[b + 1] - 1 (starts (sequences + 1,)
+    int32; None: one row for each sequence).  Rows behind the last start are
+    ignored."""
+    rows, heads, ldk = _check_heads(K, "K", cache)
+    vrows, vheads, ldv = _check_heads(V, "V", cache)
+    if heads != cache.heads or (vrows, vheads) != (rows, heads) or V.dtype != K.dtype:
+        raise ValueError("K and V must have the cache's heads, the same rows and the same dtype")
+    dt = _dtype_name(K)
+    batch = _kv_batch(cache, table, seq_lens, starts, rows)
+    fn = {"f32": gemv_kv_append_f32, "f16": gemv_kv_append_f16, "bf16": gemv_kv_append_bf16}[dt]
+    _on_device_of(K, fn, ctypes.byref(cache._struct), K.data_ptr(), ldk,
+                  V.data_ptr(), ldv, rows, ctypes.byref(batch), stream=stream)
+
+
+def kv_attend_workspace_size(cache, q_heads: int, rows: int, sequences: int, table_width: int) -> int:
+    """Workspace bytes that ``gemv_kv_attend`` needs (0: none)."""
+    n = ctypes.c_size_t(0)
+    rc = gemv_kv_attend_workspace_size(q_heads, cache.heads, cache.dim, rows, sequences, table_width,
+                                       cache.page_size, ctypes.byref(n))
+    if rc != GEMV_SUCCESS:
+        raise GemvError(rc, "gemv_kv_attend_workspace_size")
+    return n.value
+
+
+def gemv_kv_attend(Q, cache, table, seq_lens, starts=None, *, scale=None, window: int = 0, sinks: int = 0,
+                   out=None, workspace=None, stream=None):
+    """Causal attention of the batch's new tokens, Q (rows, q_heads, dim) in
+    float16 or bfloat16, over the cache, which holds their own keys and values
+    already; returns (rows, q_heads, dim) of Q's dtype.
+
+    table, seq_lens and starts as for ``gemv_kv_append``.  scale: 1 / sqrt(dim)
+    by default.  window > 0: a token sees the last ``window`` tokens (itself
+    among them) and the first ``sinks``.  Rows of out behind the last start are
+    left as they were.  workspace: a device tensor of at least
+    ``kv_attend_workspace_size(...)`` bytes, allocated here through torch when
+    not given."""
+    torch = _torch()
+    if Q.dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError("Q must be float16 or bfloat16")
+    rows, q_heads, ldq = _check_heads(Q, "Q", cache)
+    if out is None:
+        out = torch.empty((rows, q_heads, cache.dim), dtype=Q.dtype, device=Q.device)
+    if out.dtype != Q.dtype or tuple(out.shape) != tuple(Q.shape):
+        raise ValueError("out must have Q's shape and dtype")
+    _, _, ldo = _check_heads(out, "out", cache)
+    batch = _kv_batch(cache, table, seq_lens, starts, rows)
+    need = kv_attend_workspace_size(cache, q_heads, rows, batch.sequences, batch.table_width)
+    if workspace is None and need:
+        workspace = torch.empty(need // 4, dtype=torch.float32, device=Q.device)
+    if workspace is not None and (workspace.device != Q.device or not workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous tensor on Q's device")
+    fn = gemv_kv_attend_f16 if Q.dtype == torch.float16 else gemv_kv_attend_bf16
+    _on_device_of(Q, fn, ctypes.byref(cache._struct), Q.data_ptr(), ldq,
+                  out.data_ptr(), ldo, q_heads, rows, ctypes.byref(batch),
+                  cache.dim ** -0.5 if scale is None else scale, window, sinks,
+                  workspace.data_ptr() if workspace is not None else None,
+                  workspace.numel() * workspace.element_size() if workspace is not None else 0, stream=stream)
+    return out

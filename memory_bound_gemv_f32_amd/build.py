@@ -12,14 +12,17 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
 from pathlib import Path
 
 PACKAGE = Path(__file__).resolve().parent
 ROOT = PACKAGE.parent
 CSRC = PACKAGE / "csrc"
-SOURCES = [CSRC / "gemv_api.hip"]
+SOURCES = [CSRC / "gemv_api.hip", CSRC / "fp8_api.hip", CSRC / "kv_api.hip"]
 HEADERS = [CSRC / "gemv_plan.hpp", CSRC / "gemv_device.hpp",
-           CSRC / "gemv_kernels.hpp", ROOT / "include" / "gemv.h"]
+           CSRC / "gemv_kernels.hpp", CSRC / "gemv_launch.hpp",
+           CSRC / "fp8_device.hpp", CSRC / "fp8_kernels.hpp",
+           CSRC / "kv_kernels.hpp", ROOT / "include" / "gemv.h"]
 LIBRARY = PACKAGE / "libgemv.so"
 ARCH = "gfx950"
 
@@ -28,7 +31,6 @@ HIPCC_FLAGS = [
     "-O3",
     "-std=c++17",
     "-fPIC",
-    "-shared",
     "-Wall",
     # no packed fp32 instructions anywhere in the device code
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
@@ -48,17 +50,33 @@ def build(verbose: bool = False, extra_flags: list[str] | None = None,
           output: Path = LIBRARY) -> Path:
     """Compile every HIP source into ``libgemv.so`` (always recompiles)."""
     tmp = output.with_name(f"{output.name}.tmp{os.getpid()}")
-    cmd = [hipcc(), *HIPCC_FLAGS, *(extra_flags or []),
-           *[str(s) for s in SOURCES], "-o", str(tmp)]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    proc = subprocess.run(cmd, capture_output=True, text=True)
+    flags = [*HIPCC_FLAGS, *(extra_flags or [])]
+    with tempfile.TemporaryDirectory(prefix="libgemv_") as folder:
+        # the sources side by side, then one link
+        objects = [Path(folder) / f"{s.stem}.o" for s in SOURCES]
+        cmds = [[hipcc(), *flags, "-c", str(s), "-o", str(o)]
+                for s, o in zip(SOURCES, objects)]
+        running = []
+        for cmd in cmds:
+            if verbose:
+                print(" ".join(cmd), flush=True)
+            running.append(subprocess.Popen(cmd, stdout=subprocess.PIPE,
+                                            stderr=subprocess.STDOUT, text=True))
+        texts = [p.communicate()[0] for p in running]
+        failed = any(p.returncode != 0 for p in running)
+        if not failed:
+            cmd = [hipcc(), *flags, "-shared", *[str(o) for o in objects], "-o", str(tmp)]
+            if verbose:
+                print(" ".join(cmd), flush=True)
+            link = subprocess.run(cmd, capture_output=True, text=True)
+            texts.append(link.stdout + link.stderr)
+            failed = link.returncode != 0
     # hipcc's host pass does not know the packed-fp32 feature; that warning
     # is expected, anything else is shown
     noise = "is not a recognized feature for this target"
-    msgs = [ln for ln in (proc.stdout + proc.stderr).splitlines()
+    msgs = [ln for text in texts for ln in text.splitlines()
             if noise not in ln and "(ignoring feature)" not in ln and ln.strip()]
-    if proc.returncode != 0:
+    if failed:
         raise RuntimeError("hipcc failed:\n" + "\n".join(msgs))
     if verbose and msgs:
         print("\n".join(msgs), file=sys.stderr)

@@ -11,6 +11,7 @@
 
 #include "../../include/gemv.h"
 #include "gemv_kernels.hpp"
+#include "gemv_launch.hpp"
 #include "gemv_plan.hpp"
 
 namespace {
@@ -37,7 +38,9 @@ hipError_t launch(const void* fn, const Plan& p, hipStream_t stream, void** argv
     return hipLaunchKernel(fn, dim3((unsigned)p.grid), dim3((unsigned)p.block), argv, 0, stream);
 }
 
-gemv_status_t finish(hipError_t err) {
+}  // namespace
+
+gemv_status_t gemvapi::finish(hipError_t err) {
     if (err != hipSuccess) {
         g_last_launch_error = err;
         // the runtime also keeps the error as the thread's "last error";
@@ -48,6 +51,10 @@ gemv_status_t finish(hipError_t err) {
     }
     return GEMV_SUCCESS;
 }
+
+namespace {
+
+using gemvapi::finish;
 
 // ---- rows-per-wave / wave-per-row / workgroup-per-row ----------------------
 

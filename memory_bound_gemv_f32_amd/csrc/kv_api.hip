@@ -1,0 +1,216 @@
+// libgemv C ABI, the paged 8-bit key/value cache: argument checks, mapping
+// selection and launch.
+#include <hip/hip_runtime.h>
+
+#include "../../include/gemv.h"
+#include "gemv_launch.hpp"
+#include "kv_kernels.hpp"
+
+namespace {
+
+using gemvapi::finish;
+using kvdev::Attend;
+using kvdev::E4m3;
+using kvdev::Int8;
+using kvdev::TBF16;
+using kvdev::TF16;
+using kvdev::TF32;
+
+static_assert(GEMV_KV_BLOCK == kvdev::kBlock, "the header states the block");
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+bool aligned(const void* p, int n) { return (uintptr_t)p % n == 0; }
+
+gemv_status_t launch(const void* fn, dim3 grid, int threads, void** argv, hipStream_t stream) {
+    return finish(hipLaunchKernel(fn, grid, dim3((unsigned)threads), argv, 0, stream));
+}
+
+// The head dims and page sizes that there are kernels for.
+bool known_dim(int dim) { return dim == 64 || dim == 128 || dim == 256; }
+
+bool make_cache(const gemv_kv_cache_t* in, kvdev::Cache* out) {
+    if (in == nullptr || (in->format != GEMV_KV_INT8 && in->format != GEMV_KV_E4M3) ||
+        in->pages < 1 || in->heads < 1 || in->heads > 65535 || !known_dim(in->dim))
+        return false;
+    int log2 = 0;
+    while (log2 < 4 && (GEMV_KV_BLOCK << log2) != in->page_size) ++log2;
+    if ((GEMV_KV_BLOCK << log2) != in->page_size) return false;
+    if (in->k == nullptr || in->v == nullptr || in->k_scale == nullptr || in->v_scale == nullptr ||
+        !aligned(in->k, 16) || !aligned(in->v, 16) || !aligned(in->k_scale, 4) || !aligned(in->v_scale, 4))
+        return false;
+    *out = kvdev::Cache{static_cast<uint8_t*>(in->k), static_cast<uint8_t*>(in->v), in->k_scale,
+                        in->v_scale, in->heads, in->pages, log2};
+    return true;
+}
+
+bool make_batch(const gemv_kv_batch_t* in, int rows, kvdev::Batch* out) {
+    if (in == nullptr || in->sequences < 0 || in->table_width < 0 || in->table_pitch < in->table_width ||
+        rows < 0 || (in->starts == nullptr && rows != in->sequences))
+        return false;
+    if (in->sequences > 0 && rows > 0 &&
+        (in->seq_lens == nullptr || (in->table == nullptr && in->table_width > 0) ||
+         !aligned(in->table, 4) || !aligned(in->seq_lens, 4) || !aligned(in->starts, 4)))
+        return false;
+    *out = kvdev::Batch{in->table, in->table_pitch, in->table_width, in->seq_lens, in->starts,
+                        in->sequences, rows};
+    return true;
+}
+
+template <class D, class F>
+gemv_status_t append(int dim, const kvdev::Cache& c, const kvdev::Batch& q, const void* K, int64_t ldk,
+                     const void* V, int64_t ldv, hipStream_t stream) {
+    const int64_t places = q.total / GEMV_KV_BLOCK + 2 * (int64_t)q.count;
+    if (places > 0x7fffffff) return GEMV_ERROR_INVALID_VALUE;
+    void* argv[] = {(void*)&c, (void*)&q, (void*)&K, (void*)&ldk, (void*)&V, (void*)&ldv};
+    const void* fn = dim == 64    ? (const void*)&kvdev::kv_append_kernel<D, F, 64>
+                     : dim == 128 ? (const void*)&kvdev::kv_append_kernel<D, F, 128>
+                                  : (const void*)&kvdev::kv_append_kernel<D, F, 256>;
+    return launch(fn, dim3((unsigned)places, (unsigned)c.heads, 2), 64, argv, stream);
+}
+
+// How an attention call is mapped: the rows of a workgroup, whether its
+// wavefronts share them, and how many workgroups share a row tile's tokens.
+struct Mapping {
+    int row_tiles;     // 16-row tiles of a wavefront
+    int waves_share;   // 4: the wavefronts take the chunks of the same rows in turn; 1: own rows each
+    int group_rows;    // rows of a workgroup
+    int splits;
+    int64_t places;
+};
+
+constexpr int64_t kWorkgroups = 1024;  // enough to keep 256 compute units reading
+
+Mapping map_attend(int q_heads, int heads, int rows, int sequences, int64_t capacity) {
+    Mapping m;
+    const int group = q_heads / heads;
+    const int64_t per_sequence = sequences > 0 ? ceil_div((int64_t)rows * group, sequences) : 0;
+    m.waves_share = per_sequence <= 16 ? 4 : 1;
+    m.row_tiles = 1;
+    m.group_rows = 16 * m.row_tiles * (m.waves_share == 1 ? kvdev::kAttWaves : 1);
+    m.places = (int64_t)rows * group / m.group_rows + sequences;
+    const int64_t chunks = ceil_div(capacity, kvdev::kChunk * m.waves_share);
+    int64_t splits = m.places > 0 ? ceil_div(kWorkgroups, m.places * heads) : 1;
+    if (splits > chunks) splits = chunks;
+    m.splits = (int)(splits < 1 ? 1 : splits);
+    return m;
+}
+
+size_t workspace_of(const Mapping& m, int heads, int dim) {
+    if (m.splits == 1) return 0;
+    return (size_t)m.places * heads * m.splits * m.group_rows * (dim + 2) * sizeof(float);
+}
+
+int64_t capacity_of(int64_t table_width, int page_size) {
+    const int64_t n = table_width * page_size;
+    return n < 0x7fffffff ? n : 0x7fffffff;
+}
+
+template <class T, class F, int DIM>
+gemv_status_t attend(const Mapping& m, Attend& p, hipStream_t stream) {
+    int64_t places = m.places;
+    const int64_t grid = places * p.cache.heads * p.splits;
+    if (grid > 0x7fffffff) return GEMV_ERROR_INVALID_VALUE;
+    void* argv[] = {&p, &places};
+    const void* fn = m.waves_share == 4 ? (const void*)&kvdev::kv_attend_kernel<T, F, DIM, 1, 4>
+                                        : (const void*)&kvdev::kv_attend_kernel<T, F, DIM, 1, 1>;
+    const gemv_status_t st = launch(fn, dim3((unsigned)grid), kvdev::kAttWaves * 64, argv, stream);
+    if (st != GEMV_SUCCESS || p.splits == 1) return st;
+    const void* join = m.group_rows == 16 ? (const void*)&kvdev::kv_join_kernel<T, DIM, 16>
+                                          : (const void*)&kvdev::kv_join_kernel<T, DIM, 64>;
+    return launch(join, dim3((unsigned)(places * p.cache.heads), (unsigned)(m.group_rows / 16)),
+                  kvdev::kAttWaves * 64, argv, stream);
+}
+
+template <class T, class F>
+gemv_status_t attend_dim(int dim, const Mapping& m, Attend& p, hipStream_t stream) {
+    switch (dim) {
+    case 64: return attend<T, F, 64>(m, p, stream);
+    case 128: return attend<T, F, 128>(m, p, stream);
+    default: return attend<T, F, 256>(m, p, stream);
+    }
+}
+
+template <class D>
+gemv_status_t append(const gemv_kv_cache_t* cache, const void* K, int ldk, const void* V, int ldv,
+                     int rows, const gemv_kv_batch_t* batch, hipStream_t stream) {
+    kvdev::Cache c;
+    kvdev::Batch q;
+    if (!make_cache(cache, &c) || !make_batch(batch, rows, &q) ||
+        (int64_t)ldk < (int64_t)c.heads * cache->dim || (int64_t)ldv < (int64_t)c.heads * cache->dim)
+        return GEMV_ERROR_INVALID_VALUE;
+    if (rows == 0 || q.count == 0) return GEMV_SUCCESS;
+    if (K == nullptr || V == nullptr || !aligned(K, D::bytes) || !aligned(V, D::bytes))
+        return GEMV_ERROR_INVALID_VALUE;
+    return cache->format == GEMV_KV_E4M3 ? append<D, E4m3>(cache->dim, c, q, K, ldk, V, ldv, stream)
+                                         : append<D, Int8>(cache->dim, c, q, K, ldk, V, ldv, stream);
+}
+
+template <class T>
+gemv_status_t attend(const gemv_kv_cache_t* cache, const uint16_t* Q, int ldq, uint16_t* O, int ldo,
+                     int q_heads, int rows, const gemv_kv_batch_t* batch, float scale, int window,
+                     int sinks, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    Attend p;
+    if (!make_cache(cache, &p.cache) ||
+        !make_batch(batch, rows, &p.batch) || q_heads < 1 || q_heads % p.cache.heads != 0 ||
+        (int64_t)ldq < (int64_t)q_heads * cache->dim || (int64_t)ldo < (int64_t)q_heads * cache->dim ||
+        (int64_t)rows * q_heads > 0x7fffffff || window < 0 || sinks < 0 || !(scale - scale == 0.0f))
+        return GEMV_ERROR_INVALID_VALUE;
+    if (rows == 0 || p.batch.count == 0) return GEMV_SUCCESS;
+    if (Q == nullptr || O == nullptr || !aligned(Q, 2) || !aligned(O, 2)) return GEMV_ERROR_INVALID_VALUE;
+    const int64_t capacity = capacity_of(batch->table_width, cache->page_size);
+    const Mapping m = map_attend(q_heads, p.cache.heads, rows, p.batch.count, capacity);
+    const size_t need = workspace_of(m, p.cache.heads, cache->dim);
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 16)))
+        return GEMV_ERROR_INVALID_VALUE;
+    p.Q = Q;
+    p.ldq = ldq;
+    p.O = O;
+    p.ldo = ldo;
+    p.group = q_heads / p.cache.heads;
+    p.scale = scale * 1.44269504088896341f;
+    p.window = window;
+    p.sinks = sinks;
+    p.capacity = (int)capacity;
+    p.splits = m.splits;
+    p.partial = static_cast<float*>(workspace);
+    return cache->format == GEMV_KV_E4M3 ? attend_dim<T, E4m3>(cache->dim, m, p, stream)
+                                         : attend_dim<T, Int8>(cache->dim, m, p, stream);
+}
+
+}  // namespace
+
+extern "C" gemv_status_t gemv_kv_attend_workspace_size(int q_heads, int heads, int dim, int rows,
+                                                       int sequences, int table_width, int page_size,
+                                                       size_t* bytes) {
+    if (bytes == nullptr || heads < 1 || q_heads < 1 || q_heads % heads != 0 || !known_dim(dim) ||
+        rows < 0 || sequences < 0 || table_width < 0 || page_size < GEMV_KV_BLOCK)
+        return GEMV_ERROR_INVALID_VALUE;
+    *bytes = rows == 0 || sequences == 0
+                 ? 0
+                 : workspace_of(map_attend(q_heads, heads, rows, sequences, capacity_of(table_width, page_size)),
+                                heads, dim);
+    return GEMV_SUCCESS;
+}
+
+#define GEMV_KV_APPEND(NAME, D, T)                                                             \
+    extern "C" gemv_status_t gemv_kv_append_##NAME(const gemv_kv_cache_t* cache, const T* K,     \
+                                                   int ldk, const T* V, int ldv, int rows,       \
+                                                   const gemv_kv_batch_t* batch,                 \
+                                                   hipStream_t stream) {                         \
+        return append<D>(cache, K, ldk, V, ldv, rows, batch, stream);                            \
+    }
+GEMV_KV_APPEND(f32, TF32, float)
+GEMV_KV_APPEND(f16, TF16, uint16_t)
+GEMV_KV_APPEND(bf16, TBF16, uint16_t)
+
+#define GEMV_KV_ATTEND(NAME, T)                                                                  \
+    extern "C" gemv_status_t gemv_kv_attend_##NAME(                                              \
+        const gemv_kv_cache_t* cache, const uint16_t* Q, int ldq, uint16_t* O, int ldo,          \
+        int q_heads, int rows, const gemv_kv_batch_t* batch, float scale, int window, int sinks, \
+        void* workspace, size_t workspace_bytes, hipStream_t stream) {                           \
+        return attend<T>(cache, Q, ldq, O, ldo, q_heads, rows, batch, scale, window, sinks,      \
+                         workspace, workspace_bytes, stream);                                    \
+    }
+GEMV_KV_ATTEND(f16, TF16)
+GEMV_KV_ATTEND(bf16, TBF16)

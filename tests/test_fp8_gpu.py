@@ -1,0 +1,253 @@
+"""The e4m3 quantiser and product with a scale per block of 128, against
+references in 64 bits (needs a GPU)."""
+
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import memory_bound_gemv_f32_amd as lg
+from fp8_helpers import assert_close, decode, product, product_bound, quantise
+
+pytestmark = pytest.mark.gpu
+
+TYPES = [torch.float32, torch.float16, torch.bfloat16]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def rand(seed, *shape, scale=1.0, dtype=torch.float32):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(*shape, generator=g) * scale).to(dtype).cuda()
+
+
+def operand(seed, rows, K, block_rows):
+    """Random e4m3 bytes without NaN (the whole range, subnormals and both
+    zeros among them) with scales over a few powers of two."""
+    g = torch.Generator().manual_seed(seed)
+    q = torch.randint(0, 256, (rows, K), generator=g, dtype=torch.uint8)
+    q[(q & 127) == 127] = 0x80
+    s = torch.rand(-(-rows // block_rows), -(-K // 128), generator=g) * 2.0 ** torch.randint(-9, -6, (1,), generator=g)
+    return q.view(torch.float8_e4m3fn).cuda(), s.cuda()
+
+
+# ---------------------------------------------------------------------------
+# quantiser
+# ---------------------------------------------------------------------------
+
+QSHAPES = [(1, 1), (1, 128), (3, 129), (5, 127), (2, 511), (7, 512), (4, 513), (130, 1000), (129, 4096),
+           (300, 260), (1, 16411), (257, 64)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("block_rows", [1, 128])
+@pytest.mark.parametrize("rows,K", QSHAPES)
+def test_quantise_is_the_formula(rows, K, block_rows, dtype):
+    x = rand(rows * 31 + K, rows, K, scale=3.0, dtype=dtype)
+    x[:, ::37] *= 50
+    q, s = lg.gemv_fp8_quantise(x, block_rows)
+    want, scale = quantise(x, block_rows)
+    assert np.array_equal(s.cpu().numpy(), scale)
+    assert np.array_equal(decode(q), want)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_quantise_strides_and_guards(dtype, block_rows):
+    rows, K = 133, 300
+    wide = rand(5, rows + 2, K + 41, dtype=dtype)
+    x = wide[1:1 + rows, 7:7 + K]
+    qbuf = torch.full((rows + 2, K + 5), 0x55, dtype=torch.uint8, device="cuda")
+    nb = -(-rows // block_rows)
+    sbuf = torch.full((nb + 2, 6), -3.0, device="cuda")
+    lg.gemv_fp8_quantise(x, block_rows, out=qbuf[1:-1, 3:3 + K], scale=sbuf[1:-1, 1:4])
+    want, scale = quantise(x, block_rows)
+    qh, sh = qbuf.cpu(), sbuf.cpu()
+    assert np.array_equal(decode(qh[1:-1, 3:3 + K].contiguous().view(torch.float8_e4m3fn)), want)
+    assert np.array_equal(sh[1:-1, 1:4].numpy(), scale)
+    qh[1:-1, 3:3 + K] = 0x55
+    sh[1:-1, 1:4] = -3.0
+    assert (qh == 0x55).all() and (sh == -3.0).all()
+
+
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_quantise_edges(block_rows):
+    # zeros, the smallest and the largest magnitudes, and values on every tie
+    ties = torch.tensor([(decode(torch.tensor([b], dtype=torch.uint8).view(torch.float8_e4m3fn))[0]
+                          + decode(torch.tensor([b + 1], dtype=torch.uint8).view(torch.float8_e4m3fn))[0]) / 2
+                         for b in range(126)])
+    x = torch.zeros(128, 8 * 128)
+    x[:, 128:256] = 2.0 ** -149
+    x[:, 256:384] = 3.4028234e38
+    x[:, 384:510] = ties
+    x[:, 511] = 448.0
+    x[::2, 512:640] = -1e-30
+    q, s = lg.gemv_fp8_quantise(x.cuda(), block_rows)
+    want, scale = quantise(x, block_rows)
+    assert np.array_equal(s.cpu().numpy(), scale) and np.array_equal(decode(q), want)
+    # an infinity or a NaN is its block's alone
+    for bad in (float("inf"), float("-inf"), float("nan")):
+        y = torch.ones(128, 300)
+        y[5, 140] = bad
+        q, s = lg.gemv_fp8_quantise(y.cuda(), block_rows)
+        full = decode(q) * s.cpu().double().numpy().repeat(block_rows, 0).repeat(128, 1)[:, :300]
+        hit = np.zeros((128, 300), dtype=bool)
+        hit[5 if block_rows == 1 else slice(None), 128:256] = True
+        assert np.isnan(full[hit]).all() and np.allclose(full[~hit], 1.0, rtol=2 ** -20)
+
+
+def test_quantise_nothing():
+    for shape in ((0, 64), (5, 0)):
+        q, s = lg.gemv_fp8_quantise(torch.empty(shape, device="cuda"))
+        assert q.shape == shape and s.shape == (shape[0], -(-shape[1] // 128))
+
+
+# ---------------------------------------------------------------------------
+# product
+# ---------------------------------------------------------------------------
+
+PSHAPES = [(1, 1, 1), (1, 16, 128), (2, 17, 127), (3, 100, 129), (16, 64, 256), (17, 130, 1000), (33, 65, 300),
+           (5, 300, 16), (64, 128, 512), (65, 129, 513), (100, 257, 384), (128, 256, 1024), (129, 300, 640),
+           (200, 520, 272), (300, 384, 260), (1, 4096, 4096), (16, 1000, 4111), (513, 640, 1100)]
+
+
+@pytest.mark.parametrize("out", TYPES)
+@pytest.mark.parametrize("tokens,M,K", PSHAPES)
+def test_product(tokens, M, K, out):
+    W, ws = operand(M + K, M, K, 128)
+    X, xs = operand(tokens + 7 * K, tokens, K, 1)
+    bias = rand(M, M, scale=5.0) if (tokens + M) % 2 else None
+    y = lg.gemv_fp8(W, ws, X, xs, bias, out_dtype=out)
+    assert y.dtype == out
+    want, size = product(W, ws, X, xs, bias)
+    if out == torch.float16:
+        assert np.abs(want).max() < 60000
+    assert_close(y, want, product_bound(size, want, K, out), f"{tokens}x{M}x{K}")
+
+
+@pytest.mark.parametrize("tokens", [1, 20, 150, 400])
+def test_product_exact_integers(tokens):
+    """Small whole numbers and scales of one: every sum is exact."""
+    M, K = 270, 777
+    g = torch.Generator().manual_seed(tokens)
+    W = torch.randint(-4, 5, (M, K), generator=g).float().to(torch.float8_e4m3fn).cuda()
+    X = torch.randint(-4, 5, (tokens, K), generator=g).float().to(torch.float8_e4m3fn).cuda()
+    y = lg.gemv_fp8(W, torch.ones(3, 7, device="cuda"), X, torch.ones(tokens, 7, device="cuda"))
+    assert np.array_equal(y.cpu().double().numpy(), decode(X) @ decode(W).T)
+
+
+@pytest.mark.parametrize("tokens,M,K", [(1, 40, 300), (9, 150, 512), (70, 200, 400), (300, 300, 260), (260, 256, 512)])
+def test_product_layouts(tokens, M, K):
+    """Any pitch and byte alignment; nothing outside Y is written."""
+    for ow, ox, oy in ((0, 0, 0), (1, 0, 1), (0, 3, 0), (16, 16, 4), (5, 9, 3)):
+        W, ws = operand(1, M + 1, K + 33, 128)
+        X, xs = operand(2, tokens + 1, K + 18, 1)
+        W, X = W[:M, ow:ow + K], X[1:, ox:ox + K]
+        ws = torch.nn.functional.pad(ws, (1, 2))[:-(-M // 128), 1:1 + -(-K // 128)]
+        xs = xs[1:, :-(-K // 128)]
+        buf = torch.full((tokens + 2, M + 9), 777.0, device="cuda")
+        lg.gemv_fp8(W, ws, X, xs, out=buf[1:-1, oy:oy + M])
+        want, size = product(W, ws, X, xs)
+        assert_close(buf[1:-1, oy:oy + M], want, product_bound(size, want, K, torch.float32))
+        rest = buf.cpu()
+        rest[1:-1, oy:oy + M] = 777.0
+        assert (rest == 777.0).all()
+
+
+def test_product_nan_stays_in_its_row():
+    for tokens in (3, 300):
+        W, ws = operand(3, 300, 512, 128)
+        X, xs = operand(4, tokens, 512, 1)
+        W.view(torch.uint8)[137, 200] = 0x7F
+        X.view(torch.uint8)[1, 300] = 0xFF
+        xs[2, 1] = float("nan")
+        ws[2, 3] = float("nan")
+        y = torch.isnan(lg.gemv_fp8(W, ws, X, xs)).cpu().numpy()
+        want = np.zeros_like(y)
+        want[:, 137] = want[1] = want[2] = want[:, 256:] = True
+        assert np.array_equal(y, want)
+
+
+def test_product_empty():
+    one = torch.ones
+    W, ws = operand(1, 30, 0, 128)
+    X, xs = operand(1, 4, 0, 1)
+    b = one(30, device="cuda") * 2.5
+    assert (lg.gemv_fp8(W, ws, X, xs, b) == 2.5).all() and (lg.gemv_fp8(W, ws, X, xs) == 0).all()
+    W, ws = operand(1, 30, 256, 128)
+    X, xs = operand(1, 0, 256, 1)
+    assert lg.gemv_fp8(W, ws, X, xs).shape == (0, 30)
+    W, ws = operand(1, 0, 256, 128)
+    X, xs = operand(1, 4, 256, 1)
+    assert lg.gemv_fp8(W, ws, X, xs).shape == (4, 0)
+
+
+def test_product_token_independence_and_repeats():
+    """The same bits on every call, and for a token whatever the others hold."""
+    W, ws = operand(8, 520, 1100, 128)
+    for tokens in (7, 300):
+        X, xs = operand(9, tokens, 1100, 1)
+        y = lg.gemv_fp8(W, ws, X, xs)
+        assert torch.equal(y, lg.gemv_fp8(W, ws, X, xs))
+        X2, xs2 = operand(10, tokens, 1100, 1)
+        X2.view(torch.uint8)[3], xs2[3] = X.view(torch.uint8)[3], xs[3]
+        assert torch.equal(lg.gemv_fp8(W, ws, X2, xs2)[3], y[3])
+
+
+def test_product_large_offsets():
+    """A weight matrix of more than 2^31 bytes: its last rows are right."""
+    M, K = (1 << 19) + 70, 4096 + 16
+    W = torch.zeros(M, K, dtype=torch.uint8, device="cuda")
+    W[-200:] = torch.randint(0, 120, (200, K), dtype=torch.uint8, device="cuda")
+    ws = torch.full((-(-M // 128), -(-K // 128)), 0.01, device="cuda")
+    for tokens in (2, 200):
+        X, xs = operand(5, tokens, K, 1)
+        y = lg.gemv_fp8(W, ws, X, xs, out_dtype=torch.bfloat16)
+        tail = W[-200:].view(torch.float8_e4m3fn)
+        want, size = product(tail, ws[:2], X, xs)
+        assert_close(y[:, -200:], want, product_bound(size, want, K, torch.bfloat16))
+        assert (y[:, :-200] == 0).all()
+        del y
+
+
+def test_quantised_product_against_float():
+    """Quantise, multiply: within the two roundings of the values' product."""
+    x, w = rand(1, 20, 1000), rand(2, 300, 1000, scale=0.02)
+    y = lg.gemv_fp8(*lg.gemv_fp8_quantise(w, 128), *lg.gemv_fp8_quantise(x))
+    xd, wd = x.cpu().double(), w.cpu().double()
+    # each value is off by at most 2^-4 of itself, or half the smallest step (2^-10) of its block's scale
+    xa = xd.abs() * 2.0 ** -4 + 2.0 ** -10 * xd.abs().max() / 448
+    wa = wd.abs() * 2.0 ** -4 + 2.0 ** -10 * wd.abs().max() / 448
+    bound = xa @ wd.abs().T + xd.abs() @ wa.T + xa @ wa.T
+    assert ((y.cpu().double() - xd @ wd.T).abs() <= bound * 1.001).all()
+
+
+def test_refusals():
+    W, ws = operand(1, 130, 300, 128)
+    X, xs = operand(2, 5, 300, 1)
+    with pytest.raises(TypeError):
+        lg.gemv_fp8(W.float(), ws, X, xs)
+    for args in ((W, ws[:1], X, xs), (W, ws, X, xs[:, :2]), (W, ws, X[:, :200], xs), (W, ws, X, xs.double()),
+                 (W, ws, X.cpu(), xs), (W.t(), ws, X, xs)):
+        with pytest.raises(ValueError):
+            lg.gemv_fp8(*args)
+    with pytest.raises(ValueError):
+        lg.gemv_fp8(W, ws, X, xs, torch.ones(129, device="cuda"))
+    with pytest.raises(ValueError):
+        lg.gemv_fp8(W, ws, X, xs, out=torch.empty(5, 129, device="cuda"))
+    with pytest.raises(TypeError):
+        lg.gemv_fp8(W, ws, X, xs, out_dtype=torch.float64)
+    x = rand(1, 4, 300)
+    with pytest.raises(ValueError):
+        lg.gemv_fp8_quantise(x, 64)
+    with pytest.raises(TypeError):
+        lg.gemv_fp8_quantise(x.double())
+    with pytest.raises(ValueError):
+        lg.gemv_fp8_quantise(x, out=torch.empty(4, 299, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError):
+        lg.gemv_fp8_quantise(x, scale=torch.empty(4, 2, device="cuda"))
