@@ -132,14 +132,22 @@ __global__ __launch_bounds__(kTileWaves * 64) void fp8_quantise_tile_kernel(
 // ---------------------------------------------------------------------------
 // product   Y[t,m] = Σ_b sx[t,b]·sw[m/128,b]·Σ_{k in block b} W[m,k]·X[t,k] + bias[m]
 //
-// The 128 products of a block are taken by 16×16×32 fp16 matrix-core steps on
-// exactly widened values: A is 16 rows of W, B 16 tokens of X.  Measured, a
-// block's sum is then within 4e-8 of Σ|products|; the e4m3 steps (16×16×32
-// and 16×16×128 alike) align their products to fewer bits and reach 2e-5.
-// The order of the products is free as long as A and B agree, so lane l takes
-// row (or token) l % 16 and the bytes 16·(l/16) .. +15 and 64 + 16·(l/16) ..
-// +15 of the block: one load instruction then covers 64 consecutive bytes of
-// each row.  The block's sum starts from zero; it is scaled and added in fp32.
+// A block's 128 products are taken by the matrix cores in one of two ways.
+// Exactly: as 16×16×32 fp16 steps on exactly widened values; measured, the sum
+// is then within 4e-8 of Σ|products|.  Or as one 16×16×128 e4m3 step, half the
+// matrix-core cycles and no conversions.  The e4m3 steps (the 16×16×32 ones
+// too) align each 8 products to the largest of them and cut what lies 2^-13
+// below it: the sum is within 7·2^-13 of Σ|products| whatever they are, and
+// measured within 2^-15 of it on random data (a relative error of 1.5e-5 of the
+// results, where fp16's rounding is 2e-4 and bf16's 1.7e-3).  So they are taken
+// for fp16 and bf16 results of many tokens, where the matrix cores are the
+// bound, and never for fp32 results.
+//
+// A is 16 rows of W, B 16 tokens of X.  The order of the products is free as
+// long as A and B agree, so lane l takes row (or token) l % 16 and the bytes
+// 16·(l/16) .. +15 and 64 + 16·(l/16) .. +15 of the block: one load instruction
+// then covers 64 consecutive bytes of each row.  The block's sum starts from
+// zero; it is scaled and added in fp32.
 // ---------------------------------------------------------------------------
 
 // 8 e4m3 bytes as fp16, exactly.
@@ -191,12 +199,29 @@ __device__ __forceinline__ void store_y(void* Y, int64_t i, float v) {
     static_cast<typename O::storage*>(Y)[i] = narrow(O{}, v);
 }
 
+// Four neighbouring results of a token, from row m on; `vec`: they may be
+// stored at once.
+template <class O>
+__device__ __forceinline__ void store_row4(void* Y, int64_t at, int m, int M, bool vec, f32x4 v) {
+    typename O::storage* y = static_cast<typename O::storage*>(Y) + at + m;
+    if (vec && m + 4 <= M) {
+        struct alignas(4 * O::bytes) Four {
+            typename O::storage v[4];
+        };
+        *reinterpret_cast<Four*>(y) = Four{{narrow(O{}, v[0]), narrow(O{}, v[1]), narrow(O{}, v[2]), narrow(O{}, v[3])}};
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (m + e < M) y[e] = narrow(O{}, v[e]);
+}
+
 // 16 rows of W by 16·NT tokens to a workgroup; its wavefronts take the scale
 // blocks in turn and add their sums in LDS, in a fixed order.
 template <class O, int NT, int W>
 __global__ __launch_bounds__(W * 64) void fp8_few_kernel(
     const uint8_t* A, int64_t lda, const float* as, int64_t ldas, const uint8_t* X, int64_t ldx,
-    const float* xs, int64_t ldxs, const float* bias, void* Y, int64_t ldy, int M, int K, int T) {
+    const float* xs, int64_t ldxs, const float* bias, void* Y, int64_t ldy, int M, int K, int T, int, int) {
     __shared__ f32x4 part[W][NT][64];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const int r = lane & 15, group = lane >> 4;
@@ -246,6 +271,492 @@ __global__ __launch_bounds__(W * 64) void fp8_few_kernel(
                 if (m < M) store_y<O>(Y, (int64_t)t * ldy + m, bias ? v[j] + bias[m] : v[j]);
             }
     }
+}
+
+// ---------------------------------------------------------------------------
+// product over many tokens: tiles staged in LDS
+//
+// A workgroup of eight wavefronts takes BM rows of W by BN tokens, a wavefront
+// WM by WN of them, one scale block at a time.  The bytes go from memory to LDS
+// without passing through registers, STAGES - 1 blocks ahead of the products.
+//
+// Two wavefronts share a SIMD, one of each half of the workgroup, and the
+// halves work in opposite phases: while one reads its operands of a block from
+// LDS, the other multiplies, and at the barrier they change over.  (With both
+// in the same phase the LDS, the matrix cores and the vector ALUs, which scale
+// each block's sum, waited for each other in turn.)
+//
+// LDS.  A stage holds the rows' 128 bytes one behind the other in eight
+// 16-byte slots; slot s of row r holds piece s ^ (r % 8), so that the 8 lanes
+// of a read that want the same piece of 8 neighbouring rows find it in 8
+// different slots (a memory-to-LDS load writes its 64 lanes' pieces in lane
+// order, so the swizzle is in the lanes' addresses).
+// ---------------------------------------------------------------------------
+
+// The wavefront's lanes' 16-byte pieces (or words) at base + offset, written
+// to LDS from `lds` on in lane order (base and lds uniform).  The caller waits
+// (wait_loads): written as instructions, because the compiler, which cannot
+// tell the stages apart, would wait for all of them before it reads any.
+// There is no register result; m0 holds the LDS address and nothing else here
+// uses it.
+__device__ __forceinline__ void lds_load16(const uint8_t* base, uint32_t offset, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :
+                 : "s"(lds), "v"(offset), "s"(base)
+                 : "memory");
+}
+__device__ __forceinline__ void lds_load4(const float* base, uint32_t offset, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
+                 :
+                 : "s"(lds), "v"(offset), "s"(base)
+                 : "memory");
+}
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
+}
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory"); }
+// Nothing moves across a change of phase.
+__device__ __forceinline__ void change_over() {
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+__device__ __forceinline__ f32x4 mma_16x16x128(i32x8 a, i32x8 b) {
+    const f32x4 zero{0.0f, 0.0f, 0.0f, 0.0f};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, zero, 0, 0, 0, 0, 0, 0);
+}
+
+// An operand of a block as its matrix-core steps take it.
+template <bool EXACT>
+struct Operand;
+template <>
+struct Operand<true> {
+    Wide v;
+    __device__ __forceinline__ static Operand of(i32x8 x) { return Operand{widen32(x)}; }
+};
+template <>
+struct Operand<false> {
+    i32x8 v;
+    __device__ __forceinline__ static Operand of(i32x8 x) { return Operand{x}; }
+};
+__device__ __forceinline__ f32x4 block_sum(const Operand<true>& a, const Operand<true>& b) {
+    return mma_block(a.v, b.v);
+}
+__device__ __forceinline__ f32x4 block_sum(const Operand<false>& a, const Operand<false>& b) {
+    return mma_16x16x128(a.v, b.v);
+}
+
+// The 16-byte piece at byte `at` of a row of K bytes; what lies behind the row
+// reads as zero.
+__device__ __forceinline__ quad piece_of(const uint8_t* row, int64_t at, int K) {
+    return at < K ? load_bytes(row + at, (int)(K - at < 16 ? K - at : 16)) : quad{0u, 0u, 0u, 0u};
+}
+
+template <int BM_, int BN_, int WM_, int WN_, int STAGES_, int GROUP_>
+struct Tile {
+    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, STAGES = STAGES_, GROUP = GROUP_;
+    static constexpr int kWaves = BM / WM * (BN / WN);
+    static constexpr int kRows = BM + BN;                      // rows of a stage
+    static constexpr int kStageBytes = kRows * kScaleBlock;
+    static constexpr int kLoads = kRows / 8 / kWaves;          // 1 KiB loads of a wavefront per stage
+    static constexpr int kInFlight = (STAGES - 2) * kLoads;
+    // Scales lie behind the stages, those of kSpan blocks at a time and twice:
+    // the tokens', then the rows' (one for each 128), 8 lines to a load.
+    static constexpr int kSpan = 8;
+    static constexpr int kScaleLoads = BN / 8 + 1;
+    // the same number for every wavefront: spare ones repeat the last
+    static constexpr int kScaleEach = (kScaleLoads + kWaves - 1) / kWaves;
+    static constexpr int kScaleBytes = kScaleLoads * 256;
+    static constexpr int kLds = STAGES * kStageBytes + 2 * kScaleBytes;
+    // wavefronts of a SIMD: two for each workgroup whose LDS fits a compute unit
+    static constexpr int kOccupancy = 2 * (160 * 1024 / kLds) < 4 ? 2 * (160 * 1024 / kLds) : 4;
+    static_assert(kWaves == 8 && kRows % (8 * kWaves) == 0 && BM <= 8 * kScaleBlock, "whole loads");
+};
+
+template <class O, class C, bool EXACT, bool DIRECT>
+__global__ __launch_bounds__(C::kWaves * 64, DIRECT ? C::kOccupancy : 2) void fp8_tile_kernel(
+    const uint8_t* A, int64_t lda, const float* as, int64_t ldas, const uint8_t* X, int64_t ldx,
+    const float* xs, int64_t ldxs, const float* bias, void* Y, int64_t ldy, int M, int K, int T,
+    int row_tiles, int whole_pieces) {
+    constexpr int NM = C::WM / 16, NN = C::WN / 16;
+    extern __shared__ __align__(16) uint8_t lds[];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int r = lane & 15, g = lane >> 4;
+    // the workgroups that share a chiplet's cache (every eighth) take
+    // neighbouring tiles: GROUP row tiles by the tokens, one token tile after the other
+    const int tiles = gridDim.x;
+    const int per = tiles / 8, id = blockIdx.x;
+    const int tile = id < per * 8 ? id % 8 * per + id / 8 : id;
+    const int token_tiles = tiles / row_tiles;
+    const int first_row = tile / (C::GROUP * token_tiles) * C::GROUP;
+    const int in_group = tile - first_row * token_tiles;
+    const int rows = row_tiles - first_row < C::GROUP ? row_tiles - first_row : C::GROUP;
+    const int row0 = (first_row + in_group % rows) * C::BM, t0 = in_group / rows * C::BN;
+    const int wm = wave % (C::BM / C::WM) * C::WM, wn = wave / (C::BM / C::WM) * C::WN;
+    const int blocks = K / kScaleBlock + (K % kScaleBlock != 0);
+    // blocks that are loaded straight into LDS: the whole ones, if pieces are
+    // aligned (DIRECT: all; the other path's registers cost the kernel a sixth)
+    const int direct = DIRECT ? blocks : whole_pieces ? K / kScaleBlock : 0;
+
+    // what the wavefront loads of each stage: 8 rows at a time, of W or of X,
+    // a lane a piece; rows past the end repeat the last one
+    const int in = lane >> 3, piece = 16 * ((lane & 7) ^ in);
+    const uint8_t* base[C::kLoads];
+    int left[C::kLoads];  // rows behind the first of the 8
+#pragma unroll
+    for (int i = 0; i < C::kLoads; ++i) {
+        const int row = (wave + i * C::kWaves) * 8;
+        const bool of_w = row < C::BM;
+        const int last = of_w ? M - 1 : T - 1;
+        int first = of_w ? row0 + row : t0 + row - C::BM;
+        first = first < last ? first : last;
+        left[i] = last - first;
+        base[i] = of_w ? A + (int64_t)first * lda : X + (int64_t)first * ldx;
+    }
+    // ... and which scales: eight lines of eight blocks, block b of line n in
+    // place b ^ (n / 8 % 2), so that 16 neighbouring lines lie in 16 banks
+    const float* sbase[C::kScaleEach];
+    uint32_t soffset[C::kScaleEach], sto[C::kScaleEach];
+#pragma unroll
+    for (int i = 0; i < C::kScaleEach; ++i) {
+        const int n = wave + i * C::kWaves < C::kScaleLoads ? wave + i * C::kWaves : C::kScaleLoads - 1;
+        sto[i] = n * 256;
+        const bool of_x = n < C::BN / 8;
+        const int last = of_x ? T - 1 : (M - 1) / kScaleBlock;
+        int first = of_x ? t0 + n * 8 : row0 / kScaleBlock;
+        first = first < last ? first : last;
+        sbase[i] = of_x ? xs + (int64_t)first * ldxs : as + (int64_t)first * ldas;
+        soffset[i] = (uint32_t)(in < last - first ? in : last - first) * (uint32_t)(of_x ? ldxs : ldas);
+    }
+    const uint32_t lds_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
+    auto stage = [&](int to, int b) {
+        const uint32_t at = lds_at + to * C::kStageBytes;
+        if (!DIRECT && b >= direct) {
+#pragma unroll 1
+            for (int i = 0; i < C::kLoads; ++i) {
+                const int row = (wave + i * C::kWaves) * 8 + in;
+                const bool of_w = row < C::BM;
+                const int want = of_w ? row0 + row : t0 + row - C::BM, last = of_w ? M - 1 : T - 1;
+                const int64_t line = want < last ? want : last;
+                *reinterpret_cast<quad*>(lds + to * C::kStageBytes + (wave + i * C::kWaves) * 1024 + lane * 16) =
+                    piece_of(of_w ? A + line * lda : X + line * ldx, (int64_t)b * kScaleBlock + piece, K);
+            }
+            wait_lds();
+            wait_loads<0>();  // this stage adds nothing to what the phases' waits count
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < C::kLoads; ++i) {
+            const uint32_t pitch = (uint32_t)((wave + i * C::kWaves) * 8 < C::BM ? lda : ldx);
+            lds_load16(base[i] + (int64_t)b * kScaleBlock,
+                       (in < left[i] ? in : left[i]) * pitch + piece, at + (wave + i * C::kWaves) * 1024);
+        }
+    };
+    auto stage_scales = [&](int span) {
+        const uint32_t at = lds_at + C::STAGES * C::kStageBytes + (span & 1) * C::kScaleBytes;
+#pragma unroll
+        for (int i = 0; i < C::kScaleEach; ++i) {
+            const int swap = sto[i] / 256 & 1;  // line n / 8 of the load is n: all its lines share it
+            const int b = span * C::kSpan + ((lane & 7) ^ swap);
+            lds_load4(sbase[i], (soffset[i] + (b < blocks ? b : blocks - 1)) * 4, at + sto[i]);
+        }
+    };
+
+    f32x4 acc[NM][NN];
+#pragma unroll
+    for (int i = 0; i < NM; ++i)
+#pragma unroll
+        for (int j = 0; j < NN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    const int lo = r * kScaleBlock + 16 * (g ^ (r & 7));
+    const int hi = r * kScaleBlock + 16 * ((g + 4) ^ (r & 7));
+    i32x8 xf[NN], af[NM];
+    float st[NN];
+    auto read = [&](int b) {
+        const uint8_t* at = lds + b % C::STAGES * C::kStageBytes;
+        const uint8_t* a = at + wm * kScaleBlock;
+        const uint8_t* x = at + (C::BM + wn) * kScaleBlock;
+        const float* s = reinterpret_cast<const float*>(
+            lds + C::STAGES * C::kStageBytes + (b / C::kSpan & 1) * C::kScaleBytes);
+        const int span_at = b % C::kSpan;
+#pragma unroll
+        for (int j = 0; j < NN; ++j)
+            xf[j] = join(*reinterpret_cast<const quad*>(x + 16 * j * kScaleBlock + lo),
+                         *reinterpret_cast<const quad*>(x + 16 * j * kScaleBlock + hi));
+#pragma unroll
+        for (int i = 0; i < NM; ++i)
+            af[i] = join(*reinterpret_cast<const quad*>(a + 16 * i * kScaleBlock + lo),
+                         *reinterpret_cast<const quad*>(a + 16 * i * kScaleBlock + hi));
+        const float sa = s[(C::BN + wm / kScaleBlock) * C::kSpan + (span_at ^ (C::BN / 8 & 1))];
+#pragma unroll
+        for (int j = 0; j < NN; ++j) st[j] = sa * s[(wn + 16 * j + r) * C::kSpan + (span_at ^ (r >> 3))];
+    };
+    auto multiply = [&]() {
+        // a sum is scaled and added while the kLag next ones are multiplied
+        constexpr int kLag = 3;
+        f32x4 d[kLag + 1];
+        Operand<EXACT> xo[NN];
+#pragma unroll
+        for (int j = 0; j < NN; ++j) xo[j] = Operand<EXACT>::of(xf[j]);
+        Operand<EXACT> ao;
+#pragma unroll
+        for (int n = 0; n < NM * NN + kLag; ++n) {
+            if (n < NM * NN) {
+                if (n % NN == 0) ao = Operand<EXACT>::of(af[n / NN]);
+                d[n % (kLag + 1)] = block_sum(ao, xo[n % NN]);
+            }
+            if (n >= kLag) {
+                const int p = n - kLag, i = p / NN, j = p % NN;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    acc[i][j][e] = __builtin_fmaf(d[p % (kLag + 1)][e], st[j], acc[i][j][e]);
+            }
+        }
+        if constexpr (!EXACT) {
+#pragma unroll
+            for (int n = 0; n < NM * NN + kLag; ++n) {
+                if (n < NM * NN) __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                if (n >= kLag) __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+            }
+        }
+    };
+
+    // Phase 2b: the first half reads block b, the second multiplies block
+    // b - 1; phase 2b + 1: the first half multiplies block b, the second reads
+    // it.  In phase 2b every wavefront loads block b - 1 + STAGES into the stage
+    // that block b - 1 has left; before phase 2b block b has landed.  Past the
+    // last block the last is loaded again, into stages that nothing reads any
+    // more: every wavefront always waits for the same count.
+    const int half = wave >> 2;
+    // The scales of a span are loaded a block after the span before it began,
+    // when nothing reads the span before that any more.
+    auto load = [&](int b) {
+        stage(b % C::STAGES, b < blocks ? b : blocks - 1);
+        const int at = b + 1 - C::STAGES;
+        if (at % C::kSpan == 1) stage_scales(at / C::kSpan + 1);
+    };
+    stage_scales(0);
+#pragma unroll
+    for (int b = 0; b < C::STAGES - 1; ++b) load(b);
+    wait_loads<C::kInFlight>();
+    change_over();
+    if (half == 0) {
+        for (int b = 0; b < blocks; ++b) {
+            load(b + C::STAGES - 1);
+            read(b);
+            wait_lds();
+            change_over();
+            __builtin_amdgcn_s_setprio(1);
+            multiply();
+            __builtin_amdgcn_s_setprio(0);
+            wait_loads<C::kInFlight>();
+            change_over();
+        }
+        change_over();
+    } else {
+        load(C::STAGES - 1);
+        change_over();
+        for (int b = 0; b < blocks; ++b) {
+            read(b);
+            wait_lds();
+            wait_loads<C::kInFlight>();
+            change_over();
+            load(b + C::STAGES);
+            __builtin_amdgcn_s_setprio(1);
+            multiply();
+            __builtin_amdgcn_s_setprio(0);
+            change_over();
+        }
+    }
+    // The results go through LDS, so that a token's BM values are stored as
+    // one piece (straight from the registers they would be 32-byte pieces).
+    wait_loads<0>();
+    change_over();
+    using S = typename O::storage;
+    constexpr int kPitch = C::BM * O::bytes + 16;
+    static_assert(C::BN * kPitch <= C::kLds, "the results fit the stages");
+#pragma unroll
+    for (int i = 0; i < NM; ++i) {
+        const int m = wm + 16 * i + 4 * g;
+        f32x4 add{0.0f, 0.0f, 0.0f, 0.0f};
+        if (bias)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) add[e] = bias[row0 + m + e < M ? row0 + m + e : M - 1];
+#pragma unroll
+        for (int j = 0; j < NN; ++j) {
+            const f32x4 v = acc[i][j] + add;
+            struct alignas(4 * O::bytes) Four {
+                S v[4];
+            };
+            *reinterpret_cast<Four*>(lds + (wn + 16 * j + r) * kPitch + m * O::bytes) =
+                Four{{narrow(O{}, v[0]), narrow(O{}, v[1]), narrow(O{}, v[2]), narrow(O{}, v[3])}};
+        }
+    }
+    __syncthreads();
+    constexpr int kPer = 16 / O::bytes, kAcross = C::BM / kPer;  // a lane's values, the lanes of a token
+    const bool vec = ldy % kPer == 0 && (uintptr_t)Y % 16 == 0;
+    const int m = threadIdx.x % kAcross * kPer;
+    const int left_m = M - row0 - m;
+    for (int t = threadIdx.x / kAcross; t < C::BN && t0 + t < T; t += C::kWaves * 64 / kAcross) {
+        const uint8_t* from = lds + t * kPitch + m * O::bytes;
+        S* to = static_cast<S*>(Y) + (int64_t)(t0 + t) * ldy + row0 + m;
+        if (vec && left_m >= kPer)
+            *reinterpret_cast<quad*>(to) = *reinterpret_cast<const quad*>(from);
+        else
+            for (int e = 0; e < kPer && e < left_m; ++e) to[e] = reinterpret_cast<const S*>(from)[e];
+    }
+}
+
+// ---------------------------------------------------------------------------
+// product over some tens to hundreds of tokens: K split within the workgroup
+//
+// With few tiles a compute unit has one workgroup and a step is bound by its
+// latencies, not by its work; so four groups of four wavefronts take four
+// scale blocks of the same 64 rows by 64 tokens in one step, a fourth of the
+// steps, and join their sums in LDS, in a fixed order.
+// ---------------------------------------------------------------------------
+struct Split {
+    static constexpr int BM = 64, BN = 64, KS = 4, kWaves = 4 * KS;
+    static constexpr int kBlockBytes = (BM + BN) * kScaleBlock;   // of one group
+    static constexpr int kLoads = (BM + BN) / 8 / 4;              // 1 KiB loads of a wavefront per step
+    // scales of a step: a line of KS blocks for each token, then one for the rows
+    static constexpr int kScaleLoads = BN / 16 + 1;
+    static constexpr int kStageBytes = KS * kBlockBytes + kScaleLoads * 256;
+    static constexpr int kLds = 2 * kStageBytes;
+};
+
+template <class O, bool EXACT, bool DIRECT>
+__global__ __launch_bounds__(Split::kWaves * 64) void fp8_split_kernel(
+    const uint8_t* A, int64_t lda, const float* as, int64_t ldas, const uint8_t* X, int64_t ldx,
+    const float* xs, int64_t ldxs, const float* bias, void* Y, int64_t ldy, int M, int K, int T,
+    int row_tiles, int whole_pieces) {
+    using C = Split;
+    extern __shared__ __align__(16) uint8_t lds[];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int ks = wave >> 2, wm = (wave & 1) * 32, wn = (wave >> 1 & 1) * 32;
+    const int r = lane & 15, g = lane >> 4;
+    // neighbours of a chiplet take the same rows of W with all the tokens
+    const int tiles = gridDim.x, per = tiles / 8, id = blockIdx.x;
+    const int tile = id < per * 8 ? id % 8 * per + id / 8 : id;
+    const int token_tiles = tiles / row_tiles;
+    const int row0 = tile / token_tiles * C::BM, t0 = tile % token_tiles * C::BN;
+    const int blocks = K / kScaleBlock + (K % kScaleBlock != 0);
+    const int direct = DIRECT ? blocks : whole_pieces ? K / kScaleBlock : 0;
+
+    const int in = lane >> 3, piece = 16 * ((lane & 7) ^ in);
+    const uint8_t* base[C::kLoads];
+    uint32_t offset[C::kLoads];
+#pragma unroll
+    for (int i = 0; i < C::kLoads; ++i) {
+        const int row = ((wave & 3) + i * 4) * 8;
+        const bool of_w = row < C::BM;
+        const int last = of_w ? M - 1 : T - 1;
+        int first = of_w ? row0 + row : t0 + row - C::BM;
+        first = first < last ? first : last;
+        base[i] = of_w ? A + (int64_t)first * lda : X + (int64_t)first * ldx;
+        offset[i] = (uint32_t)(in < last - first ? in : last - first) * (uint32_t)(of_w ? lda : ldx) + piece;
+    }
+    const int sn = wave < C::kScaleLoads ? wave : C::kScaleLoads - 1;
+    const float* sbase;
+    uint32_t soffset;
+    {
+        const bool of_x = sn < C::BN / 16;
+        const int last = of_x ? T - 1 : (M - 1) / kScaleBlock;
+        int first = of_x ? t0 + sn * 16 : row0 / kScaleBlock;
+        first = first < last ? first : last;
+        const int line = of_x ? lane >> 2 : 0;
+        sbase = of_x ? xs + (int64_t)first * ldxs : as + (int64_t)first * ldas;
+        soffset = (uint32_t)(line < last - first ? line : last - first) * (uint32_t)(of_x ? ldxs : ldas);
+    }
+    const uint32_t lds_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
+    auto stage = [&](int n) {
+        const int b0 = n * C::KS;
+        const int half = (n & 1) * C::kStageBytes, mine = half + ks * C::kBlockBytes;
+        const int b = b0 + ks;
+        if (b < direct) {
+#pragma unroll
+            for (int i = 0; i < C::kLoads; ++i)
+                lds_load16(base[i] + (int64_t)b * kScaleBlock, offset[i],
+                           lds_at + mine + ((wave & 3) + i * 4) * 1024);
+        } else if (!DIRECT && b < blocks) {
+#pragma unroll 1
+            for (int i = 0; i < C::kLoads; ++i) {
+                const int row = ((wave & 3) + i * 4) * 8 + in;
+                const bool of_w = row < C::BM;
+                const int want = of_w ? row0 + row : t0 + row - C::BM, last = of_w ? M - 1 : T - 1;
+                const int64_t line = want < last ? want : last;
+                *reinterpret_cast<quad*>(lds + mine + ((wave & 3) + i * 4) * 1024 + lane * 16) =
+                    piece_of(of_w ? A + line * lda : X + line * ldx, (int64_t)b * kScaleBlock + piece, K);
+            }
+            wait_lds();
+        }
+        const int sb = b0 + (lane & 3);
+        lds_load4(sbase, (soffset + (sb < blocks ? sb : blocks - 1)) * 4,
+                  lds_at + half + C::KS * C::kBlockBytes + sn * 256);
+    };
+
+    f32x4 acc[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    const int lo = r * kScaleBlock + 16 * (g ^ (r & 7));
+    const int hi = r * kScaleBlock + 16 * ((g + 4) ^ (r & 7));
+    const int steps = (blocks + C::KS - 1) / C::KS;
+    if (steps > 0) stage(0);
+    for (int n = 0; n < steps; ++n) {
+        wait_loads<0>();
+        change_over();
+        if (n + 1 < steps) stage(n + 1);
+        if (n * C::KS + ks >= blocks) continue;  // (the barriers are at the loop's head)
+        const uint8_t* half = lds + (n & 1) * C::kStageBytes;
+        const uint8_t* a = half + ks * C::kBlockBytes + wm * kScaleBlock;
+        const uint8_t* x = half + ks * C::kBlockBytes + (C::BM + wn) * kScaleBlock;
+        const float* s = reinterpret_cast<const float*>(half + C::KS * C::kBlockBytes);
+        Operand<EXACT> xo[2];
+        float st[2];
+        const float sa = s[C::BN * C::KS + ks];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            xo[j] = Operand<EXACT>::of(join(*reinterpret_cast<const quad*>(x + 16 * j * kScaleBlock + lo),
+                                            *reinterpret_cast<const quad*>(x + 16 * j * kScaleBlock + hi)));
+            st[j] = sa * s[(wn + 16 * j + r) * C::KS + ks];
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const Operand<EXACT> ao =
+                Operand<EXACT>::of(join(*reinterpret_cast<const quad*>(a + 16 * i * kScaleBlock + lo),
+                                        *reinterpret_cast<const quad*>(a + 16 * i * kScaleBlock + hi)));
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const f32x4 d = block_sum(ao, xo[j]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(d[e], st[j], acc[i][j][e]);
+            }
+        }
+    }
+    change_over();
+    // join: a token's 64 values in a line, the groups' one behind the other
+    constexpr int kPitch = C::BM + 4;
+    float* sums = reinterpret_cast<float*>(lds);
+    static_assert(C::KS * C::BN * kPitch * 4 <= C::kLds, "the sums fit the stages");
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            *reinterpret_cast<f32x4*>(sums + (ks * C::BN + wn + 16 * j + r) * kPitch + wm + 16 * i + 4 * g) = acc[i][j];
+    __syncthreads();
+    const int t = threadIdx.x >> 4, m = (threadIdx.x & 15) * 4;
+    f32x4 v = *reinterpret_cast<const f32x4*>(sums + t * kPitch + m);
+#pragma unroll
+    for (int k = 1; k < C::KS; ++k) v += *reinterpret_cast<const f32x4*>(sums + (k * C::BN + t) * kPitch + m);
+    if (t0 + t >= T || row0 + m >= M) return;
+    if (bias)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] += bias[row0 + m + e < M ? row0 + m + e : M - 1];
+    const bool vec = ldy % 4 == 0 && (uintptr_t)Y % (4 * O::bytes) == 0;
+    store_row4<O>(Y, (int64_t)(t0 + t) * ldy, row0 + m, M, vec, v);
 }
 
 }  // namespace fp8dev

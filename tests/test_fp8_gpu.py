@@ -113,7 +113,7 @@ def test_quantise_nothing():
 
 PSHAPES = [(1, 1, 1), (1, 16, 128), (2, 17, 127), (3, 100, 129), (16, 64, 256), (17, 130, 1000), (33, 65, 300),
            (5, 300, 16), (64, 128, 512), (65, 129, 513), (100, 257, 384), (128, 256, 1024), (129, 300, 640),
-           (200, 520, 272), (300, 384, 260), (1, 4096, 4096), (16, 1000, 4111), (513, 640, 1100)]
+           (200, 520, 272), (300, 384, 260), (40, 5000, 640), (130, 12300, 256), (300, 4099, 400), (1000, 3333, 260), (1, 4096, 4096), (16, 1000, 4111), (513, 640, 1100)]
 
 
 @pytest.mark.parametrize("out", TYPES)
@@ -130,15 +130,21 @@ def test_product(tokens, M, K, out):
     assert_close(y, want, product_bound(size, want, K, out), f"{tokens}x{M}x{K}")
 
 
-@pytest.mark.parametrize("tokens", [1, 20, 150, 400])
-def test_product_exact_integers(tokens):
-    """Small whole numbers and scales of one: every sum is exact."""
-    M, K = 270, 777
-    g = torch.Generator().manual_seed(tokens)
-    W = torch.randint(-4, 5, (M, K), generator=g).float().to(torch.float8_e4m3fn).cuda()
-    X = torch.randint(-4, 5, (tokens, K), generator=g).float().to(torch.float8_e4m3fn).cuda()
-    y = lg.gemv_fp8(W, torch.ones(3, 7, device="cuda"), X, torch.ones(tokens, 7, device="cuda"))
-    assert np.array_equal(y.cpu().double().numpy(), decode(X) @ decode(W).T)
+@pytest.mark.parametrize("out", TYPES)
+@pytest.mark.parametrize("tokens,M", [(1, 270), (20, 270), (40, 270), (150, 270), (400, 4100), (900, 1000), (1030, 3100)])
+def test_product_exact_integers(tokens, M, out):
+    """Small whole numbers and scales of powers of two: every sum is exact, on
+    every path (products of 1 to 16 lie within the matrix cores' 13 bits), and
+    is rounded once."""
+    for K in (777, 1024):
+        g = torch.Generator().manual_seed(tokens + K)
+        W = torch.randint(-4, 5, (M, K), generator=g).float().to(torch.float8_e4m3fn).cuda()
+        X = torch.randint(-4, 5, (tokens, K), generator=g).float().to(torch.float8_e4m3fn).cuda()
+        ws = torch.exp2(torch.randint(-1, 2, (-(-M // 128), -(-K // 128)), generator=g).float()).cuda()
+        xs = torch.exp2(torch.randint(-1, 2, (tokens, -(-K // 128)), generator=g).float()).cuda()
+        y = lg.gemv_fp8(W, ws, X, xs, out_dtype=out)
+        want, _ = product(W, ws, X, xs)
+        assert torch.equal(y.cpu(), torch.from_numpy(want).to(out)), K
 
 
 @pytest.mark.parametrize("tokens,M,K", [(1, 40, 300), (9, 150, 512), (70, 200, 400), (300, 300, 260), (260, 256, 512)])

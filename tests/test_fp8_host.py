@@ -138,7 +138,7 @@ def kernels(tmp_path_factory):
 
 
 def test_kernels_use_no_scratch(kernels):
-    for family in ("fp8_quantise_rows", "fp8_quantise_tile", "fp8_few", "kv_append", "kv_attend", "kv_join"):
+    for family in ("fp8_quantise_rows", "fp8_quantise_tile", "fp8_few", "fp8_tile", "fp8_split", "kv_append", "kv_attend", "kv_join"):
         assert any(family in n for n in kernels), family
     for name, f in kernels.items():
         assert f["private_segment_fixed_size"] == "0" and f["vgpr_spill_count"] == "0", name
