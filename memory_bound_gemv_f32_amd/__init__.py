@@ -30,6 +30,7 @@ contiguous, i.e. Y as M×nvec column-major.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from pathlib import Path
 
@@ -487,47 +488,67 @@ def gemv_gate_up_silu(A_gate, A_up, x, out=None, *, stream=None):
 # e4m3 with a scale per block of 128
 # ---------------------------------------------------------------------------
 
-def _on_device_of(t, fn, *args, stream=None):
-    """fn(*args, stream handle) with t's device current, on the given stream
-    or the current one of that device; raises on a failure code."""
-    torch = _torch()
-    dev = t.device.index
-    s = torch.cuda.current_stream(dev) if stream is None else stream
-    if dev == torch.cuda.current_device():
-        rc = fn(*args, int(s.cuda_stream))
+# These helpers run between launches of a few microseconds: the checks are
+# ordered so that the usual call (contiguous tensors on the current device)
+# passes through few of them.
+if _torch_runtime is not None:
+    _F32, _I32 = _torch_runtime.float32, _torch_runtime.int32
+    _E4M3_BYTES = (_torch_runtime.float8_e4m3fn, _torch_runtime.uint8)
+
+    def _by_dtype(f32, f16, bf16):
+        return {_torch_runtime.float32: f32, _torch_runtime.float16: f16, _torch_runtime.bfloat16: bf16}
+
+    _QUANTISE = _by_dtype(gemv_fp8_quantise_f32, gemv_fp8_quantise_f16, gemv_fp8_quantise_bf16)
+    _PRODUCT = _by_dtype(gemv_fp8_f32, gemv_fp8_f16, gemv_fp8_bf16)
+    _APPEND = _by_dtype(gemv_kv_append_f32, gemv_kv_append_f16, gemv_kv_append_bf16)
+    _ATTEND = {_torch_runtime.float16: gemv_kv_attend_f16, _torch_runtime.bfloat16: gemv_kv_attend_bf16}
+
+
+def _entry(table, dtype):
+    fn = table.get(dtype)
+    if fn is None:
+        raise TypeError(f"unsupported dtype {dtype}; expected one of {', '.join(str(d) for d in table)}")
+    return fn
+
+
+def _call(dev, stream, fn, *args):
+    """fn(*args, stream handle) with device ``dev`` current, on the given
+    stream or the current one of that device; raises on a failure code."""
+    torch = _torch_runtime
+    handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if dev == torch._C._cuda_getDevice():
+        rc = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, int(s.cuda_stream))
+            rc = fn(*args, handle)
     if rc != GEMV_SUCCESS:
         raise GemvError(rc, fn.__name__)
 
 
-def _check_rows(t, name, device=None):
-    """(rows, columns, row stride) of a device matrix with unit column stride."""
-    if t.dim() != 2 or not t.is_cuda:
-        raise ValueError(f"{name} must be a 2-D device tensor")
-    rows, cols = t.shape
+def _rows(t, name, dev):
+    """(rows, columns, row stride) of a matrix with unit column stride on
+    device ``dev``."""
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be 2-D")
+    if dev < 0 or t.get_device() != dev:
+        raise ValueError(f"{name} must be a device tensor, all on one device")
+    rows, cols = shape
+    if t.is_contiguous():
+        return rows, cols, cols
     if cols > 1 and t.stride(1) != 1:
         raise ValueError(f"{name} must have unit column stride")
+    # with one row, or no columns, the pitch is never used
     pitch = t.stride(0) if rows > 1 and cols > 0 else cols
     if pitch < cols:
         raise ValueError(f"{name}'s row stride is smaller than its rows")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on another device")
     return rows, cols, pitch
 
 
-def _e4m3(t, name):
-    torch = _torch()
-    if t.dtype not in (torch.float8_e4m3fn, torch.uint8):
-        raise TypeError(f"{name} must be float8_e4m3fn (or its bytes as uint8)")
-
-
-def _check_scale(scale, name, shape, device):
-    torch = _torch()
-    rows, cols, pitch = _check_rows(scale, name, device)
-    if scale.dtype != torch.float32 or (rows, cols) != shape:
-        raise ValueError(f"{name} must be a float32 tensor of shape {shape}")
+def _scales(t, name, rows, cols, dev):
+    have, across, pitch = _rows(t, name, dev)
+    if have != rows or across != cols or t.dtype is not _F32:
+        raise ValueError(f"{name} must be a float32 tensor of shape {(rows, cols)}")
     return pitch
 
 
@@ -536,23 +557,28 @@ def gemv_fp8_quantise(X, block_rows: int = 1, out=None, scale=None, *, stream=No
     stride) held in e4m3 with a float32 scale for every ``block_rows`` rows (1
     for activations, 128 for weights) and 128 columns.  Q is float8_e4m3fn
     (rows, K), scale (ceil(rows / block_rows), ceil(K / 128))."""
-    torch = _torch()
-    if block_rows not in (1, FP8_BLOCK):
+    torch = _torch_runtime
+    if block_rows != 1 and block_rows != FP8_BLOCK:
         raise ValueError("block_rows must be 1 or 128")
-    rows, K, ldx = _check_rows(X, "X")
-    dt = _dtype_name(X)
-    shape = (-(-rows // block_rows), -(-K // FP8_BLOCK))
+    fn = _entry(_QUANTISE, X.dtype)
+    dev = X.get_device()
+    rows, K, ldx = _rows(X, "X", dev)
+    lines, blocks = -(-rows // block_rows), (K + FP8_BLOCK - 1) // FP8_BLOCK
     if out is None:
         out = torch.empty((rows, K), dtype=torch.float8_e4m3fn, device=X.device)
+        ldq = K
+    else:
+        if out.dtype not in _E4M3_BYTES:
+            raise TypeError("out must be float8_e4m3fn (or its bytes as uint8)")
+        have, across, ldq = _rows(out, "out", dev)
+        if (have, across) != (rows, K):
+            raise ValueError("out must have X's shape")
     if scale is None:
-        scale = torch.empty(shape, dtype=torch.float32, device=X.device)
-    _e4m3(out, "out")
-    if _check_rows(out, "out", X.device)[:2] != (rows, K):
-        raise ValueError("out must have X's shape")
-    lds = _check_scale(scale, "scale", shape, X.device)
-    fn = {"f32": gemv_fp8_quantise_f32, "f16": gemv_fp8_quantise_f16, "bf16": gemv_fp8_quantise_bf16}[dt]
-    _on_device_of(X, fn, X.data_ptr(), ldx, out.data_ptr(),
-                  _check_rows(out, "out")[2], scale.data_ptr(), lds, rows, K, block_rows, stream=stream)
+        scale = torch.empty((lines, blocks), dtype=_F32, device=X.device)
+        lds = blocks
+    else:
+        lds = _scales(scale, "scale", lines, blocks, dev)
+    _call(dev, stream, fn, X.data_ptr(), ldx, out.data_ptr(), ldq, scale.data_ptr(), lds, rows, K, block_rows)
     return out, scale
 
 
@@ -562,29 +588,33 @@ def gemv_fp8(W, w_scale, X, x_scale, bias=None, out=None, *, out_dtype=None, str
     ceil(K / 128)), as ``gemv_fp8_quantise`` gives them; any nvec.  Y is float32,
     or ``out_dtype`` / out's dtype (float16, bfloat16); out may be a column
     slice of a wider matrix."""
-    torch = _torch()
-    _e4m3(W, "W")
-    _e4m3(X, "X")
-    M, K, ldw = _check_rows(W, "W")
-    nvec, Kx, ldx = _check_rows(X, "X", W.device)
+    if W.dtype not in _E4M3_BYTES or X.dtype not in _E4M3_BYTES:
+        raise TypeError("W and X must be float8_e4m3fn (or its bytes as uint8)")
+    dev = W.get_device()
+    M, K, ldw = _rows(W, "W", dev)
+    nvec, Kx, ldx = _rows(X, "X", dev)
     if Kx != K:
         raise ValueError("W and X must have the same number of columns")
-    blocks = -(-K // FP8_BLOCK)
-    ldws = _check_scale(w_scale, "w_scale", (-(-M // FP8_BLOCK), blocks), W.device)
-    ldxs = _check_scale(x_scale, "x_scale", (nvec, blocks), W.device)
-    bias = _check_bias(bias, M, W.device)
+    blocks = (K + FP8_BLOCK - 1) // FP8_BLOCK
+    ldws = _scales(w_scale, "w_scale", (M + FP8_BLOCK - 1) // FP8_BLOCK, blocks, dev)
+    ldxs = _scales(x_scale, "x_scale", nvec, blocks, dev)
+    if bias is not None:
+        bias = _check_bias(bias, M, W.device).data_ptr()
     if out is None:
-        out = torch.empty((nvec, M), dtype=torch.float32 if out_dtype is None else out_dtype, device=W.device)
-    elif out_dtype is not None and out.dtype != out_dtype:
-        raise ValueError("out is not of out_dtype")
-    dt = _dtype_name(out)
-    rows, cols, ldy = _check_rows(out, "out", W.device)
-    if (rows, cols) != (nvec, M):
-        raise ValueError(f"out must be of shape {(nvec, M)}")
-    fn = {"f32": gemv_fp8_f32, "f16": gemv_fp8_f16, "bf16": gemv_fp8_bf16}[dt]
-    _on_device_of(W, fn, W.data_ptr(), ldw, w_scale.data_ptr(), ldws, X.data_ptr(),
-                  ldx, x_scale.data_ptr(), ldxs, bias.data_ptr() if bias is not None else None,
-                  out.data_ptr(), ldy, M, K, nvec, stream=stream)
+        if out_dtype is None:
+            out_dtype = _F32
+        fn = _entry(_PRODUCT, out_dtype)
+        out = _torch_runtime.empty((nvec, M), dtype=out_dtype, device=W.device)
+        ldy = M
+    else:
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError("out is not of out_dtype")
+        fn = _entry(_PRODUCT, out.dtype)
+        rows, cols, ldy = _rows(out, "out", dev)
+        if (rows, cols) != (nvec, M):
+            raise ValueError(f"out must be of shape {(nvec, M)}")
+    _call(dev, stream, fn, W.data_ptr(), ldw, w_scale.data_ptr(), ldws, X.data_ptr(), ldx, x_scale.data_ptr(),
+          ldxs, bias, out.data_ptr(), ldy, M, K, nvec)
     return out
 
 
@@ -622,8 +652,10 @@ class KVCache:
                 raise ValueError("the cache's tensors must be contiguous on one device")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.pages, self.heads, self.page_size, self.dim = pages, heads, page_size, dim
+        self._device = k.get_device()
         self._struct = KvCacheStruct(formats[k.dtype], pages, heads, page_size, dim, k.data_ptr(),
                                      v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr())
+        self._ref = ctypes.byref(self._struct)
 
     @classmethod
     def empty(cls, pages: int, heads: int, dim: int, *, page_size: int = 64, dtype=None, device="cuda"):
@@ -640,31 +672,40 @@ class KVCache:
 
 
 def _kv_batch(cache, table, seq_lens, starts, rows):
-    torch = _torch()
-    sequences = table.shape[0] if table.dim() == 2 else -1
-    if (table.dim() != 2 or table.dtype != torch.int32 or (table.shape[1] > 1 and table.stride(1) != 1)
-            or (sequences > 1 and table.stride(0) < table.shape[1])):
-        raise ValueError("table must be an int32 (sequences, pages) tensor with unit column stride")
-    if seq_lens.dtype != torch.int32 or tuple(seq_lens.shape) != (sequences,) or not seq_lens.is_contiguous():
+    dev = cache._device
+    shape = table.shape
+    if len(shape) != 2 or table.dtype is not _I32:
+        raise ValueError("table must be an int32 (sequences, pages) tensor")
+    sequences, width = shape
+    pitch = width
+    if not table.is_contiguous():
+        pitch = table.stride(0) if sequences > 1 else width
+        if (width > 1 and table.stride(1) != 1) or pitch < width:
+            raise ValueError("table must have unit column stride and a row stride of at least its width")
+    if seq_lens.dtype is not _I32 or seq_lens.shape != (sequences,) or not seq_lens.is_contiguous():
         raise ValueError("seq_lens must be a contiguous int32 (sequences,) tensor")
+    if table.get_device() != dev or seq_lens.get_device() != dev:
+        raise ValueError("table and seq_lens must be on the cache's device")
     if starts is None:
         if rows != sequences:
             raise ValueError("without starts every sequence has one row")
-    elif starts.dtype != torch.int32 or tuple(starts.shape) != (sequences + 1,) or not starts.is_contiguous():
+        return KvBatchStruct(sequences, table.data_ptr(), pitch, width, seq_lens.data_ptr(), None)
+    if starts.dtype is not _I32 or starts.shape != (sequences + 1,) or not starts.is_contiguous():
         raise ValueError("starts must be a contiguous int32 (sequences + 1,) tensor")
-    for t in (table, seq_lens, starts):
-        if t is not None and t.device != cache.k.device:
-            raise ValueError("table, seq_lens and starts must be on the cache's device")
-    return KvBatchStruct(sequences, table.data_ptr(), table.stride(0) if sequences > 1 else table.shape[1],
-                         table.shape[1], seq_lens.data_ptr(), starts.data_ptr() if starts is not None else None)
+    if starts.get_device() != dev:
+        raise ValueError("starts must be on the cache's device")
+    return KvBatchStruct(sequences, table.data_ptr(), pitch, width, seq_lens.data_ptr(), starts.data_ptr())
 
 
-def _check_heads(t, name, cache):
+def _heads(t, name, cache):
     """(rows, heads, row stride) of a (rows, heads, dim) tensor whose rows may
     be columns of a wider matrix."""
-    if t.dim() != 3 or t.shape[2] != cache.dim or t.device != cache.k.device:
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != cache.dim or t.get_device() != cache._device:
         raise ValueError(f"{name} must be (rows, heads, {cache.dim}) on the cache's device")
-    rows, heads, dim = t.shape
+    rows, heads, dim = shape
+    if t.is_contiguous():
+        return rows, heads, heads * dim
     if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
         raise ValueError(f"{name}'s heads must lie one behind the other in a row")
     pitch = t.stride(0) if rows > 1 else heads * dim
@@ -682,25 +723,27 @@ def gemv_kv_append(cache, K, V, table, seq_lens, starts=None, *, stream=None):
     last ones, in rows starts[b] .. starts[b + 1] - 1 (starts (sequences + 1,)
     int32; None: one row for each sequence).  Rows behind the last start are
     ignored."""
-    rows, heads, ldk = _check_heads(K, "K", cache)
-    vrows, vheads, ldv = _check_heads(V, "V", cache)
-    if heads != cache.heads or (vrows, vheads) != (rows, heads) or V.dtype != K.dtype:
+    rows, heads, ldk = _heads(K, "K", cache)
+    vrows, vheads, ldv = _heads(V, "V", cache)
+    if heads != cache.heads or vheads != heads or vrows != rows or V.dtype is not K.dtype:
         raise ValueError("K and V must have the cache's heads, the same rows and the same dtype")
-    dt = _dtype_name(K)
+    fn = _entry(_APPEND, K.dtype)
     batch = _kv_batch(cache, table, seq_lens, starts, rows)
-    fn = {"f32": gemv_kv_append_f32, "f16": gemv_kv_append_f16, "bf16": gemv_kv_append_bf16}[dt]
-    _on_device_of(K, fn, ctypes.byref(cache._struct), K.data_ptr(), ldk,
-                  V.data_ptr(), ldv, rows, ctypes.byref(batch), stream=stream)
+    _call(cache._device, stream, fn, cache._ref, K.data_ptr(), ldk, V.data_ptr(), ldv, rows, ctypes.byref(batch))
+
+
+@functools.lru_cache(maxsize=256)
+def _attend_workspace(q_heads, heads, dim, rows, sequences, table_width, page_size):
+    n = ctypes.c_size_t(0)
+    rc = gemv_kv_attend_workspace_size(q_heads, heads, dim, rows, sequences, table_width, page_size, ctypes.byref(n))
+    if rc != GEMV_SUCCESS:
+        raise GemvError(rc, "gemv_kv_attend_workspace_size")
+    return n.value
 
 
 def kv_attend_workspace_size(cache, q_heads: int, rows: int, sequences: int, table_width: int) -> int:
     """Workspace bytes that ``gemv_kv_attend`` needs (0: none)."""
-    n = ctypes.c_size_t(0)
-    rc = gemv_kv_attend_workspace_size(q_heads, cache.heads, cache.dim, rows, sequences, table_width,
-                                       cache.page_size, ctypes.byref(n))
-    if rc != GEMV_SUCCESS:
-        raise GemvError(rc, "gemv_kv_attend_workspace_size")
-    return n.value
+    return _attend_workspace(q_heads, cache.heads, cache.dim, rows, sequences, table_width, cache.page_size)
 
 
 def gemv_kv_attend(Q, cache, table, seq_lens, starts=None, *, scale=None, window: int = 0, sinks: int = 0,
@@ -715,25 +758,26 @@ def gemv_kv_attend(Q, cache, table, seq_lens, starts=None, *, scale=None, window
     left as they were.  workspace: a device tensor of at least
     ``kv_attend_workspace_size(...)`` bytes, allocated here through torch when
     not given."""
-    torch = _torch()
-    if Q.dtype not in (torch.float16, torch.bfloat16):
-        raise TypeError("Q must be float16 or bfloat16")
-    rows, q_heads, ldq = _check_heads(Q, "Q", cache)
+    torch = _torch_runtime
+    fn = _entry(_ATTEND, Q.dtype)
+    rows, q_heads, ldq = _heads(Q, "Q", cache)
     if out is None:
         out = torch.empty((rows, q_heads, cache.dim), dtype=Q.dtype, device=Q.device)
-    if out.dtype != Q.dtype or tuple(out.shape) != tuple(Q.shape):
-        raise ValueError("out must have Q's shape and dtype")
-    _, _, ldo = _check_heads(out, "out", cache)
+        ldo = q_heads * cache.dim
+    else:
+        if out.dtype is not Q.dtype or out.shape != Q.shape:
+            raise ValueError("out must have Q's shape and dtype")
+        ldo = _heads(out, "out", cache)[2]
     batch = _kv_batch(cache, table, seq_lens, starts, rows)
-    need = kv_attend_workspace_size(cache, q_heads, rows, batch.sequences, batch.table_width)
-    if workspace is None and need:
-        workspace = torch.empty(need // 4, dtype=torch.float32, device=Q.device)
-    if workspace is not None and (workspace.device != Q.device or not workspace.is_contiguous()):
-        raise ValueError("workspace must be a contiguous tensor on Q's device")
-    fn = gemv_kv_attend_f16 if Q.dtype == torch.float16 else gemv_kv_attend_bf16
-    _on_device_of(Q, fn, ctypes.byref(cache._struct), Q.data_ptr(), ldq,
-                  out.data_ptr(), ldo, q_heads, rows, ctypes.byref(batch),
-                  cache.dim ** -0.5 if scale is None else scale, window, sinks,
-                  workspace.data_ptr() if workspace is not None else None,
-                  workspace.numel() * workspace.element_size() if workspace is not None else 0, stream=stream)
+    need = _attend_workspace(q_heads, cache.heads, cache.dim, rows, batch.sequences, batch.table_width,
+                             cache.page_size)
+    if workspace is not None:
+        if workspace.get_device() != cache._device or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the cache's device")
+        need = workspace.numel() * workspace.element_size()
+    elif need:
+        workspace = torch.empty(need // 4, dtype=_F32, device=Q.device)
+    _call(cache._device, stream, fn, cache._ref, Q.data_ptr(), ldq, out.data_ptr(), ldo, q_heads, rows,
+          ctypes.byref(batch), cache.dim ** -0.5 if scale is None else scale, window, sinks,
+          workspace.data_ptr() if workspace is not None else None, need)
     return out
