@@ -358,8 +358,8 @@ gemv_status_t gemv_fp8_bf16(const uint8_t *W, int ldw, const float *w_scale,
  *   k_scale  [pages][heads][page_size / 16] fp32
  *   v_scale  the same
  *
- * A value is its byte times its block's scale.  Bytes are int8 (-127..127) or
- * e4m3.  A new cache needs no initial contents.
+ * A value is its byte times its block's scale, which is not negative.  Bytes
+ * are int8 (-127..127) or e4m3.  A new cache needs no initial contents.
  * ------------------------------------------------------------------------ */
 #define GEMV_KV_BLOCK 16
 
@@ -434,9 +434,10 @@ gemv_status_t gemv_kv_append_bf16(const gemv_kv_cache_t *cache, const uint16_t *
  * Q, O  rows x q_heads x dim of the type in the name, ldq and ldo elements
  *       from row to row; O must not overlap the other arguments.
  * scale finite; usually 1/sqrt(dim).
- * workspace  device memory of at least gemv_kv_attend_workspace_size bytes,
- *       16-byte aligned (may be NULL where that is 0); contract as for
- *       gemv_splitk_*.
+ * workspace  device memory of at least gemv_kv_attend_workspace_size bytes
+ *       (one_each: 1 where the batch has no starts, else 0; it depends on sizes
+ *       only, and not on the lengths), 16-byte aligned; may be NULL where that is
+ *       0; contract as for gemv_splitk_*.
  * Q and the cache's bytes enter the products exactly; scores, the softmax and
  * its sums are fp32; a softmax weight is rounded to Q's type before it meets V,
  * and the result once.  Deterministic: the order in which tokens are joined
@@ -446,8 +447,9 @@ gemv_status_t gemv_kv_append_bf16(const gemv_kv_cache_t *cache, const uint16_t *
  * finite, and a workspace that is too small. */
 gemv_status_t gemv_kv_attend_workspace_size(int q_heads, int heads, int dim,
                                             int rows, int sequences,
-                                            int table_width, int page_size,
-                                            size_t *bytes);
+                                            int one_each, int table_width,
+                                            int page_size, int window,
+                                            int sinks, size_t *bytes);
 gemv_status_t gemv_kv_attend_f16(const gemv_kv_cache_t *cache, const uint16_t *Q,
                                 int ldq, uint16_t *O, int ldo, int q_heads,
                                 int rows, const gemv_kv_batch_t *batch,

@@ -176,7 +176,7 @@ gemv_kv_append_f32 = _bind("gemv_kv_append_f32", _append_args)
 gemv_kv_append_f16 = _bind("gemv_kv_append_f16", _append_args)
 gemv_kv_append_bf16 = _bind("gemv_kv_append_bf16", _append_args)
 gemv_kv_attend_workspace_size = _bind("gemv_kv_attend_workspace_size",
-                                      [_i, _i, _i, _i, _i, _i, _i, ctypes.POINTER(_sz)])
+                                      [_i, _i, _i, _i, _i, _i, _i, _i, _i, _i, ctypes.POINTER(_sz)])
 _attend_args = [_cache_p, _vp, _i, _vp, _i, _i, _i, _batch_p, ctypes.c_float, _i, _i, _vp, _sz, _st]
 gemv_kv_attend_f16 = _bind("gemv_kv_attend_f16", _attend_args)
 gemv_kv_attend_bf16 = _bind("gemv_kv_attend_bf16", _attend_args)
@@ -733,17 +733,21 @@ def gemv_kv_append(cache, K, V, table, seq_lens, starts=None, *, stream=None):
 
 
 @functools.lru_cache(maxsize=256)
-def _attend_workspace(q_heads, heads, dim, rows, sequences, table_width, page_size):
+def _attend_workspace(q_heads, heads, dim, rows, sequences, one_each, table_width, page_size, window, sinks):
     n = ctypes.c_size_t(0)
-    rc = gemv_kv_attend_workspace_size(q_heads, heads, dim, rows, sequences, table_width, page_size, ctypes.byref(n))
+    rc = gemv_kv_attend_workspace_size(q_heads, heads, dim, rows, sequences, one_each, table_width, page_size, window,
+                                       sinks, ctypes.byref(n))
     if rc != GEMV_SUCCESS:
         raise GemvError(rc, "gemv_kv_attend_workspace_size")
     return n.value
 
 
-def kv_attend_workspace_size(cache, q_heads: int, rows: int, sequences: int, table_width: int) -> int:
-    """Workspace bytes that ``gemv_kv_attend`` needs (0: none)."""
-    return _attend_workspace(q_heads, cache.heads, cache.dim, rows, sequences, table_width, cache.page_size)
+def kv_attend_workspace_size(cache, q_heads: int, rows: int, sequences: int, table_width: int, *,
+                             one_each: bool = True, window: int = 0, sinks: int = 0) -> int:
+    """Workspace bytes that ``gemv_kv_attend`` needs (0: none); one_each: the
+    call has no ``starts``.  It depends on these sizes only."""
+    return _attend_workspace(q_heads, cache.heads, cache.dim, rows, sequences, int(one_each), table_width,
+                             cache.page_size, window, sinks)
 
 
 def gemv_kv_attend(Q, cache, table, seq_lens, starts=None, *, scale=None, window: int = 0, sinks: int = 0,
@@ -769,8 +773,8 @@ def gemv_kv_attend(Q, cache, table, seq_lens, starts=None, *, scale=None, window
             raise ValueError("out must have Q's shape and dtype")
         ldo = _heads(out, "out", cache)[2]
     batch = _kv_batch(cache, table, seq_lens, starts, rows)
-    need = _attend_workspace(q_heads, cache.heads, cache.dim, rows, batch.sequences, batch.table_width,
-                             cache.page_size)
+    need = _attend_workspace(q_heads, cache.heads, cache.dim, rows, batch.sequences, starts is None,
+                             batch.table_width, cache.page_size, window, sinks)
     if workspace is not None:
         if workspace.get_device() != cache._device or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on the cache's device")

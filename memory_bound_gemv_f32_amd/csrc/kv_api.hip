@@ -75,30 +75,58 @@ struct Mapping {
     int row_tiles;     // 16-row tiles of a wavefront
     int waves_share;   // 4: the wavefronts take the chunks of the same rows in turn; 1: own rows each
     int group_rows;    // rows of a workgroup
-    int splits;
+    int place_rows;    // rows of it that can be there
+    int splits, split_chunks;
     int64_t places;
 };
 
-constexpr int64_t kWorkgroups = 1024;  // enough to keep 256 compute units reading
+// A split is a workgroup's work.  Where all of it fits the 512 slots (two
+// workgroups for each compute unit) in splits of at most 32 chunks (2048 tokens),
+// that many, of at least 8 (less is mostly start-up); else splits of 12, short
+// enough that the last round of workgroups is not long.  Measured, us: one
+// sequence of 131071 tokens, 8 heads: 59 | 58 | 54 | 56 | 51 with splits of 8 | 12
+// | 16 | 24 | 32; 64 sequences of up to 8192: 127 | 113 | 120 | 114 | 137.  The
+// longest contexts and largest batches get longer ones, so that the workspace
+// stays at 8192 workgroups' rows.
+constexpr int64_t kLeastSplit = 8, kOneRoundSplit = 32, kSplit = 12, kSlots = 512, kMostWorkgroups = 8192;
 
-Mapping map_attend(int q_heads, int heads, int rows, int sequences, int64_t capacity) {
+Mapping map_attend(int q_heads, int heads, int dim, int rows, int sequences, bool one_each, int64_t capacity,
+                   int window, int sinks) {
     Mapping m;
     const int group = q_heads / heads;
-    const int64_t per_sequence = sequences > 0 ? ceil_div((int64_t)rows * group, sequences) : 0;
-    m.waves_share = per_sequence <= 16 ? 4 : 1;
-    m.row_tiles = 1;
-    m.group_rows = 16 * m.row_tiles * (m.waves_share == 1 ? kvdev::kAttWaves : 1);
-    m.places = (int64_t)rows * group / m.group_rows + sequences;
-    const int64_t chunks = ceil_div(capacity, kvdev::kChunk * m.waves_share);
-    int64_t splits = m.places > 0 ? ceil_div(kWorkgroups, m.places * heads) : 1;
-    if (splits > chunks) splits = chunks;
-    m.splits = (int)(splits < 1 ? 1 : splits);
+    const int64_t per_sequence = one_each ? group : ceil_div((int64_t)rows * group, sequences);
+    m.waves_share = per_sequence <= 32 ? 4 : 1;
+    m.row_tiles = per_sequence <= 16 || dim > 128 ? 1 : 2;  // (two of dim 256 would not fit the registers)
+    m.group_rows = 16 * m.row_tiles * (m.waves_share == 1 ? kvdev::kOwnWaves : 1);
+    m.places = one_each ? sequences * ceil_div(group, m.group_rows)
+                        : (int64_t)rows * group / m.group_rows + sequences;
+    m.place_rows = one_each && group < m.group_rows ? group : m.group_rows;
+    // chunks that a row tile can see
+    int64_t chunks = ceil_div(capacity, kvdev::kChunk);
+    if (window > 0) {
+        const int64_t tokens = ceil_div(m.group_rows, group) + 1;
+        const int64_t in_window = ceil_div((int64_t)window + tokens, kvdev::kChunk) + 1 +
+                                  ceil_div(sinks, kvdev::kChunk);
+        if (in_window < chunks) chunks = in_window;
+    }
+    const int64_t all = m.places * heads * chunks;
+    int64_t each = ceil_div(all, kSlots);
+    each = each > kOneRoundSplit ? kSplit : each < kLeastSplit ? kLeastSplit : each;
+    if (each < ceil_div(all, kMostWorkgroups)) each = ceil_div(all, kMostWorkgroups);
+    if (each < ceil_div(chunks, kvdev::kMaxSplits)) each = ceil_div(chunks, kvdev::kMaxSplits);
+    // a split that would save little; many rows, whose partial results cost more than they save once
+    // half the slots have a workgroup
+    if (chunks < 2 * kLeastSplit || (m.waves_share == 1 && m.places * heads >= kSlots / 2)) each = chunks;
+    m.splits = each > 0 ? (int)ceil_div(chunks, each) : 1;
+    if (m.splits < 1) m.splits = 1;
+    m.split_chunks = (int)each;
     return m;
 }
 
 size_t workspace_of(const Mapping& m, int heads, int dim) {
     if (m.splits == 1) return 0;
-    return (size_t)m.places * heads * m.splits * m.group_rows * (dim + 2) * sizeof(float);
+    const size_t parts = (size_t)m.places * heads * m.splits * m.place_rows;
+    return (parts * (dim + 2) * sizeof(float) + 15) / 16 * 16;
 }
 
 int64_t capacity_of(int64_t table_width, int page_size) {
@@ -112,14 +140,18 @@ gemv_status_t attend(const Mapping& m, Attend& p, hipStream_t stream) {
     const int64_t grid = places * p.cache.heads * p.splits;
     if (grid > 0x7fffffff) return GEMV_ERROR_INVALID_VALUE;
     void* argv[] = {&p, &places};
-    const void* fn = m.waves_share == 4 ? (const void*)&kvdev::kv_attend_kernel<T, F, DIM, 1, 4>
-                                        : (const void*)&kvdev::kv_attend_kernel<T, F, DIM, 1, 1>;
-    const gemv_status_t st = launch(fn, dim3((unsigned)grid), kvdev::kAttWaves * 64, argv, stream);
+    constexpr int kTwo = DIM <= 128 ? 2 : 1;
+    const void* fn = m.waves_share == 1 ? (const void*)&kvdev::kv_attend_kernel<T, F, DIM, kTwo, 1>
+                     : m.row_tiles == 2 ? (const void*)&kvdev::kv_attend_kernel<T, F, DIM, kTwo, 4>
+                                        : (const void*)&kvdev::kv_attend_kernel<T, F, DIM, 1, 4>;
+    const gemv_status_t st = launch(fn, dim3((unsigned)grid),
+                                    64 * (m.waves_share == 1 ? kvdev::kOwnWaves : kvdev::kShareWaves), argv, stream);
     if (st != GEMV_SUCCESS || p.splits == 1) return st;
-    const void* join = m.group_rows == 16 ? (const void*)&kvdev::kv_join_kernel<T, DIM, 16>
-                                          : (const void*)&kvdev::kv_join_kernel<T, DIM, 64>;
-    return launch(join, dim3((unsigned)(places * p.cache.heads), (unsigned)(m.group_rows / 16)),
-                  kvdev::kAttWaves * 64, argv, stream);
+    const void* join = m.waves_share == 1 ? (const void*)&kvdev::kv_join_kernel<T, DIM, 16 * kvdev::kOwnWaves * kTwo, 16 * kTwo>
+                       : m.row_tiles == 2 ? (const void*)&kvdev::kv_join_kernel<T, DIM, 16 * kTwo, 16 * kTwo>
+                                          : (const void*)&kvdev::kv_join_kernel<T, DIM, 16, 16>;
+    return launch(join, dim3((unsigned)(places * p.cache.heads), (unsigned)m.place_rows),
+                  kvdev::kShareWaves * 64, argv, stream);
 }
 
 template <class T, class F>
@@ -159,7 +191,8 @@ gemv_status_t attend(const gemv_kv_cache_t* cache, const uint16_t* Q, int ldq, u
     if (rows == 0 || p.batch.count == 0) return GEMV_SUCCESS;
     if (Q == nullptr || O == nullptr || !aligned(Q, 2) || !aligned(O, 2)) return GEMV_ERROR_INVALID_VALUE;
     const int64_t capacity = capacity_of(batch->table_width, cache->page_size);
-    const Mapping m = map_attend(q_heads, p.cache.heads, rows, p.batch.count, capacity);
+    const Mapping m = map_attend(q_heads, p.cache.heads, cache->dim, rows, p.batch.count, batch->starts == nullptr,
+                                 capacity, window, sinks);
     const size_t need = workspace_of(m, p.cache.heads, cache->dim);
     if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 16)))
         return GEMV_ERROR_INVALID_VALUE;
@@ -168,11 +201,14 @@ gemv_status_t attend(const gemv_kv_cache_t* cache, const uint16_t* Q, int ldq, u
     p.O = O;
     p.ldo = ldo;
     p.group = q_heads / p.cache.heads;
-    p.scale = scale * 1.44269504088896341f;
+    p.scale = (scale < 0.0f ? -scale : scale) * 1.44269504088896341f;
+    p.q_sign = scale < 0.0f ? 0x80008000u : 0u;
     p.window = window;
     p.sinks = sinks;
     p.capacity = (int)capacity;
     p.splits = m.splits;
+    p.split_chunks = m.split_chunks;
+    p.rows = m.place_rows;
     p.partial = static_cast<float*>(workspace);
     return cache->format == GEMV_KV_E4M3 ? attend_dim<T, E4m3>(cache->dim, m, p, stream)
                                          : attend_dim<T, Int8>(cache->dim, m, p, stream);
@@ -181,14 +217,16 @@ gemv_status_t attend(const gemv_kv_cache_t* cache, const uint16_t* Q, int ldq, u
 }  // namespace
 
 extern "C" gemv_status_t gemv_kv_attend_workspace_size(int q_heads, int heads, int dim, int rows,
-                                                       int sequences, int table_width, int page_size,
-                                                       size_t* bytes) {
+                                                       int sequences, int one_each, int table_width,
+                                                       int page_size, int window, int sinks, size_t* bytes) {
     if (bytes == nullptr || heads < 1 || q_heads < 1 || q_heads % heads != 0 || !known_dim(dim) ||
-        rows < 0 || sequences < 0 || table_width < 0 || page_size < GEMV_KV_BLOCK)
+        rows < 0 || sequences < 0 || (one_each && rows != sequences) || table_width < 0 ||
+        page_size < GEMV_KV_BLOCK || window < 0 || sinks < 0)
         return GEMV_ERROR_INVALID_VALUE;
     *bytes = rows == 0 || sequences == 0
                  ? 0
-                 : workspace_of(map_attend(q_heads, heads, rows, sequences, capacity_of(table_width, page_size)),
+                 : workspace_of(map_attend(q_heads, heads, dim, rows, sequences, one_each != 0,
+                                           capacity_of(table_width, page_size), window, sinks),
                                 heads, dim);
     return GEMV_SUCCESS;
 }

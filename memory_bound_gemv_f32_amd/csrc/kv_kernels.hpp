@@ -248,8 +248,10 @@ __global__ __launch_bounds__(64) void kv_append_kernel(Cache c, Batch q,
 //
 // K and V are widened exactly (e4m3 and int8 both fit fp16 and bf16); a
 // block's scales are one number a lane: K's multiplies S in fp32, V's
-// multiplies P.  P is rounded to Q's type; relative to the largest V scale
-// seen so far, so that it stays at most 1 and fp16 does not underflow.
+// multiplies P.  K meets Q in Q's type, P meets V in fp16, whatever Q is: P
+// times its block's V scale over the largest such scale that its row has seen is at most 1,
+// so fp16 holds it with its full 11 bits (bf16 would keep 8), and what falls
+// below fp16's range is 2^-24 of the row's largest term.
 // ---------------------------------------------------------------------------
 
 using fp8dev::bf16x2;
@@ -302,12 +304,37 @@ __device__ __forceinline__ float max_of_groups(float v) {  // over the four 16-l
     r = __builtin_amdgcn_permlane32_swap(w, w, false, false);
     return fmaxf(gemvdev::f32_of(r[0]), gemvdev::f32_of(r[1]));
 }
+__device__ __forceinline__ float wave_max(float v) {
+    v = fmaxf(v, gemvdev::dpp<gemvdev::kDppSwapAdjacent>(v));
+    v = fmaxf(v, gemvdev::dpp<gemvdev::kDppSwapPairs>(v));
+    v = fmaxf(v, gemvdev::dpp<gemvdev::kDppHalfRowMirror>(v));
+    v = fmaxf(v, gemvdev::dpp<gemvdev::kDppRowMirror>(v));
+    return max_of_groups(v);
+}
 __device__ __forceinline__ float sum_of_groups(float v) {
     return gemvdev::half_pair_sum32(gemvdev::row_pair_sum16(v));
 }
 
+// 16 bytes of the cache; ONCE: nothing reads them again in this call, so they
+// go past the caches (nontemporal; 7 % of one long sequence's time).
+template <bool ONCE>
+__device__ __forceinline__ quad load_once(const uint8_t* p) {
+    if constexpr (ONCE) return __builtin_nontemporal_load(reinterpret_cast<const quad*>(p));
+    return *reinterpret_cast<const quad*>(p);
+}
+
+// A row that has seen nothing keeps its base at -inf; its exponents are taken
+// against 0.
+__device__ __forceinline__ float finite_base(float m) { return m == -__builtin_inff() ? 0.0f : m; }
+constexpr float kSlack = 8.0f;
+
 constexpr int kChunk = 64;    // tokens of a step: four blocks
-constexpr int kAttWaves = 4;  // wavefronts of a workgroup
+// Wavefronts of a workgroup: 4 that share their rows, or 2 with rows of their
+// own (4 of those would read the same bytes more often from the same cache, but
+// leave fewer and longer workgroups: 176 us against 183 for four 1024-token prompts).
+constexpr int kShareWaves = 4, kOwnWaves = 2;
+template <int WS>
+constexpr int kWavesOf = WS == 1 ? kOwnWaves : kShareWaves;
 
 struct Attend {
     Cache cache;
@@ -317,11 +344,14 @@ struct Attend {
     uint16_t* O;
     int64_t ldo;
     int group;          // query heads that share a K/V head
-    float scale;        // softmax scale · log2(e)
+    float scale;        // |softmax scale| · log2(e)
+    uint32_t q_sign;    // sign bits of two values of Q, set where the scale is negative
     int window, sinks;  // window 0: none
     int capacity;       // tokens that a row of the table can hold
-    int splits;         // workgroups that share a row tile's tokens
-    float* partial;     // splits > 1: see partial_at
+    int splits;         // workgroups that share a row tile's tokens, ...
+    int split_chunks;   // ... each so many chunks of them; splits > 1:
+    int rows;           // rows of a place that can be there
+    float* partial;     // see partial_at
 };
 
 // What a row tile sees: chunks [0, first) hold the first tokens that stay
@@ -359,8 +389,15 @@ struct Tile {
 template <int R>
 __device__ __forceinline__ bool tile_of(const Attend& p, int64_t place, Tile& t) {
     const Batch& q = p.batch;
-    t.b = sequence_of(q, place, p.group, R, 1);
-    const int64_t r0 = (place - first_place(q, t.b, p.group, R, 1)) * R;
+    int64_t r0;
+    if (q.starts == nullptr) {  // one token each: so many places for its heads
+        const int each = (p.group + R - 1) / R;
+        t.b = (int)(place / each);
+        r0 = (place - (int64_t)t.b * each) * R;
+    } else {
+        t.b = sequence_of(q, place, p.group, R, 1);
+        r0 = (place - first_place(q, t.b, p.group, R, 1)) * R;
+    }
     t.start = start_of(q, t.b);
     const int stop = start_of(q, t.b + 1);
     // rows outside the call's are not there, whatever the starts say
@@ -372,37 +409,36 @@ __device__ __forceinline__ bool tile_of(const Attend& p, int64_t place, Tile& t)
     return r0 >= 0 && r0 < t.rows;
 }
 
-// splits > 1: each split leaves its unnormalised row and the row's m and l,
-// for rows of a place, a head and a split: first all (m, l), then all rows.
+// splits > 1: each split of a place and head leaves p.rows rows, unnormalised,
+// and their m and l: first all (m, l), then all rows.
 struct Partial {
     float* ml;
     float* rows;
 };
-template <int R, int DIM>
+template <int DIM>
 __device__ __forceinline__ Partial partial_at(const Attend& p, int64_t places, int64_t part) {
     const int64_t parts = places * p.cache.heads * p.splits;
-    return Partial{p.partial + part * R * 2, p.partial + parts * R * 2 + part * R * DIM};
+    return Partial{p.partial + part * p.rows * 2, p.partial + parts * p.rows * 2 + part * p.rows * DIM};
 }
 
 // WS = 4: the workgroup's wavefronts take the chunks of one row tile in turn
 // and join in LDS.  WS = 1: each wavefront has a row tile of its own.
 template <class T, class F, int DIM, int RT, int WS>
-__global__ __launch_bounds__(kAttWaves * 64) void kv_attend_kernel(Attend p, int64_t places) {
+__global__ __launch_bounds__(kWavesOf<WS> * 64, DIM <= 128 ? 2 : 1) void kv_attend_kernel(Attend p, int64_t places) {
     constexpr int kRows = 16 * RT;                              // rows of a wavefront
-    constexpr int kGroupRows = WS == 1 ? kAttWaves * kRows : kRows;
+    constexpr int kGroupRows = WS == 1 ? kOwnWaves * kRows : kRows;
     constexpr int kSteps = DIM / 32;                            // K·Q^T steps
     constexpr int kTiles = DIM / 16;                            // 16-dim tiles of O^T
-    constexpr bool kRelative = std::is_same<T, TF16>::value;    // P over the largest V scale
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const int n = lane & 15, g = lane >> 4;
     const Cache& c = p.cache;
     // heads fastest: neighbouring workgroups, which go to different chiplets,
-    // share no K or V; then the splits; the last rows, which see the most, first
+    // share no K or V; then the splits
     int64_t at = blockIdx.x;
     const int head = (int)(at % c.heads);
     at /= c.heads;
     const int split = (int)(at % p.splits);
-    const int64_t place = places - 1 - at / p.splits;
+    const int64_t place = at / p.splits;
     Tile t;
     if (!tile_of<kGroupRows>(p, place, t)) return;
     const int r0 = t.r0 + (WS == 1 ? wave * kRows : 0);
@@ -410,11 +446,15 @@ __global__ __launch_bounds__(kAttWaves * 64) void kv_attend_kernel(Attend p, int
     const int last = (r0 + kRows < t.rows ? r0 + kRows : t.rows) - 1;
     const int min_pos = t.first + r0 / p.group, max_pos = t.first + last / p.group;
     const Span span = span_of(p, min_pos, max_pos, t.len);
-    const int per_split = (span.count() + p.splits - 1) / p.splits;
-    const int begin = split * per_split;
-    const int end = begin + per_split < span.count() ? begin + per_split : span.count();
+    const int begin = p.splits == 1 ? 0 : split * p.split_chunks;
+    int end = p.splits == 1 ? span.count() : begin + p.split_chunks;
+    end = end < span.count() ? end : span.count();
+    if (split > 0 && begin >= end) return;  // (the whole workgroup: the splits are cut for all its rows alike)
 
     // the lane's row of each 16: its position (-1: none) and its Q
+    // (two tiles' Q does not fit the registers beside the rest: it stays in LDS)
+    constexpr bool kQInLds = RT > 1;
+    __shared__ quad q_lds[kQInLds ? kWavesOf<WS> : 1][kQInLds ? RT : 1][kQInLds ? kSteps : 1][64];
     int pos[RT];
     int64_t row[RT];     // row of the call
     int qhead[RT];
@@ -430,139 +470,238 @@ __global__ __launch_bounds__(kAttWaves * 64) void kv_attend_kernel(Attend p, int
         const uint16_t* src = p.Q + row[i] * p.ldq + (int64_t)qhead[i] * DIM + 16 * g;
 #pragma unroll
         for (int s = 0; s < kSteps; ++s)
-            q[i][s] = *reinterpret_cast<const quad_any*>(src + 64 * (s >> 1) + 8 * (s & 1));
+            q[i][s] = *reinterpret_cast<const quad_any*>(src + 64 * (s >> 1) + 8 * (s & 1)) ^ p.q_sign;
+        if constexpr (kQInLds)  // read back by the lane that wrote it
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) q_lds[wave][i][s][lane] = q[i][s];
     }
+    const auto q_of = [&](int i, int s) {
+        if constexpr (kQInLds) return q_lds[wave][i][s][lane];
+        return q[i][s];
+    };
 
     f32x4 o[RT][kTiles];
     float m[RT], l[RT];
-    float vref = kRelative ? 0.0f : 1.0f;
+    // the largest finite V scale that the row has seen, and its reciprocal (0
+    // while that is 0): o is in its unit
+    float vref[RT], vinv[RT];
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
+        vref[i] = 0.0f;
+        vinv[i] = 0.0f;
         m[i] = -__builtin_inff();
         l[i] = 0.0f;
 #pragma unroll
         for (int u = 0; u < kTiles; ++u) o[i][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
 
-    for (int it = begin + (WS == 1 ? 0 : wave); it < end; it += WS) {
+    // Of a chunk's four blocks, the lane reads K from block n / 4 and V from
+    // block g.  A block's page is looked up two chunks ahead.  With one row
+    // tile a chunk's bytes are loaded while the chunk before it is worked on,
+    // into registers of their own (single tokens wait for memory, and a wave's 16
+    // KiB in flight are what hides it); with two, or dim 256, there is room for one
+    // chunk, and its K is loaded behind the first product of the chunk before, its V behind
+    // the second.
+    constexpr bool kAhead = RT == 1 && DIM <= 128;
+    // The table's entries as they are: what they are worth is looked at when
+    // they are used, so that the lookup never waits for the loads before it.
+    struct Where {
+        int kpage, vpage;
+    };
+    const int* table = p.batch.table + (int64_t)t.b * p.batch.table_pitch;
+    auto entry_of = [&](int block) {
+        const int i = block >> c.per_page_log2;
+        return table[i < p.batch.table_width ? i : p.batch.table_width - 1];
+    };
+    auto look_up = [&](int it) {
         const int chunk = span.chunk(it);
-        // of the four blocks, the lane reads K from block n / 4 and V from block g
-        const int kb = 4 * chunk + (n >> 2), vb = 4 * chunk + g;
-        int kpage = kb * kBlock < t.len ? page_of(p.batch, c, t.b, kb) : -1;
-        int vpage = vb * kBlock < t.len ? page_of(p.batch, c, t.b, vb) : -1;
-        const int64_t ki = block_index(c, kpage < 0 ? 0 : kpage, head, kb);
-        const int64_t vi = block_index(c, vpage < 0 ? 0 : vpage, head, vb);
-        const uint8_t* kp = c.k + ki * (kBlock * DIM) + (n & 3) * DIM + 16 * g;
-        const uint8_t* vp = c.v + vi * (kBlock * DIM) + n * kBlock;
+        return Where{entry_of(4 * chunk + (n >> 2)), entry_of(4 * chunk + g)};
+    };
+    // the page in an entry for a block, or -1 where the block is not there
+    auto page_in = [&](int entry, int block) {
+        const bool there = (unsigned)entry < (unsigned)c.pages && block * kBlock < t.len &&
+                           block >> c.per_page_log2 < p.batch.table_width;
+        return there ? entry : -1;
+    };
+    struct Bytes {
         quad k[4][DIM / 64], v[kTiles];
+        float kscale, vscale;
+    };
+    auto load_k = [&](int it, const Where& w, Bytes& to) {
+        const int kb = 4 * span.chunk(it) + (n >> 2);
+        const int page = page_in(w.kpage, kb);
+        const uint8_t* kp = c.k + block_index(c, page < 0 ? 0 : page, head, kb) * (kBlock * DIM) +
+                            (n & 3) * DIM + 16 * g;
 #pragma unroll
         for (int tt = 0; tt < 4; ++tt)
 #pragma unroll
             for (int h = 0; h < DIM / 64; ++h)
-                k[tt][h] = *reinterpret_cast<const quad*>(kp + 4 * tt * DIM + 64 * h);
+                to.k[tt][h] = load_once<WS == 4>(kp + 4 * tt * DIM + 64 * h);
+    };
+    auto load_v = [&](int it, const Where& w, Bytes& to) {
+        const int vb = 4 * span.chunk(it) + g;
+        const int page = page_in(w.vpage, vb);
+        const int64_t vi = block_index(c, page < 0 ? 0 : page, head, vb);
+        to.kscale = c.k_scale[vi];
+        to.vscale = c.v_scale[vi];
+        const uint8_t* vp = c.v + vi * (kBlock * DIM) + n * kBlock;
 #pragma unroll
-        for (int u = 0; u < kTiles; ++u) v[u] = *reinterpret_cast<const quad*>(vp + 16 * u * kBlock);
-        const float ks = c.k_scale[vi] * p.scale;
-        float vs = vpage < 0 ? 0.0f : c.v_scale[vi];
+        for (int u = 0; u < kTiles; ++u) to.v[u] = load_once<WS == 4>(vp + 16 * u * kBlock);
+    };
+
+    int it = begin + (WS == 1 ? 0 : wave);
+    Bytes first, second;
+    Where now{-1, -1}, next{-1, -1};
+    if (it < end) {
+        now = look_up(it);
+        load_k(it, now, first);
+        load_v(it, now, first);
+        if (it + WS < end) next = look_up(it + WS);
+    }
+    auto step = [&](Bytes& in, Bytes& ahead) {
+        const bool more = it + WS < end;
+        const Where then = next;
+        if (kAhead && more) {
+            load_k(it + WS, then, ahead);
+            load_v(it + WS, then, ahead);
+            if (it + 2 * WS < end) next = look_up(it + 2 * WS);
+        }
+        const int chunk = span.chunk(it);
+        const int vb = 4 * chunk + g;
         // tokens of block g that are there
-        int there = vpage < 0 ? 0 : t.len - vb * kBlock;
+        const bool held = page_in(now.vpage, vb) >= 0;
+        int there = held ? t.len - vb * kBlock : 0;
         there = there < 0 ? 0 : there > kBlock ? kBlock : there;
         const int lo = chunk * kChunk, hi = lo + kChunk - 1;
         const bool whole = __all(there == kBlock) && hi <= min_pos &&
                            (p.window == 0 || max_pos - lo < p.window || hi < p.sinks);
-        if (!whole) {
+
+        f32x4 s[RT][4];
 #pragma unroll
-            for (int u = 0; u < kTiles; ++u) v[u] = first_bytes(v[u], there);
-        }
-        if (kRelative) {
-            const float top = max_of_groups(vs);
-            if (__any(top > vref)) {
-                const float down = vref / top;
+        for (int tt = 0; tt < 4; ++tt) {
 #pragma unroll
-                for (int i = 0; i < RT; ++i)
+            for (int i = 0; i < RT; ++i) s[i][tt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                    for (int u = 0; u < kTiles; ++u) o[i][u] *= down;
-                vref = top;
+            for (int st = 0; st < kSteps; ++st) {
+                const quad& w = in.k[tt][st >> 1];
+                const quad a = widen8<F, T>(w[2 * (st & 1)], w[2 * (st & 1) + 1]);
+#pragma unroll
+                for (int i = 0; i < RT; ++i) s[i][tt] = gemvdev::mma_16x16x32(T{}, a, q_of(i, st), s[i][tt]);
             }
-            vs = vref > 0.0f ? vs / vref : vs;
+            // (else all of K is widened first, and two row tiles run out of registers)
+            if (RT > 1 && tt == 1) __builtin_amdgcn_sched_barrier(0);
         }
+        if (!kAhead && more) {
+            load_k(it + WS, then, ahead);
+            if (it + 2 * WS < end) next = look_up(it + 2 * WS);
+        }
+        // a block's keys have one scale, so the largest score of the lane's 16
+        // is the largest product times it (a scale is not negative; a negative
+        // softmax scale has been given to Q)
+        const float ks = in.kscale * p.scale;
+        const float vs = held ? in.vscale : 0.0f;
+        const float finite = vs < __builtin_inff() ? vs : 0.0f;
+        const float largest = max_of_groups(finite);
 
         quad pb[RT][2];
+        const auto weigh = [&](auto all_seen) {
+            constexpr bool WHOLE = decltype(all_seen)::value;
 #pragma unroll
-        for (int i = 0; i < RT; ++i) {
-            f32x4 s[4];
+            for (int i = 0; i < RT; ++i) {
+                uint32_t sees = 0xffffu;  // tokens of block g that the lane's row sees
+                float scale = largest;    // (of blocks that the row does not see, none)
+                if constexpr (!WHOLE) {
+                    sees = 0;
 #pragma unroll
-            for (int tt = 0; tt < 4; ++tt) {
-                s[tt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                    for (int off = 0; off < kBlock; ++off) {
+                        const int j = vb * kBlock + off;
+                        if (off < there && j <= pos[i] &&
+                            (p.window == 0 || pos[i] - j < p.window || j < p.sinks))
+                            sees |= 1u << off;
+                    }
 #pragma unroll
-                for (int st = 0; st < kSteps; ++st) {
-                    const quad& w = k[tt][st >> 1];
-                    const quad a = widen8<F, T>(w[2 * (st & 1)], w[2 * (st & 1) + 1]);
-                    s[tt] = gemvdev::mma_16x16x32(T{}, a, q[i][st], s[tt]);
+                    for (int e = 0; e < kBlock; ++e)
+                        if (!(sees >> e & 1)) s[i][e >> 2][e & 3] = -__builtin_inff();
+                    scale = max_of_groups(sees != 0 ? finite : 0.0f);
+                }
+                if (__any(scale > vref[i])) {
+                    const float unit = fmaxf(vref[i], scale);
+                    vinv[i] = unit > 0.0f ? 1.0f / unit : 0.0f;
+                    const float down = vref[i] * vinv[i];
+#pragma unroll
+                    for (int u = 0; u < kTiles; ++u) o[i][u] *= down;
+                    vref[i] = unit;
+                }
+                float top = s[i][0][0];
+#pragma unroll
+                for (int e = 1; e < kBlock; ++e) top = fmaxf(top, s[i][e >> 2][e & 3]);
+                // (a lane that sees nothing has top = -inf; ks = 0 would make that a NaN)
+                top = WHOLE || sees != 0 ? top * ks : -__builtin_inff();
+                top = max_of_groups(top);
+                // the base of the exponents follows the maximum only where that
+                // has grown past it by kSlack: most chunks leave it, and o and l
+                // with it, as they are, and no weight passes 2^kSlack
+                if (__any(top > m[i] + kSlack)) {
+                    const float to = fmaxf(m[i], top);
+                    const float down = __builtin_amdgcn_exp2f(m[i] - finite_base(to));
+                    l[i] *= down;
+#pragma unroll
+                    for (int u = 0; u < kTiles; ++u) o[i][u] *= down;
+                    m[i] = to;
+                }
+                const float base = finite_base(m[i]), by = vs * vinv[i];
+                float sum = 0.0f;
+#pragma unroll
+                for (int e = 0; e < kBlock; ++e) {
+                    float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i][e >> 2][e & 3], ks, -base));
+                    // a hidden token's weight is zero whatever its block's scales
+                    if (!WHOLE && !(sees >> e & 1)) x = 0.0f;
+                    sum += x;
+                    x *= by;
+                    if (!WHOLE && !(sees >> e & 1)) x = 0.0f;
+                    s[i][e >> 2][e & 3] = x;
+                }
+                l[i] += sum;
+#pragma unroll
+                for (int tt = 0; tt < 4; ++tt) {
+                    pb[i][tt >> 1][2 * (tt & 1)] = pack(TF16{}, s[i][tt][0], s[i][tt][1]);
+                    pb[i][tt >> 1][2 * (tt & 1) + 1] = pack(TF16{}, s[i][tt][2], s[i][tt][3]);
                 }
             }
-            // tokens of block g that the lane's row sees
-            uint32_t sees = 0xffffu;
-            if (!whole) {
-                sees = 0;
+        };
+        if (whole)
+            weigh(std::true_type{});
+        else
+            weigh(std::false_type{});
+        if (!whole) {
 #pragma unroll
-                for (int off = 0; off < kBlock; ++off) {
-                    const int j = vb * kBlock + off;
-                    if (off < there && j <= pos[i] &&
-                        (p.window == 0 || pos[i] - j < p.window || j < p.sinks))
-                        sees |= 1u << off;
-                }
-            }
-            float top = -__builtin_inff();
-#pragma unroll
-            for (int tt = 0; tt < 4; ++tt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float x = s[tt][e] * ks;
-                    s[tt][e] = sees >> (4 * tt + e) & 1 ? x : -__builtin_inff();
-                    top = fmaxf(top, s[tt][e]);
-                }
-            top = fmaxf(m[i], max_of_groups(top));
-            // a row that has seen nothing yet keeps its maximum at -inf; its
-            // exponents are taken against 0
-            const float base = top == -__builtin_inff() ? 0.0f : top;
-            if (__any(top != m[i])) {
-                const float down = __builtin_amdgcn_exp2f(m[i] - base);
-                l[i] *= down;
-#pragma unroll
-                for (int u = 0; u < kTiles; ++u) o[i][u] *= down;
-                m[i] = top;
-            }
-#pragma unroll
-            for (int tt = 0; tt < 4; ++tt) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float x = __builtin_amdgcn_exp2f(s[tt][e] - base);
-                    l[i] += x;
-                    // a hidden token's weight is zero whatever its block's scale
-                    s[tt][e] = sees >> (4 * tt + e) & 1 ? x * vs : 0.0f;
-                }
-                pb[i][tt >> 1][2 * (tt & 1)] = pack(T{}, s[tt][0], s[tt][1]);
-                pb[i][tt >> 1][2 * (tt & 1) + 1] = pack(T{}, s[tt][2], s[tt][3]);
-            }
+            for (int u = 0; u < kTiles; ++u) in.v[u] = first_bytes(in.v[u], there);
         }
 #pragma unroll
         for (int u = 0; u < kTiles; ++u) {
-            const quad a0 = widen8<F, T>(v[u][0], v[u][1]), a1 = widen8<F, T>(v[u][2], v[u][3]);
+            const quad a0 = widen8<F, TF16>(in.v[u][0], in.v[u][1]), a1 = widen8<F, TF16>(in.v[u][2], in.v[u][3]);
 #pragma unroll
             for (int i = 0; i < RT; ++i) {
-                o[i][u] = gemvdev::mma_16x16x32(T{}, a0, pb[i][0], o[i][u]);
-                o[i][u] = gemvdev::mma_16x16x32(T{}, a1, pb[i][1], o[i][u]);
+                o[i][u] = gemvdev::mma_16x16x32(TF16{}, a0, pb[i][0], o[i][u]);
+                o[i][u] = gemvdev::mma_16x16x32(TF16{}, a1, pb[i][1], o[i][u]);
             }
         }
+        now = then;
+        it += WS;
+        if (!kAhead && more) load_v(it, now, ahead);
+    };
+    while (it < end) {
+        step(first, kAhead ? second : first);
+        if (!kAhead) continue;
+        if (it >= end) break;
+        step(second, first);
     }
 
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
         l[i] = sum_of_groups(l[i]);
-        if (kRelative)
 #pragma unroll
-            for (int u = 0; u < kTiles; ++u) o[i][u] *= vref;
+        for (int u = 0; u < kTiles; ++u) o[i][u] *= vref[i];
     }
     if constexpr (WS > 1) {
         // wavefronts 2 and 3 join 0 and 1, then 1 joins 0
@@ -586,8 +725,7 @@ __global__ __launch_bounds__(kAttWaves * 64) void kv_attend_kernel(Attend p, int
 #pragma unroll
                 for (int i = 0; i < RT; ++i) {
                     const float m2 = stat[wave][i][0][lane];
-                    const float top = fmaxf(m[i], m2);
-                    const float base = top == -__builtin_inff() ? 0.0f : top;
+                    const float top = fmaxf(m[i], m2), base = finite_base(top);
                     const float a = __builtin_amdgcn_exp2f(m[i] - base);
                     const float b = __builtin_amdgcn_exp2f(m2 - base);
                     m[i] = top;
@@ -617,8 +755,7 @@ __global__ __launch_bounds__(kAttWaves * 64) void kv_attend_kernel(Attend p, int
         }
         return;
     }
-    const Partial out = partial_at<kGroupRows, DIM>(
-        p, places, (place * c.heads + head) * p.splits + split);
+    const Partial out = partial_at<DIM>(p, places, (place * c.heads + head) * p.splits + split);
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
         if (r0 + 16 * i + n > last) continue;
@@ -633,39 +770,67 @@ __global__ __launch_bounds__(kAttWaves * 64) void kv_attend_kernel(Attend p, int
     }
 }
 
-// Joins the splits of each row: a wavefront a row.
-template <class T, int DIM, int R>
-__global__ __launch_bounds__(kAttWaves * 64) void kv_join_kernel(Attend p, int64_t places) {
+// Joins the splits of a row, a workgroup a row (R: rows of a place, RW: of one
+// of its wavefronts): the splits' maxima and sums
+// give each its weight, then the wavefronts add the weighted rows in turn and
+// join in LDS, in a fixed order.
+constexpr int kMaxSplits = 512;
+template <class T, int DIM, int R, int RW>
+__global__ __launch_bounds__(kShareWaves * 64) void kv_join_kernel(Attend p, int64_t places) {
     constexpr int kPer = DIM / 64;
+    __shared__ float weight[kMaxSplits];
+    __shared__ float part[kShareWaves][DIM];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const Cache& c = p.cache;
     const int64_t place = blockIdx.x / c.heads;
     const int head = (int)(blockIdx.x - place * c.heads);
     Tile t;
-    if (!tile_of<R>(p, place, t)) return;
-    for (int r = (int)blockIdx.y * kAttWaves + wave; r < R && t.r0 + r < t.rows; r += kAttWaves * gridDim.y) {
-        float m = -__builtin_inff(), l = 0.0f, o[kPer];
+    const int r = blockIdx.y;
+    if (!tile_of<R>(p, place, t) || t.r0 + r >= t.rows) return;
+    // the splits that its wavefront's rows have (split 0 always leaves its rows)
+    const int r0 = t.r0 + r / RW * RW, last = (r0 + RW < t.rows ? r0 + RW : t.rows) - 1;
+    const int chunks = span_of(p, t.first + r0 / p.group, t.first + last / p.group, t.len).count();
+    const int splits = chunks > p.split_chunks ? (chunks + p.split_chunks - 1) / p.split_chunks : 1;
+    const Partial in = partial_at<DIM>(p, places, (place * c.heads + head) * p.splits);
+    // every wavefront reduces the maxima and sums for itself
+    float top = -__builtin_inff();
+    for (int s = lane; s < splits; s += 64) top = fmaxf(top, in.ml[(s * p.rows + r) * 2]);
+    const float base = finite_base(wave_max(top));
+    float l = 0.0f;
+    for (int s = lane; s < splits; s += 64) {
+        const float ls = in.ml[(s * p.rows + r) * 2 + 1];
+        // a split in which the row sees nothing adds nothing, whatever its row holds
+        const float w = ls == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(in.ml[(s * p.rows + r) * 2] - base);
+        l += ls == 0.0f ? 0.0f : w * ls;
+        if (wave == 0) weight[s] = ls == 0.0f ? -1.0f : w;
+    }
+    l = gemvdev::segment_sum<64>(l);
+    __syncthreads();
+    float o[kPer];
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) o[i] = 0.0f;
-        for (int s = 0; s < p.splits; ++s) {
-            const Partial in = partial_at<R, DIM>(p, places, (place * c.heads + head) * p.splits + s);
-            const float m2 = in.ml[2 * r], l2 = in.ml[2 * r + 1];
-            if (l2 == 0.0f) continue;
-            const float top = fmaxf(m, m2);
-            const float base = top == -__builtin_inff() ? 0.0f : top;
-            const float a = __builtin_amdgcn_exp2f(m - base), b = __builtin_amdgcn_exp2f(m2 - base);
-            m = top;
-            l = l * a + l2 * b;
+    for (int i = 0; i < kPer; ++i) o[i] = 0.0f;
+#pragma unroll 8
+    for (int s = wave; s < splits; s += kShareWaves) {
+        const float w = weight[s];
+        const float* row = in.rows + ((int64_t)s * p.rows + r) * DIM;
 #pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                o[i] = o[i] * a + in.rows[(int64_t)r * DIM + i * 64 + lane] * b;
+        for (int i = 0; i < kPer; ++i) {
+            const float x = row[i * 64 + lane];
+            o[i] += w == -1.0f ? 0.0f : x * w;
         }
-        const float by = l == 0.0f ? 0.0f : 1.0f / l;
-        const int token = (t.r0 + r) / p.group;
-        uint16_t* dst = p.O + ((int64_t)t.start + token) * p.ldo +
-                        (int64_t)(head * p.group + (t.r0 + r - token * p.group)) * DIM;
+    }
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) dst[i * 64 + lane] = fp8dev::narrow(T{}, o[i] * by);
+    for (int i = 0; i < kPer; ++i) part[wave][i * 64 + lane] = o[i];
+    __syncthreads();
+    const float by = l == 0.0f ? 0.0f : 1.0f / l;
+    const int token = (t.r0 + r) / p.group;
+    uint16_t* dst = p.O + ((int64_t)t.start + token) * p.ldo +
+                    (int64_t)(head * p.group + (t.r0 + r - token * p.group)) * DIM;
+    for (int d = threadIdx.x; d < DIM; d += kShareWaves * 64) {
+        float v = part[0][d];
+#pragma unroll
+        for (int w = 1; w < kShareWaves; ++w) v += part[w][d];
+        dst[d] = fp8dev::narrow(T{}, v * by);
     }
 }
 

@@ -163,9 +163,9 @@ class PlainCache:
                     pos, row = pos + take, row + take
 
     def gather(self, batch, b, head):
-        """(len, dim) keys and values of a sequence in 64 bits; tokens of bad
-        pages are absent: (k, v, positions)."""
-        k, v, at = [], [], []
+        """Of a sequence in 64 bits: (keys, values, positions, the values' bytes
+        in the unit of the largest V scale); tokens of bad pages are absent."""
+        k, v, at, units, top = [], [], [], [], 0.0
         for pos in range(0, batch.lens[b], 16):
             i = pos // self.page_size
             page = int(batch.table[b, i]) if i < batch.table.shape[1] else -1
@@ -173,12 +173,14 @@ class PlainCache:
                 continue
             sub, take = pos % self.page_size // 16, min(16, batch.lens[b] - pos)
             k.append(self.block("k", page, head, sub)[:take] * self.k_scale[page, head, sub])
+            units.append(np.abs(self.block("v", page, head, sub)[:take]))
             v.append(self.block("v", page, head, sub)[:take] * self.v_scale[page, head, sub])
+            top = max(top, self.v_scale[page, head, sub])
             at.append(np.arange(pos, pos + take))
         dim = self.k.shape[3]
         if not k:
-            return np.zeros((0, dim)), np.zeros((0, dim)), np.zeros(0, dtype=int)
-        return np.concatenate(k), np.concatenate(v), np.concatenate(at)
+            return np.zeros((0, dim)), np.zeros((0, dim)), np.zeros(0, dtype=int), np.zeros((0, dim))
+        return np.concatenate(k), np.concatenate(v), np.concatenate(at), np.concatenate(units) * top
 
 
 def attend(Q, plain, batch, scale, window=0, sinks=0, dtype=torch.bfloat16):
@@ -186,9 +188,11 @@ def attend(Q, plain, batch, scale, window=0, sinks=0, dtype=torch.bfloat16):
 
     A score is a sum of dim exact products in fp32 (at most dim roundings of
     one step each, and three more for the scales); an error d of the scores
-    moves a weight by a factor within exp(2d).  A weight is rounded to dtype
-    once, its scale and the running maximum's factors round it by a few fp32
-    steps, the sums of n tokens by n more; the result is rounded once."""
+    moves a weight by a factor within exp(2d).  A weight, relative to the largest
+    V scale, is rounded to fp16 once (half a step, 2^-11, or half the smallest
+    step, 2^-25, where it is below fp16's normal range); its scale and the
+    running maximum's factors round it by a few fp32 steps, the sums of n tokens
+    by n more; the result is rounded once."""
     rows, q_heads, dim = Q.shape
     heads = plain.k.shape[1]
     group = q_heads // heads
@@ -197,7 +201,7 @@ def attend(Q, plain, batch, scale, window=0, sinks=0, dtype=torch.bfloat16):
     for b, (n, m) in enumerate(zip(batch.lens, batch.new)):
         r0 = int(batch.starts[b])
         for h in range(heads):
-            k, v, at = plain.gather(batch, b, h)
+            k, v, at, unit = plain.gather(batch, b, h)
             for i in range(m):
                 p = n - m + i
                 sees = at <= p
@@ -205,7 +209,7 @@ def attend(Q, plain, batch, scale, window=0, sinks=0, dtype=torch.bfloat16):
                     sees &= (p - at < window) | (at < sinks)
                 if not sees.any():
                     continue
-                kk, vv = k[sees], v[sees]
+                kk, vv, uu = k[sees], v[sees], unit[sees]
                 for gq in range(h * group, (h + 1) * group):
                     q = Q[r0 + i, gq]
                     s = scale * (kk @ q)
@@ -216,9 +220,8 @@ def attend(Q, plain, batch, scale, window=0, sinks=0, dtype=torch.bfloat16):
                     o = w @ vv
                     out[r0 + i, gq] = o
                     spread = w @ np.abs(vv)
-                    rel = half + 2 * d + (len(s) + 64) * 2.0 ** -23
-                    # a weight below fp16's normal range is off by half its smallest step
-                    low = 2.0 ** -25 * np.abs(vv).sum(0) if dtype == torch.float16 else 0.0
+                    rel = 2.0 ** -11 + 2 * d + (len(s) + 64) * 2.0 ** -23
+                    low = 2.0 ** -25 * uu.sum(0) * w.max()
                     bound[r0 + i, gq] = 1.01 * (rel * spread + low) + half * np.abs(o) + 2.0 ** -24 * np.abs(o).max() + 1e-30
     return out, bound
 

@@ -95,7 +95,7 @@ def test_attend_refusals(fn):
         assert call(**kw) == BAD, kw
     # a batch that is split over its tokens needs its workspace
     n = ctypes.c_size_t()
-    assert lg.gemv_kv_attend_workspace_size(8, 2, 128, 2, 2, 1000, 64, ctypes.byref(n)) == 0 and n.value > 0
+    assert lg.gemv_kv_attend_workspace_size(8, 2, 128, 2, 2, 1, 1000, 64, 0, 0, ctypes.byref(n)) == 0 and n.value > 0
     wide = dict(b=batch(table_width=1000, table_pitch=1000, starts=None), rows=2)
     assert call(**wide, ws=None) == BAD and call(**wide, wsb=n.value - 1) == BAD and call(**wide, ws=P + 8) == BAD
     assert call(rows=0) == 0
@@ -104,12 +104,21 @@ def test_attend_refusals(fn):
 def test_workspace_size():
     n = ctypes.c_size_t(7)
     f = lg.gemv_kv_attend_workspace_size
-    for bad in ((7, 2, 128, 1, 1, 1, 64), (0, 2, 128, 1, 1, 1, 64), (8, 0, 128, 1, 1, 1, 64), (8, 2, 100, 1, 1, 1, 64),
-                (8, 2, 128, -1, 1, 1, 64), (8, 2, 128, 1, -1, 1, 64), (8, 2, 128, 1, 1, -1, 64),
-                (8, 2, 128, 1, 1, 1, 8)):
-        assert f(*bad, ctypes.byref(n)) == BAD, bad
-    assert f(8, 2, 128, 1, 1, 1, 64, None) == BAD
-    assert f(8, 2, 128, 0, 1, 1, 64, ctypes.byref(n)) == 0 and n.value == 0
+    good = dict(q_heads=8, heads=2, dim=128, rows=1, sequences=1, one_each=1, table_width=100, page_size=64, window=0,
+                sinks=0)
+    assert f(*good.values(), ctypes.byref(n)) == 0 and n.value > 0 and n.value % 16 == 0
+    for bad in (dict(q_heads=7), dict(q_heads=0), dict(heads=0), dict(dim=100), dict(rows=-1), dict(sequences=-1),
+                dict(rows=2), dict(table_width=-1), dict(page_size=8), dict(window=-1), dict(sinks=-1)):
+        assert f(*{**good, **bad}.values(), ctypes.byref(n)) == BAD, bad
+    assert f(*good.values(), None) == BAD
+    for none in (dict(rows=0, sequences=0), dict(table_width=0), dict(table_width=8), dict(window=100)):
+        assert f(*{**good, **none}.values(), ctypes.byref(n)) == 0 and n.value == 0, none
+    # a longer table never needs less, and the workspace stays bounded
+    last = 0
+    for width in (1, 10, 100, 1000, 10000, 1 << 25):
+        assert f(*{**good, "table_width": width}.values(), ctypes.byref(n)) == 0 and n.value >= last
+        last = n.value
+    assert last < 1 << 30
 
 
 @pytest.fixture(scope="module")
