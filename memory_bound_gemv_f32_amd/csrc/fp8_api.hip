@@ -122,8 +122,8 @@ gemv_status_t product(const uint8_t* W, int ldw, const float* w_scale, int ldws,
     // also the empty sum, and scales too far apart for the tiles' 32-bit offsets
     if (nvec <= kFewTokens || K == 0 || ldws >= (1 << 26) || ldxs >= (1 << 26)) {
         const int nt = nvec <= 16 ? 1 : 2;
-        const void* fn = nt == 1 ? (const void*)&fp8dev::fp8_few_kernel<O, 1, kFewWaves>
-                                 : (const void*)&fp8dev::fp8_few_kernel<O, 2, kFewWaves>;
+        const void* fn = nt == 1 ? (const void*)&fp8dev::fp8_few_kernel<O, 1, 1, kFewWaves, 4>
+                                 : (const void*)&fp8dev::fp8_few_kernel<O, 2, 1, kFewWaves, 2>;
         constexpr int kMostTokens = 65535 * 32;  // of one launch
         for (int t = 0; t < nvec; t += tokens) {
             tokens = nvec - t < kMostTokens ? nvec - t : kMostTokens;

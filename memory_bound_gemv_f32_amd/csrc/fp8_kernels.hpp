@@ -194,11 +194,6 @@ __device__ __forceinline__ i32x8 load_block(const uint8_t* p, int k, int group, 
     return join(load_bytes(at, n), load_bytes(at + 64, n - 64));
 }
 
-template <class O>
-__device__ __forceinline__ void store_y(void* Y, int64_t i, float v) {
-    static_cast<typename O::storage*>(Y)[i] = narrow(O{}, v);
-}
-
 // Four neighbouring results of a token, from row m on; `vec`: they may be
 // stored at once.
 template <class O>
@@ -216,21 +211,25 @@ __device__ __forceinline__ void store_row4(void* Y, int64_t at, int m, int M, bo
         if (m + e < M) y[e] = narrow(O{}, v[e]);
 }
 
-// 16 rows of W by 16·NT tokens to a workgroup; its wavefronts take the scale
-// blocks in turn and add their sums in LDS, in a fixed order.
-template <class O, int NT, int W>
+// Few tokens: 16·RG rows of W by 16·NT tokens to a workgroup; its wavefronts
+// take the scale blocks in turn, U at a time with all their loads in flight, and
+// add their sums in LDS, in a fixed order.  W, which is read once, goes past the
+// caches.  Bound by W's bytes: see the host's choice of RG for times.
+template <class O, int NT, int RG, int W, int U>
 __global__ __launch_bounds__(W * 64) void fp8_few_kernel(
     const uint8_t* A, int64_t lda, const float* as, int64_t ldas, const uint8_t* X, int64_t ldx,
     const float* xs, int64_t ldxs, const float* bias, void* Y, int64_t ldy, int M, int K, int T, int, int) {
-    __shared__ f32x4 part[W][NT][64];
+    __shared__ f32x4 part[W][RG][NT][64];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const int r = lane & 15, group = lane >> 4;
-    const int row0 = (int)blockIdx.x * 16;
+    const int row0 = (int)blockIdx.x * 16 * RG;
     const int t0 = (int)blockIdx.y * 16 * NT;
     const int blocks = K / kScaleBlock + (K % kScaleBlock != 0);
     // rows and tokens past the end repeat the last one; their results are not stored
-    const int row = row0 + r < M ? row0 + r : M - 1;
-    const uint8_t* a = A + (int64_t)row * lda;
+    const uint8_t* a[RG];
+#pragma unroll
+    for (int i = 0; i < RG; ++i)
+        a[i] = A + (int64_t)(row0 + 16 * i + r < M ? row0 + 16 * i + r : M - 1) * lda;
     const float* asr = as + (int64_t)(row0 / kScaleBlock) * ldas;
     const uint8_t* x[NT];
     const float* xsr[NT];
@@ -240,36 +239,80 @@ __global__ __launch_bounds__(W * 64) void fp8_few_kernel(
         x[i] = X + (int64_t)t * ldx;
         xsr[i] = xs + (int64_t)t * ldxs;
     }
-    f32x4 acc[NT];
+    f32x4 acc[RG][NT];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int b = wave; b < blocks; b += W) {
-        const Wide af = widen32(load_block(a, b * kScaleBlock, group, K));
-        const float s = asr[b];
+    for (int i = 0; i < RG; ++i)
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            const Wide xf = widen32(load_block(x[i], b * kScaleBlock, group, K));
-            const float st = s * xsr[i][b];
-            const f32x4 d = mma_block(af, xf);
+        for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    const auto add = [&](const i32x8 (&af)[RG], const i32x8 (&xf)[NT], float s, const float (&st)[NT]) {
+        Wide xw[NT];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_fmaf(d[j], st, acc[i][j]);
+        for (int j = 0; j < NT; ++j) xw[j] = widen32(xf[j]);
+#pragma unroll
+        for (int i = 0; i < RG; ++i) {
+            const Wide aw = widen32(af[i]);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const f32x4 d = mma_block(aw, xw[j]);
+                const float by = s * st[j];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(d[e], by, acc[i][j][e]);
+            }
         }
+    };
+    const int whole = K / kScaleBlock;  // blocks that have all their columns
+    int b = wave;
+    for (; b + (U - 1) * W < whole; b += U * W) {
+        i32x8 af[U][RG], xf[U][NT];
+        float s[U], st[U][NT];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t k = (int64_t)(b + u * W) * kScaleBlock + 16 * group;
+#pragma unroll
+            for (int i = 0; i < RG; ++i)
+                af[u][i] = join(__builtin_nontemporal_load(reinterpret_cast<const quad_any*>(a[i] + k)),
+                                __builtin_nontemporal_load(reinterpret_cast<const quad_any*>(a[i] + k + 64)));
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                xf[u][j] = join(*reinterpret_cast<const quad_any*>(x[j] + k),
+                                *reinterpret_cast<const quad_any*>(x[j] + k + 64));
+                st[u][j] = xsr[j][b + u * W];
+            }
+            s[u] = asr[b + u * W];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) add(af[u], xf[u], s[u], st[u]);
+    }
+    for (; b < blocks; b += W) {
+        i32x8 af[RG], xf[NT];
+        float st[NT];
+#pragma unroll
+        for (int i = 0; i < RG; ++i) af[i] = load_block(a[i], b * kScaleBlock, group, K);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            xf[j] = load_block(x[j], b * kScaleBlock, group, K);
+            st[j] = xsr[j][b];
+        }
+        add(af, xf, asr[b], st);
     }
 #pragma unroll
-    for (int i = 0; i < NT; ++i) part[wave][i][lane] = acc[i];
+    for (int i = 0; i < RG; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) part[wave][i][j][lane] = acc[i][j];
     __syncthreads();
-    for (int e = threadIdx.x; e < NT * 64; e += W * 64) {
-        const int i = e >> 6, l = e & 63;
-        f32x4 v = part[0][i][l];
+    for (int e = threadIdx.x; e < RG * NT * 64; e += W * 64) {
+        const int i = e / (NT * 64), j = e / 64 % NT, l = e & 63;
+        f32x4 v = part[0][i][j][l];
 #pragma unroll
-        for (int w = 1; w < W; ++w) v += part[w][i][l];
-        const int t = t0 + 16 * i + (l & 15);
-        if (t < T)
+        for (int w = 1; w < W; ++w) v += part[w][i][j][l];
+        const int t = t0 + 16 * j + (l & 15);
+        const int m = row0 + 16 * i + 4 * (l >> 4);
+        if (t < T && m < M) {
+            if (bias)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int m = row0 + 4 * (l >> 4) + j;
-                if (m < M) store_y<O>(Y, (int64_t)t * ldy + m, bias ? v[j] + bias[m] : v[j]);
-            }
+                for (int n = 0; n < 4; ++n) v[n] += bias[m + n < M ? m + n : M - 1];
+            store_row4<O>(Y, (int64_t)t * ldy, m, M, ldy % 4 == 0 && (uintptr_t)Y % (4 * O::bytes) == 0, v);
+        }
     }
 }
 

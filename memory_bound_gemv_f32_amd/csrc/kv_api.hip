@@ -60,7 +60,8 @@ bool make_batch(const gemv_kv_batch_t* in, int rows, kvdev::Batch* out) {
 template <class D, class F>
 gemv_status_t append(int dim, const kvdev::Cache& c, const kvdev::Batch& q, const void* K, int64_t ldk,
                      const void* V, int64_t ldv, hipStream_t stream) {
-    const int64_t places = q.total / GEMV_KV_BLOCK + 2 * (int64_t)q.count;
+    // a token each is one block each
+    const int64_t places = q.starts == nullptr ? q.count : q.total / GEMV_KV_BLOCK + 2 * (int64_t)q.count;
     if (places > 0x7fffffff) return GEMV_ERROR_INVALID_VALUE;
     void* argv[] = {(void*)&c, (void*)&q, (void*)&K, (void*)&ldk, (void*)&V, (void*)&ldv};
     const void* fn = dim == 64    ? (const void*)&kvdev::kv_append_kernel<D, F, 64>

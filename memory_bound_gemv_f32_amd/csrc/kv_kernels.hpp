@@ -81,16 +81,21 @@ __device__ __forceinline__ int64_t block_index(const Cache& c, int page, int hea
 __device__ __forceinline__ int64_t first_place(const Batch& q, int b, int64_t n, int64_t d, int extra) {
     return (int64_t)start_of(q, b) * n / d + (int64_t)extra * b;
 }
+// Every lane of the wavefront takes part: the last 64 candidates are looked at
+// side by side.
 __device__ __forceinline__ int sequence_of(const Batch& q, int64_t place, int64_t n, int64_t d, int extra) {
-    int lo = 0, hi = q.count - 1;  // the last b whose first place is at most `place`
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
+    int lo = 0, hi = q.count;  // the last b in [lo, hi) whose first place is at most `place`
+    while (hi - lo > 64) {
+        const int mid = (lo + hi) >> 1;
         if (first_place(q, mid, n, d, extra) <= place)
             lo = mid;
         else
-            hi = mid - 1;
+            hi = mid;
     }
-    return lo;
+    const int b = lo + (int)(threadIdx.x & 63);
+    const uint64_t before = __ballot(b < hi && first_place(q, b < hi ? b : lo, n, d, extra) <= place);
+    const int found = lo + __popcll(before) - 1;
+    return found < lo ? lo : found;
 }
 
 // ---------------------------------------------------------------------------
@@ -125,23 +130,52 @@ __device__ __forceinline__ uint32_t round8(E4m3, float v) {
     v = fminf(fmaxf(v, -448.0f), 448.0f);
     return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v, v, 0, false) & 0xffu;
 }
+// 16 values over their scale, in the order of their bytes.
+template <class F>
+__device__ __forceinline__ quad pack16(F, const float (&x)[16], float inv) {
+    quad w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = fminf(fmaxf(x[4 * i + e] * inv, -F::qmax), F::qmax);
+        if constexpr (F::qmax == 448.0f) {
+            w[i] = fp8dev::to_e4m3x4(v[0], v[1], v[2], v[3]);
+        } else {
+            w[i] = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[i] |= ((uint32_t)(int)__builtin_rintf(v[e]) & 0xffu) << (8 * e);
+        }
+    }
+    return w;
+}
 __device__ __forceinline__ float value8(Int8, uint32_t byte) { return (float)(int)(int8_t)byte; }
 __device__ __forceinline__ float value8(E4m3, uint32_t byte) {
     return __builtin_amdgcn_cvt_f32_fp8((int)byte, 0);
 }
 
-// 16 elements from p on, `step` apart, of which bit i of `take` says whether
-// element i is there.
-template <class D>
-__device__ __forceinline__ void load16(const typename D::storage* p, int64_t step, uint32_t take,
-                                       float (&v)[16]) {
+// N consecutive elements from p on, widened to fp32.
+template <class D, int N>
+__device__ __forceinline__ void load_run(const typename D::storage* p, float (&v)[N]) {
+    using S = typename D::storage;
+    struct __attribute__((packed, aligned(D::bytes))) Run {
+        S v[N];
+    };
+    const Run r = *reinterpret_cast<const Run*>(p);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = take >> i & 1 ? widen(D{}, p[i * step]) : 0.0f;
+    for (int i = 0; i < N; ++i) v[i] = widen(D{}, r.v[i]);
+}
+
+// The lowest n of 16 bits, n clamped to 0..16.
+__device__ __forceinline__ uint32_t low_bits(int64_t n) {
+    return n <= 0 ? 0u : n >= 16 ? 0xffffu : (1u << (int)n) - 1;
 }
 
 // One wavefront per block of one head's keys or values.  16-byte piece p of
 // the block is 16 dims of a token (K) or the 16 tokens of a dim (V); a lane
-// holds pieces lane, lane + 64, ...
+// holds K's pieces lane, lane + 64, ... and V's pieces of DIM / 64 neighbouring
+// dims, so that both read runs of elements.  The values are asked for before
+// the page, which they do not need.
 template <class D, class F, int DIM>
 __global__ __launch_bounds__(64) void kv_append_kernel(Cache c, Batch q,
                                                        const typename D::storage* K, int64_t ldk,
@@ -151,50 +185,59 @@ __global__ __launch_bounds__(64) void kv_append_kernel(Cache c, Batch q,
     const int head = (int)blockIdx.y;
     const bool values = blockIdx.z != 0;
     const int64_t place = blockIdx.x;
-    const int b = sequence_of(q, place, 1, kBlock, 2);
+    int b;
+    int64_t ahead;  // blocks of the sequence's new tokens before this one
+    if (q.starts == nullptr) {
+        b = (int)place;
+        ahead = 0;
+    } else {
+        b = sequence_of(q, place, 1, kBlock, 2);
+        ahead = place - first_place(q, b, 1, kBlock, 2);
+    }
     const int start = start_of(q, b), stop = start_of(q, b + 1);
     const int len = q.lens[b];
     const int64_t first = (int64_t)len - ((int64_t)stop - start);  // position of the first new token
-    const int64_t block64 = (first > 0 ? first : 0) / kBlock + place - first_place(q, b, 1, kBlock, 2);
-    if (block64 < 0 || block64 * kBlock >= len || stop <= start) return;
-    const int block = (int)block64;
+    const int64_t at = ((first > 0 ? first : 0) / kBlock + ahead) * kBlock;  // ... of the block's token 0
+    if (ahead < 0 || at >= len || stop <= start) return;
+    const int64_t row0 = start + at - first;                       // its row
+    // tokens of the block that stay, and those that this call brings
+    const uint32_t stay = low_bits(first - at);
+    const uint32_t fresh = low_bits(len - at) & ~stay & low_bits(q.total - row0) & ~low_bits(-row0);
+    if (fresh == 0) return;
+    float x[kPieces][16];
+    if (values) {
+        const typename D::storage* p = V + row0 * ldv + (int64_t)head * DIM + lane * kPieces;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float run[kPieces] = {};
+            if (fresh >> i & 1) load_run<D, kPieces>(p + i * ldv, run);
+#pragma unroll
+            for (int j = 0; j < kPieces; ++j) x[j][i] = run[j];
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) {
+            const int piece = lane + 64 * j, token = piece / (DIM / 16), dim = piece % (DIM / 16) * 16;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[j][i] = 0.0f;
+            if (fresh >> token & 1) load_run<D, 16>(K + (row0 + token) * ldk + (int64_t)head * DIM + dim, x[j]);
+        }
+    }
+    const int block = (int)(at / kBlock);
     const int page = page_of(q, c, b, block);
     if (page < 0) return;
     const int64_t index = block_index(c, page, head, block);
     uint8_t* held = (values ? c.v : c.k) + index * (kBlock * DIM);
     float* scale = (values ? c.v_scale : c.k_scale) + index;
-    // tokens of the block that this call brings, and those that stay
-    uint32_t fresh = 0, stay = 0;
-    for (int i = 0; i < kBlock; ++i) {
-        const int64_t pos = (int64_t)block * kBlock + i;
-        const int64_t row = start + pos - first;
-        if (pos < first)
-            stay |= 1u << i;
-        else if (pos < len && row >= 0 && row < q.total)
-            fresh |= 1u << i;
-    }
-    if (fresh == 0) return;
-    const int64_t row0 = start + (int64_t)block * kBlock - first;  // the row of the block's token 0
-    float x[kPieces][16];
+    const float old = stay != 0 ? *scale : 0.0f;
     uint32_t m = 0;
 #pragma unroll
-    for (int j = 0; j < kPieces; ++j) {
-        const int piece = lane + 64 * j;
-        if (values) {
-            const int dim = piece;
-            load16<D>(V + row0 * ldv + (int64_t)head * DIM + dim, ldv, fresh, x[j]);
-        } else {
-            const int token = piece / (DIM / 16), dim = piece % (DIM / 16) * 16;
-            load16<D>(K + (row0 + token) * ldk + (int64_t)head * DIM + dim, 1,
-                      fresh >> token & 1 ? 0xffffu : 0u, x[j]);
-        }
+    for (int j = 0; j < kPieces; ++j)
 #pragma unroll
         for (int i = 0; i < 16; ++i) m = max_u32(m, fp8dev::magnitude(x[j][i]));
-    }
     const float need = block_scale<F>(fp8dev::wave_max(m));
     float s = need, ratio = 1.0f;
     if (stay != 0) {
-        const float old = *scale;
         if (!(old <= need)) s = old;  // the larger, and NaN once either is
         if (need != need) s = need;
         ratio = old / s;
@@ -203,13 +246,17 @@ __global__ __launch_bounds__(64) void kv_append_kernel(Cache c, Batch q,
     const bool bad = s != s;  // the bytes of a block with no scale are zero
 #pragma unroll
     for (int j = 0; j < kPieces; ++j) {
-        const int piece = lane + 64 * j;
+        const int piece = values ? lane * kPieces + j : lane + 64 * j;
         const int token = piece / (DIM / 16);
         const uint32_t put = values ? fresh : (fresh >> token & 1 ? 0xffffu : 0u);
         const uint32_t keep = values ? stay : (stay >> token & 1 ? 0xffffu : 0u);
         if (put == 0 && (keep == 0 || ratio == 1.0f)) continue;
-        quad* at = reinterpret_cast<quad*>(held) + piece;
-        quad w = put == 0xffffu ? quad{0u, 0u, 0u, 0u} : *at;
+        quad* to = reinterpret_cast<quad*>(held) + piece;
+        if (put == 0xffffu && !bad) {
+            *to = pack16(F{}, x[j], inv);
+            continue;
+        }
+        quad w = put == 0xffffu ? quad{0u, 0u, 0u, 0u} : *to;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             const uint32_t was = w[i >> 2] >> (8 * (i & 3)) & 0xffu;
@@ -220,7 +267,7 @@ __global__ __launch_bounds__(64) void kv_append_kernel(Cache c, Batch q,
                 now = bad ? 0u : round8(F{}, value8(F{}, was) * ratio);
             w[i >> 2] = (w[i >> 2] & ~(0xffu << (8 * (i & 3)))) | now << (8 * (i & 3));
         }
-        *at = w;
+        *to = w;
     }
     if (lane == 0) *scale = s;
 }
