@@ -26,49 +26,75 @@ gemv_status_t launch(const void* fn, dim3 grid, int threads, int lds_bytes, void
 
 // ---- the product's mapping ---------------------------------------------------
 
-// Up to so many tokens a workgroup takes 16 rows of W with all the tokens.
-constexpr int kFewTokens = 32;
-constexpr int kFewWaves = 8;
-
-// 128 x 128 tiles move the fewest bytes, 128 x 64 and 64 x 64 give more
-// workgroups, the split gives more wavefronts to a workgroup.  The largest
-// that fills three quarters of the compute units is taken; measured, us at
-// 1024 x 4096 x 4096 (tokens x rows x K): 33 | 32 | 40 | 58; 512 x 4096 x 4096:
-// 31 | 19 | 22 | 28; 250 x 4096 x 11008: 82 | 45 | 35 | 38; 128 x 4096 x 4096:
-// 26 | 18 | 15 | 12.
+using fp8dev::Split;
 using Large = fp8dev::Tile<128, 128, 64, 32, 2, 8>;
 using Medium = fp8dev::Tile<128, 64, 32, 32, 4, 8>;
 using Small = fp8dev::Tile<64, 64, 32, 16, 4, 8>;
-constexpr int64_t kEnoughTiles = 192;
+using Split64 = Split<64, 64, 2>;
+using Split32 = Split<64, 32, 3>;
+using Split16 = Split<64, 16, 3>;
 
-template <class O, class C, bool EXACT>
-const void* tile_fn(bool direct) {
-    return direct ? (const void*)&fp8dev::fp8_tile_kernel<O, C, EXACT, true>
-                  : (const void*)&fp8dev::fp8_tile_kernel<O, C, EXACT, false>;
+constexpr int kFewTokens = 16, kFewRows = 8192, kFewWaves = 16, kFewBlocks = 2;
+constexpr int kExactTokens = 32;  // up to so many, every result takes the exact steps
+constexpr int64_t kUnits = 256, kEnoughTiles = 192;
+
+// A kernel and what its launch needs.
+struct Tiled {
+    const void* fn;
+    int block_m, block_n, threads, lds_bytes;
+};
+
+template <class C>
+Tiled tiled(const void* fn) {
+    return Tiled{fn, C::BM, C::BN, C::kWaves * 64, C::kLds};
 }
 
-template <class O>
-const void* tiled_kernel(int M, int nvec, bool direct, int* block_m, int* block_n, int* threads,
-                         int* lds_bytes) {
+template <class O, class C>
+Tiled tile_kernel(bool direct) {
     // fp32 results take the exact steps: the e4m3 ones' 2^-15 would show
     constexpr bool kExact = O::bytes == 4;
-    const auto use = [&](auto c, const void* fn) {
-        using C = decltype(c);
-        *block_m = C::BM;
-        *block_n = C::BN;
-        *threads = C::kWaves * 64;
-        *lds_bytes = C::kLds;
-        return fn;
-    };
-    const auto tiles = [&](auto c) {
-        using C = decltype(c);
-        return ceil_div(M, C::BM) * ceil_div(nvec, C::BN);
-    };
-    if (tiles(Large{}) >= kEnoughTiles) return use(Large{}, tile_fn<O, Large, kExact>(direct));
-    if (tiles(Medium{}) >= kEnoughTiles) return use(Medium{}, tile_fn<O, Medium, kExact>(direct));
-    if (tiles(Small{}) >= kEnoughTiles) return use(Small{}, tile_fn<O, Small, kExact>(direct));
-    return use(fp8dev::Split{}, direct ? (const void*)&fp8dev::fp8_split_kernel<O, kExact, true>
-                                       : (const void*)&fp8dev::fp8_split_kernel<O, kExact, false>);
+    return tiled<C>(direct ? (const void*)&fp8dev::fp8_tile_kernel<O, C, kExact, true>
+                           : (const void*)&fp8dev::fp8_tile_kernel<O, C, kExact, false>);
+}
+
+template <class O, class C>
+Tiled split_kernel(bool direct, bool exact) {
+    if constexpr (O::bytes == 2)
+        if (!exact)
+            return tiled<C>(direct ? (const void*)&fp8dev::fp8_split_kernel<O, C, false, true>
+                                   : (const void*)&fp8dev::fp8_split_kernel<O, C, false, false>);
+    return tiled<C>(direct ? (const void*)&fp8dev::fp8_split_kernel<O, C, true, true>
+                           : (const void*)&fp8dev::fp8_split_kernel<O, C, true, false>);
+}
+
+template <class C>
+int64_t tiles_of(int M, int nvec) {
+    return ceil_div(M, C::BM) * ceil_div(nvec, C::BN);
+}
+
+// Which tile, for everything but few tokens of few rows.  The split kernels, with
+// the widest token tile that keeps a workgroup to each compute unit at most,
+// win wherever they fit; past that the largest tile that fills three
+// quarters of the units (the larger, the fewer bytes move).  Measured, us at
+// tokens x rows x K (Split16 | Split32 | Split64 | Small | Medium | Large):
+//   16 x 14336 x 4096    15.4 | 15.5 | 18.2 | 16.7 |      |
+//   64 x 4096 x 4096      8.2 |  8.6 | 11.9 | 14.4 |      |
+//   128 x 4096 x 4096    14.7 |  8.7 | 12.0 | 14.5 | 17   | 27
+//   192 x 4096 x 4096    20.9 | 15.6 | 12.3 | 14.6 |      |
+//   250 x 4096 x 11008   78   | 47   | 38.7 | 34.4 | 45   | 82
+//   512 x 4096 x 4096         |      | 28   | 22   | 19   | 31
+//   1024 x 4096 x 4096        |      | 58   | 40   | 36   | 33
+//   4096 x 14336 x 4096       |      | 783  | 460  | 458  | 267
+template <class O>
+Tiled tiled_kernel(int M, int nvec, bool direct) {
+    const bool exact = nvec <= kExactTokens;
+    if (nvec <= kFewTokens || tiles_of<Split16>(M, nvec) <= kUnits)
+        return split_kernel<O, Split16>(direct, exact);
+    if (nvec <= 32 || tiles_of<Split32>(M, nvec) <= kUnits) return split_kernel<O, Split32>(direct, exact);
+    if (tiles_of<Large>(M, nvec) >= kEnoughTiles) return tile_kernel<O, Large>(direct);
+    if (tiles_of<Medium>(M, nvec) >= kEnoughTiles) return tile_kernel<O, Medium>(direct);
+    if (tiles_of<Small>(M, nvec) >= kEnoughTiles) return tile_kernel<O, Small>(direct);
+    return split_kernel<O, Split64>(direct, O::bytes == 4);
 }
 
 template <class D>
@@ -119,16 +145,18 @@ gemv_status_t product(const uint8_t* W, int ldw, const float* w_scale, int ldws,
     int row_tiles = 0, tokens = nvec;
     void* argv[] = {&W,     &ldw64, &w_scale, &ldws64, &X, &ldx64,  &x_scale,   &ldxs64,
                     &bias,  &Y,     &ldy64,   &M,      &K, &tokens, &row_tiles, &whole_pieces};
-    // also the empty sum, and scales too far apart for the tiles' 32-bit offsets
-    if (nvec <= kFewTokens || K == 0 || ldws >= (1 << 26) || ldxs >= (1 << 26)) {
-        const int nt = nvec <= 16 ? 1 : 2;
-        const void* fn = nt == 1 ? (const void*)&fp8dev::fp8_few_kernel<O, 1, 1, kFewWaves, 4>
-                                 : (const void*)&fp8dev::fp8_few_kernel<O, 2, 1, kFewWaves, 2>;
-        constexpr int kMostTokens = 65535 * 32;  // of one launch
+    // few tokens of few rows: a workgroup for each 16 rows reads W straight into
+    // registers (16 x 4096 x 4096: 7.6 us against 7.9 in LDS; 16 x 8192 x 4096: 13.2
+    // against 12.0).  Also the empty sum, and scales too far apart for the
+    // tiles' 32-bit offsets.
+    if ((nvec <= kFewTokens && M < kFewRows) || K == 0 || ldws >= (1 << 26) || ldxs >= (1 << 26)) {
+        constexpr int kMostTokens = 65535 * 16;  // of one launch
         for (int t = 0; t < nvec; t += tokens) {
             tokens = nvec - t < kMostTokens ? nvec - t : kMostTokens;
-            const dim3 grid((unsigned)ceil_div(M, 16), (unsigned)ceil_div(tokens, 16 * nt));
-            const gemv_status_t st = launch(fn, grid, kFewWaves * 64, 0, argv, stream);
+            const dim3 grid((unsigned)ceil_div(M, 16), (unsigned)ceil_div(tokens, 16));
+            const gemv_status_t st =
+                launch((const void*)&fp8dev::fp8_few_kernel<O, kFewWaves, kFewBlocks>, grid, kFewWaves * 64, 0,
+                       argv, stream);
             if (st != GEMV_SUCCESS) return st;
             if (K > 0) {
                 X += tokens * ldx64;
@@ -138,13 +166,11 @@ gemv_status_t product(const uint8_t* W, int ldw, const float* w_scale, int ldws,
         }
         return GEMV_SUCCESS;
     }
-    const bool direct = whole_pieces && K % GEMV_FP8_BLOCK == 0;
-    int block_m, block_n, threads, lds_bytes;
-    const void* fn = tiled_kernel<O>(M, nvec, direct, &block_m, &block_n, &threads, &lds_bytes);
-    row_tiles = (int)ceil_div(M, block_m);
-    const int64_t grid = row_tiles * ceil_div(nvec, block_n);
+    const Tiled k = tiled_kernel<O>(M, nvec, whole_pieces && K % GEMV_FP8_BLOCK == 0);
+    row_tiles = (int)ceil_div(M, k.block_m);
+    const int64_t grid = row_tiles * ceil_div(nvec, k.block_n);
     if (grid > 0x7fffffff) return GEMV_ERROR_INVALID_VALUE;
-    return launch(fn, dim3((unsigned)grid), threads, lds_bytes, argv, stream);
+    return launch(k.fn, dim3((unsigned)grid), k.threads, k.lds_bytes, argv, stream);
 }
 
 }  // namespace

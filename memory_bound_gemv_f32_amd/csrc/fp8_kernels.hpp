@@ -211,109 +211,62 @@ __device__ __forceinline__ void store_row4(void* Y, int64_t at, int m, int M, bo
         if (m + e < M) y[e] = narrow(O{}, v[e]);
 }
 
-// Few tokens: 16·RG rows of W by 16·NT tokens to a workgroup; its wavefronts
-// take the scale blocks in turn, U at a time with all their loads in flight, and
-// add their sums in LDS, in a fixed order.  W, which is read once, goes past the
-// caches.  Bound by W's bytes: see the host's choice of RG for times.
-template <class O, int NT, int RG, int W, int U>
+// Few tokens of few rows: 16 rows of W by 16 tokens to a workgroup; its
+// wavefronts take the scale blocks in turn, U at a time with all their loads in
+// flight, and add their sums in LDS, in a fixed order.  W, which is read once,
+// goes past the caches.  Bound by latency: 1 x 1024 x 4096 takes 5.4 us, of
+// which W's 4 MiB are 0.9; 1 x 4096 x 4096 5.8, 16 x 4096 x 4096 7.6.
+template <class O, int W, int U>
 __global__ __launch_bounds__(W * 64) void fp8_few_kernel(
     const uint8_t* A, int64_t lda, const float* as, int64_t ldas, const uint8_t* X, int64_t ldx,
     const float* xs, int64_t ldxs, const float* bias, void* Y, int64_t ldy, int M, int K, int T, int, int) {
-    __shared__ f32x4 part[W][RG][NT][64];
+    __shared__ f32x4 part[W][64];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const int r = lane & 15, group = lane >> 4;
-    const int row0 = (int)blockIdx.x * 16 * RG;
-    const int t0 = (int)blockIdx.y * 16 * NT;
+    const int row0 = (int)blockIdx.x * 16, t0 = (int)blockIdx.y * 16;
     const int blocks = K / kScaleBlock + (K % kScaleBlock != 0);
-    // rows and tokens past the end repeat the last one; their results are not stored
-    const uint8_t* a[RG];
-#pragma unroll
-    for (int i = 0; i < RG; ++i)
-        a[i] = A + (int64_t)(row0 + 16 * i + r < M ? row0 + 16 * i + r : M - 1) * lda;
-    const float* asr = as + (int64_t)(row0 / kScaleBlock) * ldas;
-    const uint8_t* x[NT];
-    const float* xsr[NT];
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-        const int t = t0 + 16 * i + r < T ? t0 + 16 * i + r : T - 1;
-        x[i] = X + (int64_t)t * ldx;
-        xsr[i] = xs + (int64_t)t * ldxs;
-    }
-    f32x4 acc[RG][NT];
-#pragma unroll
-    for (int i = 0; i < RG; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    const auto add = [&](const i32x8 (&af)[RG], const i32x8 (&xf)[NT], float s, const float (&st)[NT]) {
-        Wide xw[NT];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) xw[j] = widen32(xf[j]);
-#pragma unroll
-        for (int i = 0; i < RG; ++i) {
-            const Wide aw = widen32(af[i]);
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const f32x4 d = mma_block(aw, xw[j]);
-                const float by = s * st[j];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(d[e], by, acc[i][j][e]);
-            }
-        }
-    };
     const int whole = K / kScaleBlock;  // blocks that have all their columns
+    // rows and tokens past the end repeat the last one; their results are not stored
+    const uint8_t* a = A + (int64_t)(row0 + r < M ? row0 + r : M - 1) * lda;
+    const float* asr = as + (int64_t)(row0 / kScaleBlock) * ldas;
+    const int64_t token = t0 + r < T ? t0 + r : T - 1;
+    const uint8_t* x = X + token * ldx;
+    const float* xsr = xs + token * ldxs;
+    f32x4 acc{0.0f, 0.0f, 0.0f, 0.0f};
+    const auto add = [&](i32x8 af, i32x8 xf, float by) {
+        const f32x4 d = mma_block(widen32(af), widen32(xf));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(d[e], by, acc[e]);
+    };
     int b = wave;
     for (; b + (U - 1) * W < whole; b += U * W) {
-        i32x8 af[U][RG], xf[U][NT];
-        float s[U], st[U][NT];
+        i32x8 af[U], xf[U];
+        float s[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t k = (int64_t)(b + u * W) * kScaleBlock + 16 * group;
-#pragma unroll
-            for (int i = 0; i < RG; ++i)
-                af[u][i] = join(__builtin_nontemporal_load(reinterpret_cast<const quad_any*>(a[i] + k)),
-                                __builtin_nontemporal_load(reinterpret_cast<const quad_any*>(a[i] + k + 64)));
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                xf[u][j] = join(*reinterpret_cast<const quad_any*>(x[j] + k),
-                                *reinterpret_cast<const quad_any*>(x[j] + k + 64));
-                st[u][j] = xsr[j][b + u * W];
-            }
-            s[u] = asr[b + u * W];
+            af[u] = join(__builtin_nontemporal_load(reinterpret_cast<const quad_any*>(a + k)),
+                         __builtin_nontemporal_load(reinterpret_cast<const quad_any*>(a + k + 64)));
+            xf[u] = join(*reinterpret_cast<const quad_any*>(x + k), *reinterpret_cast<const quad_any*>(x + k + 64));
+            s[u] = asr[b + u * W] * xsr[b + u * W];
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u) add(af[u], xf[u], s[u], st[u]);
+        for (int u = 0; u < U; ++u) add(af[u], xf[u], s[u]);
     }
-    for (; b < blocks; b += W) {
-        i32x8 af[RG], xf[NT];
-        float st[NT];
-#pragma unroll
-        for (int i = 0; i < RG; ++i) af[i] = load_block(a[i], b * kScaleBlock, group, K);
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            xf[j] = load_block(x[j], b * kScaleBlock, group, K);
-            st[j] = xsr[j][b];
-        }
-        add(af, xf, asr[b], st);
-    }
-#pragma unroll
-    for (int i = 0; i < RG; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) part[wave][i][j][lane] = acc[i][j];
+    for (; b < blocks; b += W)
+        add(load_block(a, b * kScaleBlock, group, K), load_block(x, b * kScaleBlock, group, K), asr[b] * xsr[b]);
+    part[wave][lane] = acc;
     __syncthreads();
-    for (int e = threadIdx.x; e < RG * NT * 64; e += W * 64) {
-        const int i = e / (NT * 64), j = e / 64 % NT, l = e & 63;
-        f32x4 v = part[0][i][j][l];
+    if (threadIdx.x >= 64) return;
+    f32x4 v = part[0][lane];
 #pragma unroll
-        for (int w = 1; w < W; ++w) v += part[w][i][j][l];
-        const int t = t0 + 16 * j + (l & 15);
-        const int m = row0 + 16 * i + 4 * (l >> 4);
-        if (t < T && m < M) {
-            if (bias)
+    for (int w = 1; w < W; ++w) v += part[w][lane];
+    const int m = row0 + 4 * group;
+    if (t0 + r >= T || m >= M) return;
+    if (bias)
 #pragma unroll
-                for (int n = 0; n < 4; ++n) v[n] += bias[m + n < M ? m + n : M - 1];
-            store_row4<O>(Y, (int64_t)t * ldy, m, M, ldy % 4 == 0 && (uintptr_t)Y % (4 * O::bytes) == 0, v);
-        }
-    }
+        for (int n = 0; n < 4; ++n) v[n] += bias[m + n < M ? m + n : M - 1];
+    store_row4<O>(Y, (int64_t)(t0 + r) * ldy, m, M, ldy % 4 == 0 && (uintptr_t)Y % (4 * O::bytes) == 0, v);
 }
 
 // ---------------------------------------------------------------------------
@@ -652,32 +605,42 @@ __global__ __launch_bounds__(C::kWaves * 64, DIRECT ? C::kOccupancy : 2) void fp
 }
 
 // ---------------------------------------------------------------------------
-// product over some tens to hundreds of tokens: K split within the workgroup
+// product with few tiles: K split within the workgroup
 //
-// With few tiles a compute unit has one workgroup and a step is bound by its
-// latencies, not by its work; so four groups of four wavefronts take four
-// scale blocks of the same 64 rows by 64 tokens in one step, a fourth of the
-// steps, and join their sums in LDS, in a fixed order.
+// With few tiles, or few tokens, a compute unit has one workgroup and a step is
+// bound by its latencies, not by its work; so four groups of four wavefronts
+// take four scale blocks of the same BM rows by BN tokens in one step, a fourth
+// of the steps, STAGES - 1 steps of bytes are in flight, and the groups join their
+// sums in LDS, in a fixed order.
 // ---------------------------------------------------------------------------
+template <int BM_, int BN_, int STAGES_>
 struct Split {
-    static constexpr int BM = 64, BN = 64, KS = 4, kWaves = 4 * KS;
+    static constexpr int BM = BM_, BN = BN_, STAGES = STAGES_, KS = 4, kWaves = 4 * KS;
+    static constexpr int kAcross = BN >= 64 ? 2 : 1;              // wavefronts of a group across the tokens
+    static constexpr int NM = BM / 16 / (4 / kAcross), NN = BN / 16 / kAcross;
     static constexpr int kBlockBytes = (BM + BN) * kScaleBlock;   // of one group
-    static constexpr int kLoads = (BM + BN) / 8 / 4;              // 1 KiB loads of a wavefront per step
+    // 1 KiB loads of a wavefront per step: of W, and of X (where those are
+    // fewer than the wavefronts, the spare ones repeat the last)
+    static constexpr int kLoadsW = BM / 32, kLoadsX = (BN / 8 + 3) / 4;
     // scales of a step: a line of KS blocks for each token, then one for the rows
     static constexpr int kScaleLoads = BN / 16 + 1;
     static constexpr int kStageBytes = KS * kBlockBytes + kScaleLoads * 256;
-    static constexpr int kLds = 2 * kStageBytes;
+    static constexpr int kInFlight = (STAGES - 2) * (kLoadsW + kLoadsX + 1);
+    static constexpr int kPitch = BM + 4;                         // of a token's sums, in fp32
+    static constexpr int kLds = STAGES * kStageBytes;
+    static_assert(BM % 64 == 0 && BN % 16 == 0 && kScaleLoads <= kWaves, "whole loads");
+    static_assert(KS * BN * kPitch * 4 <= kLds && kLds <= 160 * 1024, "the sums fit the stages");
 };
 
-template <class O, bool EXACT, bool DIRECT>
-__global__ __launch_bounds__(Split::kWaves * 64) void fp8_split_kernel(
+template <class O, class C, bool EXACT, bool DIRECT>
+__global__ __launch_bounds__(C::kWaves * 64) void fp8_split_kernel(
     const uint8_t* A, int64_t lda, const float* as, int64_t ldas, const uint8_t* X, int64_t ldx,
     const float* xs, int64_t ldxs, const float* bias, void* Y, int64_t ldy, int M, int K, int T,
     int row_tiles, int whole_pieces) {
-    using C = Split;
     extern __shared__ __align__(16) uint8_t lds[];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const int ks = wave >> 2, wm = (wave & 1) * 32, wn = (wave >> 1 & 1) * 32;
+    const int ks = wave >> 2, member = wave & 3;
+    const int wm = member / C::kAcross * 16 * C::NM, wn = member % C::kAcross * 16 * C::NN;
     const int r = lane & 15, g = lane >> 4;
     // neighbours of a chiplet take the same rows of W with all the tokens
     const int tiles = gridDim.x, per = tiles / 8, id = blockIdx.x;
@@ -687,13 +650,20 @@ __global__ __launch_bounds__(Split::kWaves * 64) void fp8_split_kernel(
     const int blocks = K / kScaleBlock + (K % kScaleBlock != 0);
     const int direct = DIRECT ? blocks : whole_pieces ? K / kScaleBlock : 0;
 
+    // what the wavefront loads of each step: 8 rows at a time, of W, then of X
+    constexpr int kLoads = C::kLoadsW + C::kLoadsX;
     const int in = lane >> 3, piece = 16 * ((lane & 7) ^ in);
-    const uint8_t* base[C::kLoads];
-    uint32_t offset[C::kLoads];
+    const auto first_row = [&](int i) {  // of load i, among the BM + BN
+        if (i < C::kLoadsW) return (member + i * 4) * 8;
+        const int n = member + (i - C::kLoadsW) * 4;
+        return C::BM + (n < C::BN / 8 ? n : C::BN / 8 - 1) * 8;
+    };
+    const uint8_t* base[kLoads];
+    uint32_t offset[kLoads];
 #pragma unroll
-    for (int i = 0; i < C::kLoads; ++i) {
-        const int row = ((wave & 3) + i * 4) * 8;
-        const bool of_w = row < C::BM;
+    for (int i = 0; i < kLoads; ++i) {
+        const int row = first_row(i);
+        const bool of_w = i < C::kLoadsW;
         const int last = of_w ? M - 1 : T - 1;
         int first = of_w ? row0 + row : t0 + row - C::BM;
         first = first < last ? first : last;
@@ -708,98 +678,106 @@ __global__ __launch_bounds__(Split::kWaves * 64) void fp8_split_kernel(
         const int last = of_x ? T - 1 : (M - 1) / kScaleBlock;
         int first = of_x ? t0 + sn * 16 : row0 / kScaleBlock;
         first = first < last ? first : last;
-        const int line = of_x ? lane >> 2 : 0;
+        const int line = lane >> 2;
         sbase = of_x ? xs + (int64_t)first * ldxs : as + (int64_t)first * ldas;
         soffset = (uint32_t)(line < last - first ? line : last - first) * (uint32_t)(of_x ? ldxs : ldas);
     }
     const uint32_t lds_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
-    auto stage = [&](int n) {
-        const int b0 = n * C::KS;
-        const int half = (n & 1) * C::kStageBytes, mine = half + ks * C::kBlockBytes;
-        const int b = b0 + ks;
-        if (b < direct) {
+    // Past the last block the last is loaded again, into places that nothing
+    // reads: every wavefront always waits for the same count.
+    auto stage = [&](int n, int to) {
+        const int at = to * C::kStageBytes, mine = at + ks * C::kBlockBytes;
+        int b = n * C::KS + ks;
+        b = b < blocks ? b : blocks - 1;
+        if (DIRECT || b < direct) {
 #pragma unroll
-            for (int i = 0; i < C::kLoads; ++i)
-                lds_load16(base[i] + (int64_t)b * kScaleBlock, offset[i],
-                           lds_at + mine + ((wave & 3) + i * 4) * 1024);
-        } else if (!DIRECT && b < blocks) {
+            for (int i = 0; i < kLoads; ++i)
+                lds_load16(base[i] + (int64_t)b * kScaleBlock, offset[i], lds_at + mine + first_row(i) * kScaleBlock);
+        } else {
 #pragma unroll 1
-            for (int i = 0; i < C::kLoads; ++i) {
-                const int row = ((wave & 3) + i * 4) * 8 + in;
-                const bool of_w = row < C::BM;
+            for (int i = 0; i < kLoads; ++i) {
+                const int row = first_row(i) + in;
+                const bool of_w = i < C::kLoadsW;
                 const int want = of_w ? row0 + row : t0 + row - C::BM, last = of_w ? M - 1 : T - 1;
                 const int64_t line = want < last ? want : last;
-                *reinterpret_cast<quad*>(lds + mine + ((wave & 3) + i * 4) * 1024 + lane * 16) =
+                *reinterpret_cast<quad*>(lds + mine + first_row(i) * kScaleBlock + lane * 16) =
                     piece_of(of_w ? A + line * lda : X + line * ldx, (int64_t)b * kScaleBlock + piece, K);
             }
             wait_lds();
+            wait_loads<0>();  // this step adds less than the waits count
         }
-        const int sb = b0 + (lane & 3);
+        const int sb = n * C::KS + (lane & 3);
         lds_load4(sbase, (soffset + (sb < blocks ? sb : blocks - 1)) * 4,
-                  lds_at + half + C::KS * C::kBlockBytes + sn * 256);
+                  lds_at + at + C::KS * C::kBlockBytes + sn * 256);
     };
 
-    f32x4 acc[2][2];
+    f32x4 acc[C::NM][C::NN];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < C::NM; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int j = 0; j < C::NN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     const int lo = r * kScaleBlock + 16 * (g ^ (r & 7));
     const int hi = r * kScaleBlock + 16 * ((g + 4) ^ (r & 7));
     const int steps = (blocks + C::KS - 1) / C::KS;
-    if (steps > 0) stage(0);
-    for (int n = 0; n < steps; ++n) {
-        wait_loads<0>();
-        change_over();
-        if (n + 1 < steps) stage(n + 1);
-        if (n * C::KS + ks >= blocks) continue;  // (the barriers are at the loop's head)
-        const uint8_t* half = lds + (n & 1) * C::kStageBytes;
-        const uint8_t* a = half + ks * C::kBlockBytes + wm * kScaleBlock;
-        const uint8_t* x = half + ks * C::kBlockBytes + (C::BM + wn) * kScaleBlock;
-        const float* s = reinterpret_cast<const float*>(half + C::KS * C::kBlockBytes);
-        Operand<EXACT> xo[2];
-        float st[2];
-        const float sa = s[C::BN * C::KS + ks];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+    for (int n = 0; n < C::STAGES - 1; ++n) stage(n, n);
+    int now = 0, next = C::STAGES - 1;
+    for (int n = 0; n < steps; ++n) {
+        wait_loads<C::kInFlight>();
+        change_over();
+        stage(n + C::STAGES - 1, next);
+        const uint8_t* at = lds + now * C::kStageBytes;
+        next = now;
+        now = now + 1 == C::STAGES ? 0 : now + 1;
+        if (n * C::KS + ks >= blocks) continue;  // (the barriers are at the loop's head)
+        const uint8_t* a = at + ks * C::kBlockBytes + wm * kScaleBlock;
+        const uint8_t* x = at + ks * C::kBlockBytes + (C::BM + wn) * kScaleBlock;
+        const float* s = reinterpret_cast<const float*>(at + C::KS * C::kBlockBytes);
+        Operand<EXACT> xo[C::NN];
+        float st[C::NN];
+        const float sa = s[(C::BN + wm / kScaleBlock) * C::KS + ks];
+#pragma unroll
+        for (int j = 0; j < C::NN; ++j) {
             xo[j] = Operand<EXACT>::of(join(*reinterpret_cast<const quad*>(x + 16 * j * kScaleBlock + lo),
                                             *reinterpret_cast<const quad*>(x + 16 * j * kScaleBlock + hi)));
             st[j] = sa * s[(wn + 16 * j + r) * C::KS + ks];
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < C::NM; ++i) {
             const Operand<EXACT> ao =
                 Operand<EXACT>::of(join(*reinterpret_cast<const quad*>(a + 16 * i * kScaleBlock + lo),
                                         *reinterpret_cast<const quad*>(a + 16 * i * kScaleBlock + hi)));
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
+            for (int j = 0; j < C::NN; ++j) {
                 const f32x4 d = block_sum(ao, xo[j]);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(d[e], st[j], acc[i][j][e]);
             }
         }
     }
+    wait_loads<0>();
     change_over();
-    // join: a token's 64 values in a line, the groups' one behind the other
-    constexpr int kPitch = C::BM + 4;
+    // join: a token's BM values in a line, the groups' one behind the other
     float* sums = reinterpret_cast<float*>(lds);
-    static_assert(C::KS * C::BN * kPitch * 4 <= C::kLds, "the sums fit the stages");
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < C::NM; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-            *reinterpret_cast<f32x4*>(sums + (ks * C::BN + wn + 16 * j + r) * kPitch + wm + 16 * i + 4 * g) = acc[i][j];
+        for (int j = 0; j < C::NN; ++j)
+            *reinterpret_cast<f32x4*>(sums + (ks * C::BN + wn + 16 * j + r) * C::kPitch + wm + 16 * i + 4 * g) = acc[i][j];
     __syncthreads();
-    const int t = threadIdx.x >> 4, m = (threadIdx.x & 15) * 4;
-    f32x4 v = *reinterpret_cast<const f32x4*>(sums + t * kPitch + m);
-#pragma unroll
-    for (int k = 1; k < C::KS; ++k) v += *reinterpret_cast<const f32x4*>(sums + (k * C::BN + t) * kPitch + m);
-    if (t0 + t >= T || row0 + m >= M) return;
-    if (bias)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] += bias[row0 + m + e < M ? row0 + m + e : M - 1];
     const bool vec = ldy % 4 == 0 && (uintptr_t)Y % (4 * O::bytes) == 0;
-    store_row4<O>(Y, (int64_t)(t0 + t) * ldy, row0 + m, M, vec, v);
+    constexpr int kLine = C::BM / 4;  // lanes of a token
+    for (int e = threadIdx.x; e < C::BN * kLine; e += C::kWaves * 64) {
+        const int t = e / kLine, m = e % kLine * 4;
+        if (t0 + t >= T || row0 + m >= M) continue;
+        f32x4 v = *reinterpret_cast<const f32x4*>(sums + t * C::kPitch + m);
+#pragma unroll
+        for (int k = 1; k < C::KS; ++k) v += *reinterpret_cast<const f32x4*>(sums + (k * C::BN + t) * C::kPitch + m);
+        if (bias)
+#pragma unroll
+            for (int n = 0; n < 4; ++n) v[n] += bias[row0 + m + n < M ? row0 + m + n : M - 1];
+        store_row4<O>(Y, (int64_t)(t0 + t) * ldy, row0 + m, M, vec, v);
+    }
 }
 
 }  // namespace fp8dev

@@ -131,7 +131,8 @@ def test_product(tokens, M, K, out):
 
 
 @pytest.mark.parametrize("out", TYPES)
-@pytest.mark.parametrize("tokens,M", [(1, 270), (20, 270), (40, 270), (150, 270), (400, 4100), (900, 1000), (1030, 3100)])
+@pytest.mark.parametrize("tokens,M", [(1, 270), (20, 270), (40, 270), (150, 270), (400, 4100), (900, 1000), (1030, 3100),
+                                      (5, 8200), (18, 17000), (40, 17000), (90, 4200), (200, 2050)])
 def test_product_exact_integers(tokens, M, out):
     """Small whole numbers and scales of powers of two: every sum is exact, on
     every path (products of 1 to 16 lie within the matrix cores' 13 bits), and
