@@ -138,13 +138,13 @@ gemv_status_t product(const uint8_t* W, int ldw, const float* w_scale, int ldws,
     if (K > 0 && (W == nullptr || X == nullptr || w_scale == nullptr || x_scale == nullptr))
         return GEMV_ERROR_INVALID_VALUE;
     int64_t ldw64 = ldw, ldws64 = ldws, ldx64 = ldx, ldxs64 = ldxs, ldy64 = ldy;
-    // pieces of 16 bytes that may be loaded straight into LDS (with 32-bit
-    // offsets within 8 rows)
-    int whole_pieces = ldw % 16 == 0 && ldx % 16 == 0 && aligned(W, 16) && aligned(X, 16) &&
-                       ldw < (1 << 28) && ldx < (1 << 28);
+    // whole blocks of aligned 16-byte pieces may be loaded straight into LDS
+    // (with 32-bit offsets within 8 rows)
+    const bool direct = K % GEMV_FP8_BLOCK == 0 && ldw % 16 == 0 && ldx % 16 == 0 && aligned(W, 16) &&
+                        aligned(X, 16) && ldw < (1 << 28) && ldx < (1 << 28);
     int row_tiles = 0, tokens = nvec;
-    void* argv[] = {&W,     &ldw64, &w_scale, &ldws64, &X, &ldx64,  &x_scale,   &ldxs64,
-                    &bias,  &Y,     &ldy64,   &M,      &K, &tokens, &row_tiles, &whole_pieces};
+    void* argv[] = {&W,    &ldw64, &w_scale, &ldws64, &X, &ldx64,  &x_scale, &ldxs64,
+                    &bias, &Y,     &ldy64,   &M,      &K, &tokens, &row_tiles};
     // few tokens of few rows: a workgroup for each 16 rows reads W straight into
     // registers (16 x 4096 x 4096: 7.6 us against 7.9 in LDS; 16 x 8192 x 4096: 13.2
     // against 12.0).  Also the empty sum, and scales too far apart for the
@@ -166,7 +166,7 @@ gemv_status_t product(const uint8_t* W, int ldw, const float* w_scale, int ldws,
         }
         return GEMV_SUCCESS;
     }
-    const Tiled k = tiled_kernel<O>(M, nvec, whole_pieces && K % GEMV_FP8_BLOCK == 0);
+    const Tiled k = tiled_kernel<O>(M, nvec, direct);
     row_tiles = (int)ceil_div(M, k.block_m);
     const int64_t grid = row_tiles * ceil_div(nvec, k.block_n);
     if (grid > 0x7fffffff) return GEMV_ERROR_INVALID_VALUE;

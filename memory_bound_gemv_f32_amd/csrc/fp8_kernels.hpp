@@ -219,7 +219,7 @@ __device__ __forceinline__ void store_row4(void* Y, int64_t at, int m, int M, bo
 template <class O, int W, int U>
 __global__ __launch_bounds__(W * 64) void fp8_few_kernel(
     const uint8_t* A, int64_t lda, const float* as, int64_t ldas, const uint8_t* X, int64_t ldx,
-    const float* xs, int64_t ldxs, const float* bias, void* Y, int64_t ldy, int M, int K, int T, int, int) {
+    const float* xs, int64_t ldxs, const float* bias, void* Y, int64_t ldy, int M, int K, int T, int) {
     __shared__ f32x4 part[W][64];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const int r = lane & 15, group = lane >> 4;
@@ -344,10 +344,13 @@ __device__ __forceinline__ f32x4 block_sum(const Operand<false>& a, const Operan
     return mma_16x16x128(a.v, b.v);
 }
 
-// The 16-byte piece at byte `at` of a row of K bytes; what lies behind the row
-// reads as zero.
-__device__ __forceinline__ quad piece_of(const uint8_t* row, int64_t at, int K) {
-    return at < K ? load_bytes(row + at, (int)(K - at < 16 ? K - at : 16)) : quad{0u, 0u, 0u, 0u};
+// The 16-byte piece at byte `piece` of block b of a row of K bytes, from any
+// address; what lies behind the row reads as zero.
+__device__ __forceinline__ quad piece_of(const uint8_t* row, int b, int piece, int K) {
+    const uint8_t* at = row + (int64_t)b * kScaleBlock + piece;
+    const int left = K - b * kScaleBlock;  // uniform: of the row, from the block on
+    if (left >= kScaleBlock) return *reinterpret_cast<const quad_any*>(at);
+    return load_bytes(at, left - piece);
 }
 
 template <int BM_, int BN_, int WM_, int WN_, int STAGES_, int GROUP_>
@@ -375,7 +378,7 @@ template <class O, class C, bool EXACT, bool DIRECT>
 __global__ __launch_bounds__(C::kWaves * 64, DIRECT ? C::kOccupancy : 2) void fp8_tile_kernel(
     const uint8_t* A, int64_t lda, const float* as, int64_t ldas, const uint8_t* X, int64_t ldx,
     const float* xs, int64_t ldxs, const float* bias, void* Y, int64_t ldy, int M, int K, int T,
-    int row_tiles, int whole_pieces) {
+    int row_tiles) {
     constexpr int NM = C::WM / 16, NN = C::WN / 16;
     extern __shared__ __align__(16) uint8_t lds[];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -392,10 +395,6 @@ __global__ __launch_bounds__(C::kWaves * 64, DIRECT ? C::kOccupancy : 2) void fp
     const int row0 = (first_row + in_group % rows) * C::BM, t0 = in_group / rows * C::BN;
     const int wm = wave % (C::BM / C::WM) * C::WM, wn = wave / (C::BM / C::WM) * C::WN;
     const int blocks = K / kScaleBlock + (K % kScaleBlock != 0);
-    // blocks that are loaded straight into LDS: the whole ones, if pieces are
-    // aligned (DIRECT: all; the other path's registers cost the kernel a sixth)
-    const int direct = DIRECT ? blocks : whole_pieces ? K / kScaleBlock : 0;
-
     // what the wavefront loads of each stage: 8 rows at a time, of W or of X,
     // a lane a piece; rows past the end repeat the last one
     const int in = lane >> 3, piece = 16 * ((lane & 7) ^ in);
@@ -427,27 +426,32 @@ __global__ __launch_bounds__(C::kWaves * 64, DIRECT ? C::kOccupancy : 2) void fp
         soffset[i] = (uint32_t)(in < last - first ? in : last - first) * (uint32_t)(of_x ? ldxs : ldas);
     }
     const uint32_t lds_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
+    // Straight into LDS (DIRECT: whole blocks of aligned pieces) ...
     auto stage = [&](int to, int b) {
         const uint32_t at = lds_at + to * C::kStageBytes;
-        if (!DIRECT && b >= direct) {
-#pragma unroll 1
-            for (int i = 0; i < C::kLoads; ++i) {
-                const int row = (wave + i * C::kWaves) * 8 + in;
-                const bool of_w = row < C::BM;
-                const int want = of_w ? row0 + row : t0 + row - C::BM, last = of_w ? M - 1 : T - 1;
-                const int64_t line = want < last ? want : last;
-                *reinterpret_cast<quad*>(lds + to * C::kStageBytes + (wave + i * C::kWaves) * 1024 + lane * 16) =
-                    piece_of(of_w ? A + line * lda : X + line * ldx, (int64_t)b * kScaleBlock + piece, K);
-            }
-            wait_lds();
-            wait_loads<0>();  // this stage adds nothing to what the phases' waits count
-            return;
-        }
 #pragma unroll
         for (int i = 0; i < C::kLoads; ++i) {
             const uint32_t pitch = (uint32_t)((wave + i * C::kWaves) * 8 < C::BM ? lda : ldx);
             lds_load16(base[i] + (int64_t)b * kScaleBlock,
                        (in < left[i] ? in : left[i]) * pitch + piece, at + (wave + i * C::kWaves) * 1024);
+        }
+    };
+    // ... or through registers: fetched when a stage becomes free, written to it
+    // at the end of the next phase.
+    quad held[DIRECT ? 1 : C::kLoads];
+    auto fetch = [&](int b) {
+#pragma unroll
+        for (int i = 0; i < C::kLoads; ++i) {
+            const int64_t pitch = (wave + i * C::kWaves) * 8 < C::BM ? lda : ldx;
+            held[i] = piece_of(base[i] + (in < left[i] ? in : left[i]) * pitch, b, piece, K);
+        }
+    };
+    auto commit = [&](int to) {
+        if constexpr (!DIRECT) {
+#pragma unroll
+            for (int i = 0; i < C::kLoads; ++i)
+                *reinterpret_cast<quad*>(lds + to * C::kStageBytes + (wave + i * C::kWaves) * 1024 + lane * 16) = held[i];
+            wait_lds();
         }
     };
     auto stage_scales = [&](int span) {
@@ -528,14 +532,23 @@ __global__ __launch_bounds__(C::kWaves * 64, DIRECT ? C::kOccupancy : 2) void fp
     // The scales of a span are loaded a block after the span before it began,
     // when nothing reads the span before that any more.
     auto load = [&](int b) {
-        stage(b % C::STAGES, b < blocks ? b : blocks - 1);
+        if constexpr (DIRECT)
+            stage(b % C::STAGES, b < blocks ? b : blocks - 1);
+        else
+            fetch(b < blocks ? b : blocks - 1);
         const int at = b + 1 - C::STAGES;
         if (at % C::kSpan == 1) stage_scales(at / C::kSpan + 1);
     };
+    // loads that may be in flight when a block must have landed (the scales of
+    // the next span may be: they are wanted blocks later)
+    constexpr int kInFlight = DIRECT ? C::kInFlight : 0;
     stage_scales(0);
 #pragma unroll
-    for (int b = 0; b < C::STAGES - 1; ++b) load(b);
-    wait_loads<C::kInFlight>();
+    for (int b = 0; b < C::STAGES - 1; ++b) {
+        load(b);
+        commit(b);
+    }
+    wait_loads<kInFlight>();
     change_over();
     if (half == 0) {
         for (int b = 0; b < blocks; ++b) {
@@ -546,7 +559,8 @@ __global__ __launch_bounds__(C::kWaves * 64, DIRECT ? C::kOccupancy : 2) void fp
             __builtin_amdgcn_s_setprio(1);
             multiply();
             __builtin_amdgcn_s_setprio(0);
-            wait_loads<C::kInFlight>();
+            commit((b + C::STAGES - 1) % C::STAGES);
+            wait_loads<kInFlight>();
             change_over();
         }
         change_over();
@@ -556,7 +570,8 @@ __global__ __launch_bounds__(C::kWaves * 64, DIRECT ? C::kOccupancy : 2) void fp
         for (int b = 0; b < blocks; ++b) {
             read(b);
             wait_lds();
-            wait_loads<C::kInFlight>();
+            commit((b + C::STAGES - 1) % C::STAGES);
+            wait_loads<kInFlight>();
             change_over();
             load(b + C::STAGES);
             __builtin_amdgcn_s_setprio(1);
@@ -565,6 +580,7 @@ __global__ __launch_bounds__(C::kWaves * 64, DIRECT ? C::kOccupancy : 2) void fp
             change_over();
         }
     }
+    wait_loads<0>();
     // The results go through LDS, so that a token's BM values are stored as
     // one piece (straight from the registers they would be 32-byte pieces).
     wait_loads<0>();
@@ -636,7 +652,7 @@ template <class O, class C, bool EXACT, bool DIRECT>
 __global__ __launch_bounds__(C::kWaves * 64) void fp8_split_kernel(
     const uint8_t* A, int64_t lda, const float* as, int64_t ldas, const uint8_t* X, int64_t ldx,
     const float* xs, int64_t ldxs, const float* bias, void* Y, int64_t ldy, int M, int K, int T,
-    int row_tiles, int whole_pieces) {
+    int row_tiles) {
     extern __shared__ __align__(16) uint8_t lds[];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int ks = wave >> 2, member = wave & 3;
@@ -648,7 +664,6 @@ __global__ __launch_bounds__(C::kWaves * 64) void fp8_split_kernel(
     const int token_tiles = tiles / row_tiles;
     const int row0 = tile / token_tiles * C::BM, t0 = tile % token_tiles * C::BN;
     const int blocks = K / kScaleBlock + (K % kScaleBlock != 0);
-    const int direct = DIRECT ? blocks : whole_pieces ? K / kScaleBlock : 0;
 
     // what the wavefront loads of each step: 8 rows at a time, of W, then of X
     constexpr int kLoads = C::kLoadsW + C::kLoadsX;
@@ -659,7 +674,7 @@ __global__ __launch_bounds__(C::kWaves * 64) void fp8_split_kernel(
         return C::BM + (n < C::BN / 8 ? n : C::BN / 8 - 1) * 8;
     };
     const uint8_t* base[kLoads];
-    uint32_t offset[kLoads];
+    int line[kLoads];  // the lane's, behind the first
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
         const int row = first_row(i);
@@ -668,7 +683,7 @@ __global__ __launch_bounds__(C::kWaves * 64) void fp8_split_kernel(
         int first = of_w ? row0 + row : t0 + row - C::BM;
         first = first < last ? first : last;
         base[i] = of_w ? A + (int64_t)first * lda : X + (int64_t)first * ldx;
-        offset[i] = (uint32_t)(in < last - first ? in : last - first) * (uint32_t)(of_w ? lda : ldx) + piece;
+        line[i] = in < last - first ? in : last - first;
     }
     const int sn = wave < C::kScaleLoads ? wave : C::kScaleLoads - 1;
     const float* sbase;
@@ -683,33 +698,35 @@ __global__ __launch_bounds__(C::kWaves * 64) void fp8_split_kernel(
         soffset = (uint32_t)(line < last - first ? line : last - first) * (uint32_t)(of_x ? ldxs : ldas);
     }
     const uint32_t lds_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
-    // Past the last block the last is loaded again, into places that nothing
-    // reads: every wavefront always waits for the same count.
+    // Straight into LDS (DIRECT), or through registers, written to the stage at
+    // the end of the step.  Past the last block the last is loaded again, into
+    // places that nothing reads: every wavefront always waits for the same count.
+    quad held[DIRECT ? 1 : kLoads];
     auto stage = [&](int n, int to) {
-        const int at = to * C::kStageBytes, mine = at + ks * C::kBlockBytes;
         int b = n * C::KS + ks;
         b = b < blocks ? b : blocks - 1;
-        if (DIRECT || b < direct) {
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i)
-                lds_load16(base[i] + (int64_t)b * kScaleBlock, offset[i], lds_at + mine + first_row(i) * kScaleBlock);
-        } else {
-#pragma unroll 1
-            for (int i = 0; i < kLoads; ++i) {
-                const int row = first_row(i) + in;
-                const bool of_w = i < C::kLoadsW;
-                const int want = of_w ? row0 + row : t0 + row - C::BM, last = of_w ? M - 1 : T - 1;
-                const int64_t line = want < last ? want : last;
-                *reinterpret_cast<quad*>(lds + mine + first_row(i) * kScaleBlock + lane * 16) =
-                    piece_of(of_w ? A + line * lda : X + line * ldx, (int64_t)b * kScaleBlock + piece, K);
-            }
-            wait_lds();
-            wait_loads<0>();  // this step adds less than the waits count
-        }
+        for (int i = 0; i < kLoads; ++i)
+            if constexpr (DIRECT)
+                lds_load16(base[i] + (int64_t)b * kScaleBlock,
+                           line[i] * (uint32_t)(i < C::kLoadsW ? lda : ldx) + piece,
+                           lds_at + to * C::kStageBytes + ks * C::kBlockBytes + first_row(i) * kScaleBlock);
+            else
+                held[i] = piece_of(base[i] + line[i] * (i < C::kLoadsW ? lda : ldx), b, piece, K);
         const int sb = n * C::KS + (lane & 3);
         lds_load4(sbase, (soffset + (sb < blocks ? sb : blocks - 1)) * 4,
-                  lds_at + at + C::KS * C::kBlockBytes + sn * 256);
+                  lds_at + to * C::kStageBytes + C::KS * C::kBlockBytes + sn * 256);
     };
+    auto commit = [&](int to) {
+        if constexpr (!DIRECT) {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i)
+                *reinterpret_cast<quad*>(lds + to * C::kStageBytes + ks * C::kBlockBytes +
+                                         first_row(i) * kScaleBlock + lane * 16) = held[i];
+            wait_lds();
+        }
+    };
+    constexpr int kInFlight = DIRECT ? C::kInFlight : 0;
 
     f32x4 acc[C::NM][C::NN];
 #pragma unroll
@@ -719,17 +736,8 @@ __global__ __launch_bounds__(C::kWaves * 64) void fp8_split_kernel(
     const int lo = r * kScaleBlock + 16 * (g ^ (r & 7));
     const int hi = r * kScaleBlock + 16 * ((g + 4) ^ (r & 7));
     const int steps = (blocks + C::KS - 1) / C::KS;
-#pragma unroll
-    for (int n = 0; n < C::STAGES - 1; ++n) stage(n, n);
-    int now = 0, next = C::STAGES - 1;
-    for (int n = 0; n < steps; ++n) {
-        wait_loads<C::kInFlight>();
-        change_over();
-        stage(n + C::STAGES - 1, next);
-        const uint8_t* at = lds + now * C::kStageBytes;
-        next = now;
-        now = now + 1 == C::STAGES ? 0 : now + 1;
-        if (n * C::KS + ks >= blocks) continue;  // (the barriers are at the loop's head)
+    auto product_of = [&](int from) {
+        const uint8_t* at = lds + from * C::kStageBytes;
         const uint8_t* a = at + ks * C::kBlockBytes + wm * kScaleBlock;
         const uint8_t* x = at + ks * C::kBlockBytes + (C::BM + wn) * kScaleBlock;
         const float* s = reinterpret_cast<const float*>(at + C::KS * C::kBlockBytes);
@@ -754,6 +762,21 @@ __global__ __launch_bounds__(C::kWaves * 64) void fp8_split_kernel(
                 for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(d[e], st[j], acc[i][j][e]);
             }
         }
+    };
+#pragma unroll
+    for (int n = 0; n < C::STAGES - 1; ++n) {
+        stage(n, n);
+        commit(n);
+    }
+    int now = 0, next = C::STAGES - 1;
+    for (int n = 0; n < steps; ++n) {
+        wait_loads<kInFlight>();
+        change_over();
+        stage(n + C::STAGES - 1, next);
+        if (n * C::KS + ks < blocks) product_of(now);
+        commit(next);
+        next = now;
+        now = now + 1 == C::STAGES ? 0 : now + 1;
     }
     wait_loads<0>();
     change_over();
