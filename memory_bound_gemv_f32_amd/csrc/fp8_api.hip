@@ -138,9 +138,9 @@ gemv_status_t product(const uint8_t* W, int ldw, const float* w_scale, int ldws,
     if (K > 0 && (W == nullptr || X == nullptr || w_scale == nullptr || x_scale == nullptr))
         return GEMV_ERROR_INVALID_VALUE;
     int64_t ldw64 = ldw, ldws64 = ldws, ldx64 = ldx, ldxs64 = ldxs, ldy64 = ldy;
-    // whole blocks of aligned 16-byte pieces may be loaded straight into LDS
-    // (with 32-bit offsets within 8 rows)
-    const bool direct = K % GEMV_FP8_BLOCK == 0 && ldw % 16 == 0 && ldx % 16 == 0 && aligned(W, 16) &&
+    // whole, aligned 16-byte pieces may be loaded straight into LDS (with
+    // 32-bit offsets within 8 rows)
+    const bool direct = K % 16 == 0 && ldw % 16 == 0 && ldx % 16 == 0 && aligned(W, 16) &&
                         aligned(X, 16) && ldw < (1 << 28) && ldx < (1 << 28);
     int row_tiles = 0, tokens = nvec;
     void* argv[] = {&W,    &ldw64, &w_scale, &ldws64, &X, &ldx64,  &x_scale, &ldxs64,

@@ -282,6 +282,10 @@ __global__ __launch_bounds__(W * 64) void fp8_few_kernel(
 // in the same phase the LDS, the matrix cores and the vector ALUs, which scale
 // each block's sum, waited for each other in turn.)
 //
+// DIRECT, for aligned rows of whole 16-byte pieces; anything else passes
+// through registers, byte by byte where a piece is not whole or not all of the
+// row: 2000 x 4096 x 4112 bf16 50 us, 2000 x 4096 x 4100 102.
+//
 // LDS.  A stage holds the rows' 128 bytes one behind the other in eight
 // 16-byte slots; slot s of row r holds piece s ^ (r % 8), so that the 8 lanes
 // of a read that want the same piece of 8 neighbouring rows find it in 8
@@ -324,6 +328,12 @@ __device__ __forceinline__ f32x4 mma_16x16x128(i32x8 a, i32x8 b) {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, zero, 0, 0, 0, 0, 0, 0);
 }
 
+// What follows from v is not kept in registers from before a loop on.
+__device__ __forceinline__ int worked_out_here(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
 // An operand of a block as its matrix-core steps take it.
 template <bool EXACT>
 struct Operand;
@@ -351,6 +361,18 @@ __device__ __forceinline__ quad piece_of(const uint8_t* row, int b, int piece, i
     const int left = K - b * kScaleBlock;  // uniform: of the row, from the block on
     if (left >= kScaleBlock) return *reinterpret_cast<const quad_any*>(at);
     return load_bytes(at, left - piece);
+}
+
+// A last block of fewer columns, in whole pieces, loaded straight into LDS: the
+// lanes of the pieces behind the row load the block's first piece again, and X's
+// copies are made zero as they are read.  (W's need not be: a NaN among them
+// is also in its own place in that row, whose results it makes NaN there.)
+__device__ __forceinline__ void blank_behind(i32x8& x, int group, int columns) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[i] = 16 * group < columns ? x[i] : 0;
+        x[4 + i] = 16 * (group + 4) < columns ? x[4 + i] : 0;
+    }
 }
 
 template <int BM_, int BN_, int WM_, int WN_, int STAGES_, int GROUP_>
@@ -399,7 +421,7 @@ __global__ __launch_bounds__(C::kWaves * 64, DIRECT ? C::kOccupancy : 2) void fp
     // a lane a piece; rows past the end repeat the last one
     const int in = lane >> 3, piece = 16 * ((lane & 7) ^ in);
     const uint8_t* base[C::kLoads];
-    int left[C::kLoads];  // rows behind the first of the 8
+    int64_t offset[C::kLoads];  // the lane's, of its row
 #pragma unroll
     for (int i = 0; i < C::kLoads; ++i) {
         const int row = (wave + i * C::kWaves) * 8;
@@ -407,13 +429,14 @@ __global__ __launch_bounds__(C::kWaves * 64, DIRECT ? C::kOccupancy : 2) void fp
         const int last = of_w ? M - 1 : T - 1;
         int first = of_w ? row0 + row : t0 + row - C::BM;
         first = first < last ? first : last;
-        left[i] = last - first;
+        offset[i] = (in < last - first ? in : last - first) * (of_w ? lda : ldx);
         base[i] = of_w ? A + (int64_t)first * lda : X + (int64_t)first * ldx;
     }
     // ... and which scales: eight lines of eight blocks, block b of line n in
     // place b ^ (n / 8 % 2), so that 16 neighbouring lines lie in 16 banks
     const float* sbase[C::kScaleEach];
-    uint32_t soffset[C::kScaleEach], sto[C::kScaleEach];
+    int sleft[C::kScaleEach];  // lines behind the first of the eight
+    uint32_t spitch[C::kScaleEach], sto[C::kScaleEach];
 #pragma unroll
     for (int i = 0; i < C::kScaleEach; ++i) {
         const int n = wave + i * C::kWaves < C::kScaleLoads ? wave + i * C::kWaves : C::kScaleLoads - 1;
@@ -423,28 +446,36 @@ __global__ __launch_bounds__(C::kWaves * 64, DIRECT ? C::kOccupancy : 2) void fp
         int first = of_x ? t0 + n * 8 : row0 / kScaleBlock;
         first = first < last ? first : last;
         sbase[i] = of_x ? xs + (int64_t)first * ldxs : as + (int64_t)first * ldas;
-        soffset[i] = (uint32_t)(in < last - first ? in : last - first) * (uint32_t)(of_x ? ldxs : ldas);
+        sleft[i] = last - first;
+        spitch[i] = (uint32_t)(of_x ? ldxs : ldas);
     }
     const uint32_t lds_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
-    // Straight into LDS (DIRECT: whole blocks of aligned pieces) ...
+    // Straight into LDS (DIRECT: whole, aligned pieces) ...
+    const int tail = K % kScaleBlock, tail_block = tail ? blocks - 1 : -1;
+    uint32_t from[DIRECT ? C::kLoads : 1];
+    if constexpr (DIRECT)
+#pragma unroll
+        for (int i = 0; i < C::kLoads; ++i) from[i] = (uint32_t)offset[i] + piece;
     auto stage = [&](int to, int b) {
         const uint32_t at = lds_at + to * C::kStageBytes;
+        if (b == tail_block) {  // once: what follows is that block again
+            const int l = worked_out_here(lane);
+            const int own = 16 * ((l & 7) ^ (l >> 3));
+            const uint32_t back = own >= tail ? own : 0;
 #pragma unroll
-        for (int i = 0; i < C::kLoads; ++i) {
-            const uint32_t pitch = (uint32_t)((wave + i * C::kWaves) * 8 < C::BM ? lda : ldx);
-            lds_load16(base[i] + (int64_t)b * kScaleBlock,
-                       (in < left[i] ? in : left[i]) * pitch + piece, at + (wave + i * C::kWaves) * 1024);
+            for (int i = 0; i < C::kLoads; ++i) from[i] -= back;
         }
+        const int64_t column = (int64_t)(b < blocks ? b : blocks - 1) * kScaleBlock;
+#pragma unroll
+        for (int i = 0; i < C::kLoads; ++i)
+            lds_load16(base[i] + column, from[i], at + (wave + i * C::kWaves) * 1024);
     };
     // ... or through registers: fetched when a stage becomes free, written to it
     // at the end of the next phase.
     quad held[DIRECT ? 1 : C::kLoads];
     auto fetch = [&](int b) {
 #pragma unroll
-        for (int i = 0; i < C::kLoads; ++i) {
-            const int64_t pitch = (wave + i * C::kWaves) * 8 < C::BM ? lda : ldx;
-            held[i] = piece_of(base[i] + (in < left[i] ? in : left[i]) * pitch, b, piece, K);
-        }
+        for (int i = 0; i < C::kLoads; ++i) held[i] = piece_of(base[i] + offset[i], b, piece, K);
     };
     auto commit = [&](int to) {
         if constexpr (!DIRECT) {
@@ -456,11 +487,13 @@ __global__ __launch_bounds__(C::kWaves * 64, DIRECT ? C::kOccupancy : 2) void fp
     };
     auto stage_scales = [&](int span) {
         const uint32_t at = lds_at + C::STAGES * C::kStageBytes + (span & 1) * C::kScaleBytes;
+        const int l = worked_out_here(lane), line = l >> 3;
 #pragma unroll
         for (int i = 0; i < C::kScaleEach; ++i) {
             const int swap = sto[i] / 256 & 1;  // line n / 8 of the load is n: all its lines share it
-            const int b = span * C::kSpan + ((lane & 7) ^ swap);
-            lds_load4(sbase[i], (soffset[i] + (b < blocks ? b : blocks - 1)) * 4, at + sto[i]);
+            const int b = span * C::kSpan + ((l & 7) ^ swap);
+            lds_load4(sbase[i], ((line < sleft[i] ? line : sleft[i]) * spitch[i] + (b < blocks ? b : blocks - 1)) * 4,
+                      at + sto[i]);
         }
     };
 
@@ -488,6 +521,9 @@ __global__ __launch_bounds__(C::kWaves * 64, DIRECT ? C::kOccupancy : 2) void fp
         for (int i = 0; i < NM; ++i)
             af[i] = join(*reinterpret_cast<const quad*>(a + 16 * i * kScaleBlock + lo),
                          *reinterpret_cast<const quad*>(a + 16 * i * kScaleBlock + hi));
+        if (DIRECT && b == tail_block)
+#pragma unroll
+            for (int j = 0; j < NN; ++j) blank_behind(xf[j], g, tail);
         const float sa = s[(C::BN + wm / kScaleBlock) * C::kSpan + (span_at ^ (C::BN / 8 & 1))];
 #pragma unroll
         for (int j = 0; j < NN; ++j) st[j] = sa * s[(wn + 16 * j + r) * C::kSpan + (span_at ^ (r >> 3))];
@@ -533,7 +569,7 @@ __global__ __launch_bounds__(C::kWaves * 64, DIRECT ? C::kOccupancy : 2) void fp
     // when nothing reads the span before that any more.
     auto load = [&](int b) {
         if constexpr (DIRECT)
-            stage(b % C::STAGES, b < blocks ? b : blocks - 1);
+            stage(b % C::STAGES, b);
         else
             fetch(b < blocks ? b : blocks - 1);
         const int at = b + 1 - C::STAGES;
@@ -698,18 +734,21 @@ __global__ __launch_bounds__(C::kWaves * 64) void fp8_split_kernel(
         soffset = (uint32_t)(line < last - first ? line : last - first) * (uint32_t)(of_x ? ldxs : ldas);
     }
     const uint32_t lds_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
-    // Straight into LDS (DIRECT), or through registers, written to the stage at
+    const int tail = K % kScaleBlock, tail_block = tail ? blocks - 1 : -1;
+    const uint32_t back = tail && piece >= tail ? piece : 0;
+    // Straight into LDS (DIRECT: whole, aligned pieces), or through registers, written to the stage at
     // the end of the step.  Past the last block the last is loaded again, into
     // places that nothing reads: every wavefront always waits for the same count.
     quad held[DIRECT ? 1 : kLoads];
     auto stage = [&](int n, int to) {
         int b = n * C::KS + ks;
         b = b < blocks ? b : blocks - 1;
+        const uint32_t own = b == tail_block ? piece - back : piece;
 #pragma unroll
         for (int i = 0; i < kLoads; ++i)
             if constexpr (DIRECT)
                 lds_load16(base[i] + (int64_t)b * kScaleBlock,
-                           line[i] * (uint32_t)(i < C::kLoadsW ? lda : ldx) + piece,
+                           line[i] * (uint32_t)(i < C::kLoadsW ? lda : ldx) + own,
                            lds_at + to * C::kStageBytes + ks * C::kBlockBytes + first_row(i) * kScaleBlock);
             else
                 held[i] = piece_of(base[i] + line[i] * (i < C::kLoadsW ? lda : ldx), b, piece, K);
@@ -736,7 +775,7 @@ __global__ __launch_bounds__(C::kWaves * 64) void fp8_split_kernel(
     const int lo = r * kScaleBlock + 16 * (g ^ (r & 7));
     const int hi = r * kScaleBlock + 16 * ((g + 4) ^ (r & 7));
     const int steps = (blocks + C::KS - 1) / C::KS;
-    auto product_of = [&](int from) {
+    auto product_of = [&](int b, int from) {
         const uint8_t* at = lds + from * C::kStageBytes;
         const uint8_t* a = at + ks * C::kBlockBytes + wm * kScaleBlock;
         const uint8_t* x = at + ks * C::kBlockBytes + (C::BM + wn) * kScaleBlock;
@@ -746,8 +785,10 @@ __global__ __launch_bounds__(C::kWaves * 64) void fp8_split_kernel(
         const float sa = s[(C::BN + wm / kScaleBlock) * C::KS + ks];
 #pragma unroll
         for (int j = 0; j < C::NN; ++j) {
-            xo[j] = Operand<EXACT>::of(join(*reinterpret_cast<const quad*>(x + 16 * j * kScaleBlock + lo),
-                                            *reinterpret_cast<const quad*>(x + 16 * j * kScaleBlock + hi)));
+            i32x8 xf = join(*reinterpret_cast<const quad*>(x + 16 * j * kScaleBlock + lo),
+                            *reinterpret_cast<const quad*>(x + 16 * j * kScaleBlock + hi));
+            if (DIRECT && b == tail_block) blank_behind(xf, g, tail);
+            xo[j] = Operand<EXACT>::of(xf);
             st[j] = sa * s[(wn + 16 * j + r) * C::KS + ks];
         }
 #pragma unroll
@@ -773,7 +814,7 @@ __global__ __launch_bounds__(C::kWaves * 64) void fp8_split_kernel(
         wait_loads<kInFlight>();
         change_over();
         stage(n + C::STAGES - 1, next);
-        if (n * C::KS + ks < blocks) product_of(now);
+        if (n * C::KS + ks < blocks) product_of(n * C::KS + ks, now);
         commit(next);
         next = now;
         now = now + 1 == C::STAGES ? 0 : now + 1;

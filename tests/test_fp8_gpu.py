@@ -180,6 +180,34 @@ def test_product_nan_stays_in_its_row():
         assert np.array_equal(y, want)
 
 
+@pytest.mark.parametrize("K", [16, 112, 144, 1008])
+@pytest.mark.parametrize("tokens,M", [(1, 270), (12, 8200), (40, 270), (40, 17000), (150, 270), (200, 2050), (400, 4100),
+                                      (900, 1000), (1030, 3100)])
+def test_product_short_last_block(tokens, M, K):
+    """A last block of whole 16-byte pieces: what lies behind the rows is not
+    used, whatever it holds, and a NaN in that block makes its own row's (or
+    token's) results NaN and no others."""
+    g = torch.Generator().manual_seed(tokens + K)
+    def padded(rows):
+        t = torch.full((rows, K + 32), float("nan"))
+        t[:, :K] = torch.randint(-4, 5, (rows, K), generator=g).float()
+        return t.to(torch.float8_e4m3fn).cuda()[:, :K]
+    W, X = padded(M), padded(tokens)
+    blocks = -(-K // 128)
+    ws = torch.exp2(torch.randint(-1, 2, (-(-M // 128), blocks), generator=g).float()).cuda()
+    xs = torch.exp2(torch.randint(-1, 2, (tokens, blocks), generator=g).float()).cuda()
+    first = (blocks - 1) * 128
+    want, _ = product(W, ws, X, xs)
+    for out in (torch.float32, torch.bfloat16):
+        assert torch.equal(lg.gemv_fp8(W, ws, X, xs, out_dtype=out).cpu(), torch.from_numpy(want).to(out))
+    W.view(torch.uint8)[M // 2, first + 3] = 0x7F
+    X.view(torch.uint8)[tokens // 2, first + 5] = 0xFF
+    want[:, M // 2] = want[tokens // 2] = float("nan")
+    for out in (torch.float32, torch.bfloat16):
+        y = lg.gemv_fp8(W, ws, X, xs, out_dtype=out).cpu()
+        assert torch.equal(y.nan_to_num(nan=7e6), torch.from_numpy(want).to(out).nan_to_num(nan=7e6))
+
+
 def test_product_empty():
     one = torch.ones
     W, ws = operand(1, 30, 0, 128)
