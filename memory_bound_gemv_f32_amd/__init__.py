@@ -501,6 +501,7 @@ if _torch_runtime is not None:
     _QUANTISE = _by_dtype(gemv_fp8_quantise_f32, gemv_fp8_quantise_f16, gemv_fp8_quantise_bf16)
     _PRODUCT = _by_dtype(gemv_fp8_f32, gemv_fp8_f16, gemv_fp8_bf16)
     _APPEND = _by_dtype(gemv_kv_append_f32, gemv_kv_append_f16, gemv_kv_append_bf16)
+    _KV_FORMATS = {_torch_runtime.int8: KV_INT8, _torch_runtime.float8_e4m3fn: KV_E4M3}
     _ATTEND = {_torch_runtime.float16: gemv_kv_attend_f16, _torch_runtime.bfloat16: gemv_kv_attend_bf16}
 
 
@@ -632,28 +633,30 @@ class KVCache:
     allocates them."""
 
     def __init__(self, k, v, k_scale, v_scale):
-        torch = _torch()
-        if k.dim() != 4 or v.dim() != 5:
+        _torch()
+        shape = k.shape
+        if len(shape) != 4 or v.dim() != 5:
             raise ValueError("k must be (pages, heads, page_size, dim) and v (pages, heads, page_size // 16, dim, 16)")
-        pages, heads, page_size, dim = k.shape
+        pages, heads, page_size, dim = shape
         if page_size not in (16, 32, 64, 128, 256) or dim not in (64, 128, 256):
             raise ValueError("page_size must be 16, 32, 64, 128 or 256 and dim 64, 128 or 256")
         blocks = page_size // KV_BLOCK
-        if tuple(v.shape) != (pages, heads, blocks, dim, KV_BLOCK):
+        if v.shape != (pages, heads, blocks, dim, KV_BLOCK):
             raise ValueError(f"v must be of shape {(pages, heads, blocks, dim, KV_BLOCK)}")
-        formats = {torch.int8: KV_INT8, torch.float8_e4m3fn: KV_E4M3}
-        if k.dtype not in formats or v.dtype != k.dtype:
+        cache_format = _KV_FORMATS.get(k.dtype)
+        if cache_format is None or v.dtype is not k.dtype:
             raise TypeError("k and v must both be int8 or both float8_e4m3fn")
-        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-            if t.dtype != torch.float32 or tuple(t.shape) != (pages, heads, blocks):
-                raise ValueError(f"{name} must be a float32 tensor of shape {(pages, heads, blocks)}")
-        for t in (k, v, k_scale, v_scale):
-            if not t.is_cuda or not t.is_contiguous() or t.device != k.device:
-                raise ValueError("the cache's tensors must be contiguous on one device")
+        scale = (pages, heads, blocks)
+        if k_scale.dtype is not _F32 or v_scale.dtype is not _F32 or k_scale.shape != scale or v_scale.shape != scale:
+            raise ValueError(f"k_scale and v_scale must be float32 tensors of shape {scale}")
+        dev = k.get_device()
+        if dev < 0 or not (dev == v.get_device() == k_scale.get_device() == v_scale.get_device()) or not (
+                k.is_contiguous() and v.is_contiguous() and k_scale.is_contiguous() and v_scale.is_contiguous()):
+            raise ValueError("the cache's tensors must be contiguous on one device")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.pages, self.heads, self.page_size, self.dim = pages, heads, page_size, dim
-        self._device = k.get_device()
-        self._struct = KvCacheStruct(formats[k.dtype], pages, heads, page_size, dim, k.data_ptr(),
+        self._device = dev
+        self._struct = KvCacheStruct(cache_format, pages, heads, page_size, dim, k.data_ptr(),
                                      v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr())
         self._ref = ctypes.byref(self._struct)
 

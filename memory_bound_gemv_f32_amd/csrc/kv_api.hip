@@ -74,7 +74,7 @@ gemv_status_t append(int dim, const kvdev::Cache& c, const kvdev::Batch& q, cons
 // wavefronts share them, and how many workgroups share a row tile's tokens.
 struct Mapping {
     int row_tiles;     // 16-row tiles of a wavefront
-    int waves_share;   // 4: the wavefronts take the chunks of the same rows in turn; 1: own rows each
+    int waves_share;   // 4 or 8: so many wavefronts take the chunks of the same rows in turn; 1: own rows each
     int group_rows;    // rows of a workgroup
     int place_rows;    // rows of it that can be there
     int splits, split_chunks;
@@ -121,6 +121,13 @@ Mapping map_attend(int q_heads, int heads, int dim, int rows, int sequences, boo
     m.splits = each > 0 ? (int)ceil_div(chunks, each) : 1;
     if (m.splits < 1) m.splits = 1;
     m.split_chunks = (int)each;
+    // No more than a workgroup for each compute unit, and latency is all: eight
+    // wavefronts (of dim 256 too large for the registers) halve the chunks that wait
+    // for each other (4 sequences, window 512: 13.8 us with four, 12.2 with eight;
+    // 4 x 4000 tokens, in two launches: 13.7 and 13.2).
+    if (dim <= 128 && m.waves_share == 4 && m.row_tiles == 1 && each > 4 &&
+        m.places * heads * m.splits <= kSlots / 2)
+        m.waves_share = 8;
     return m;
 }
 
@@ -142,11 +149,13 @@ gemv_status_t attend(const Mapping& m, Attend& p, hipStream_t stream) {
     if (grid > 0x7fffffff) return GEMV_ERROR_INVALID_VALUE;
     void* argv[] = {&p, &places};
     constexpr int kTwo = DIM <= 128 ? 2 : 1;
+    constexpr int kSmall = DIM <= 128 ? DIM : 128;  // (dim 256 has no eight, see map_attend)
     const void* fn = m.waves_share == 1 ? (const void*)&kvdev::kv_attend_kernel<T, F, DIM, kTwo, 1>
                      : m.row_tiles == 2 ? (const void*)&kvdev::kv_attend_kernel<T, F, DIM, kTwo, 4>
-                                        : (const void*)&kvdev::kv_attend_kernel<T, F, DIM, 1, 4>;
+                     : m.waves_share == 8 ? (const void*)&kvdev::kv_attend_kernel<T, F, kSmall, 1, 8>
+                                          : (const void*)&kvdev::kv_attend_kernel<T, F, DIM, 1, 4>;
     const gemv_status_t st = launch(fn, dim3((unsigned)grid),
-                                    64 * (m.waves_share == 1 ? kvdev::kOwnWaves : kvdev::kShareWaves), argv, stream);
+                                    64 * (m.waves_share == 1 ? kvdev::kOwnWaves : m.waves_share), argv, stream);
     if (st != GEMV_SUCCESS || p.splits == 1) return st;
     const void* join = m.waves_share == 1 ? (const void*)&kvdev::kv_join_kernel<T, DIM, 16 * kvdev::kOwnWaves * kTwo, 16 * kTwo>
                        : m.row_tiles == 2 ? (const void*)&kvdev::kv_join_kernel<T, DIM, 16 * kTwo, 16 * kTwo>

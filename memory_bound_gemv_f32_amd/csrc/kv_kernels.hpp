@@ -376,12 +376,18 @@ __device__ __forceinline__ float finite_base(float m) { return m == -__builtin_i
 constexpr float kSlack = 8.0f;
 
 constexpr int kChunk = 64;    // tokens of a step: four blocks
-// Wavefronts of a workgroup: 4 that share their rows, or 2 with rows of their
+// Wavefronts of a workgroup: 4 or 8 that share their rows, or 2 with rows of their
 // own (4 of those would read the same bytes more often from the same cache, but
 // leave fewer and longer workgroups: 176 us against 183 for four 1024-token prompts).
 constexpr int kShareWaves = 4, kOwnWaves = 2;
 template <int WS>
-constexpr int kWavesOf = WS == 1 ? kOwnWaves : kShareWaves;
+constexpr int kWavesOf = WS == 1 ? kOwnWaves : WS;
+
+// The first n of a block's 16 tokens, as bits.
+__device__ __forceinline__ uint32_t first_bits(int n) {
+    n = n < 0 ? 0 : n > kBlock ? kBlock : n;
+    return (1u << n) - 1;
+}
 
 struct Attend {
     Cache cache;
@@ -468,7 +474,7 @@ __device__ __forceinline__ Partial partial_at(const Attend& p, int64_t places, i
     return Partial{p.partial + part * p.rows * 2, p.partial + parts * p.rows * 2 + part * p.rows * DIM};
 }
 
-// WS = 4: the workgroup's wavefronts take the chunks of one row tile in turn
+// WS > 1: the workgroup's wavefronts take the chunks of one row tile in turn
 // and join in LDS.  WS = 1: each wavefront has a row tile of its own.
 template <class T, class F, int DIM, int RT, int WS>
 __global__ __launch_bounds__(kWavesOf<WS> * 64, DIM <= 128 ? 2 : 1) void kv_attend_kernel(Attend p, int64_t places) {
@@ -548,8 +554,10 @@ __global__ __launch_bounds__(kWavesOf<WS> * 64, DIM <= 128 ? 2 : 1) void kv_atte
     // into registers of their own (single tokens wait for memory, and a wave's 16
     // KiB in flight are what hides it); with two, or dim 256, there is room for one
     // chunk, and its K is loaded behind the first product of the chunk before, its V behind
-    // the second.
-    constexpr bool kAhead = RT == 1 && DIM <= 128;
+    // the second.  (With eight wavefronts, which have few chunks each, the plain
+    // step beats the pair: 12.2 us against 12.9 for 4 sequences with a window
+    // of 512; it is half the code.)
+    constexpr bool kAhead = RT == 1 && DIM <= 128 && WS <= 4;
     // The table's entries as they are: what they are worth is looked at when
     // they are used, so that the lookup never waits for the loads before it.
     struct Where {
@@ -583,7 +591,7 @@ __global__ __launch_bounds__(kWavesOf<WS> * 64, DIM <= 128 ? 2 : 1) void kv_atte
         for (int tt = 0; tt < 4; ++tt)
 #pragma unroll
             for (int h = 0; h < DIM / 64; ++h)
-                to.k[tt][h] = load_once<WS == 4>(kp + 4 * tt * DIM + 64 * h);
+                to.k[tt][h] = load_once<(WS > 1)>(kp + 4 * tt * DIM + 64 * h);
     };
     auto load_v = [&](int it, const Where& w, Bytes& to) {
         const int vb = 4 * span.chunk(it) + g;
@@ -593,7 +601,7 @@ __global__ __launch_bounds__(kWavesOf<WS> * 64, DIM <= 128 ? 2 : 1) void kv_atte
         to.vscale = c.v_scale[vi];
         const uint8_t* vp = c.v + vi * (kBlock * DIM) + n * kBlock;
 #pragma unroll
-        for (int u = 0; u < kTiles; ++u) to.v[u] = load_once<WS == 4>(vp + 16 * u * kBlock);
+        for (int u = 0; u < kTiles; ++u) to.v[u] = load_once<(WS > 1)>(vp + 16 * u * kBlock);
     };
 
     int it = begin + (WS == 1 ? 0 : wave);
@@ -658,14 +666,10 @@ __global__ __launch_bounds__(kWavesOf<WS> * 64, DIM <= 128 ? 2 : 1) void kv_atte
                 uint32_t sees = 0xffffu;  // tokens of block g that the lane's row sees
                 float scale = largest;    // (of blocks that the row does not see, none)
                 if constexpr (!WHOLE) {
-                    sees = 0;
-#pragma unroll
-                    for (int off = 0; off < kBlock; ++off) {
-                        const int j = vb * kBlock + off;
-                        if (off < there && j <= pos[i] &&
-                            (p.window == 0 || pos[i] - j < p.window || j < p.sinks))
-                            sees |= 1u << off;
-                    }
+                    const int j = vb * kBlock;
+                    sees = first_bits(there) & first_bits(pos[i] + 1 - j);
+                    if (p.window > 0 && pos[i] >= p.window)
+                        sees &= ~first_bits(pos[i] - p.window + 1 - j) | first_bits(p.sinks - j);
 #pragma unroll
                     for (int e = 0; e < kBlock; ++e)
                         if (!(sees >> e & 1)) s[i][e >> 2][e & 3] = -__builtin_inff();
@@ -751,13 +755,13 @@ __global__ __launch_bounds__(kWavesOf<WS> * 64, DIM <= 128 ? 2 : 1) void kv_atte
         for (int u = 0; u < kTiles; ++u) o[i][u] *= vref[i];
     }
     if constexpr (WS > 1) {
-        // wavefronts 2 and 3 join 0 and 1, then 1 joins 0
-        __shared__ f32x4 rows[2][RT][kTiles][64];
-        __shared__ float stat[2][RT][2][64];
+        // the upper half of the wavefronts joins the lower, and so on
+        __shared__ f32x4 rows[WS / 2][RT][kTiles][64];
+        __shared__ float stat[WS / 2][RT][2][64];
 #pragma unroll
-        for (int round = 2; round >= 1; --round) {
+        for (int round = WS / 2; round >= 1; round /= 2) {
             const int slot = wave - round;
-            if (round == 1) __syncthreads();
+            if (round < WS / 2) __syncthreads();
             if (slot >= 0 && slot < round) {
 #pragma unroll
                 for (int i = 0; i < RT; ++i) {
