@@ -29,7 +29,6 @@ gemv_status_t launch(const void* fn, dim3 grid, int threads, int lds_bytes, void
 using fp8dev::Split;
 using Large = fp8dev::Tile<128, 128, 64, 32, 2, 8>;
 using Medium = fp8dev::Tile<128, 64, 32, 32, 4, 8>;
-using Small = fp8dev::Tile<64, 64, 32, 16, 4, 8>;
 using Split64 = Split<64, 64, 2>;
 using Split32 = Split<64, 32, 3>;
 using Split16 = Split<64, 16, 3>;
@@ -73,28 +72,29 @@ int64_t tiles_of(int M, int nvec) {
 }
 
 // Which tile, for everything but few tokens of few rows.  The split kernels, with
-// the widest token tile that keeps a workgroup to each compute unit at most,
-// win wherever they fit; past that the largest tile that fills three
-// quarters of the units (the larger, the fewer bytes move).  Measured, us at
-// tokens x rows x K (Split16 | Split32 | Split64 | Small | Medium | Large):
-//   16 x 14336 x 4096    15.4 | 15.5 | 18.2 | 16.7 |      |
-//   64 x 4096 x 4096      8.2 |  8.6 | 11.9 | 14.4 |      |
-//   128 x 4096 x 4096    14.7 |  8.7 | 12.0 | 14.5 | 17   | 27
-//   192 x 4096 x 4096    20.9 | 15.6 | 12.3 | 14.6 |      |
-//   250 x 4096 x 11008   78   | 47   | 38.7 | 34.4 | 45   | 82
-//   512 x 4096 x 4096         |      | 28   | 22   | 19   | 31
-//   1024 x 4096 x 4096        |      | 58   | 40   | 36   | 33
-//   4096 x 14336 x 4096       |      | 783  | 460  | 458  | 267
+// the narrowest token tile that keeps a workgroup to each compute unit at most,
+// win wherever they fit; past that the larger tile, which moves fewer bytes,
+// where it fills three quarters of the units.  Measured, us at
+// tokens x rows x K, bf16 (Split16 | Split32 | Split64 | Medium | Large):
+//   16 x 14336 x 4096      12.1 |   13.4 |   15.9 |   18.0 |   25.0
+//   64 x 4096 x 4096       10.0 |   10.1 |   12.5 |   17.1 |   23.3
+//   128 x 4096 x 4096      15.8 |   10.3 |   12.7 |   17.4 |   24.1
+//   192 x 4096 x 4096      22.5 |   18.2 |   13.5 |   18.1 |   24.6
+//   250 x 4096 x 11008     61.5 |   38.1 |   29.6 |   40.7 |   61.6
+//   300 x 4096 x 4096      34.3 |   24.3 |   22.7 |   17.9 |   24.7
+//   512 x 4096 x 4096      55.6 |   32.1 |   24.0 |   18.8 |   24.8
+//   768 x 4096 x 4096      78.7 |   46.3 |   35.7 |   33.1 |   25.6
+//   1024 x 4096 x 4096    108.4 |   65.0 |   48.7 |   34.6 |   27.1
+//   4096 x 14336 x 4096  1528.2 |  936.3 |  801.9 |  442.0 |  276.1
 template <class O>
 Tiled tiled_kernel(int M, int nvec, bool direct) {
     const bool exact = nvec <= kExactTokens;
     if (nvec <= kFewTokens || tiles_of<Split16>(M, nvec) <= kUnits)
         return split_kernel<O, Split16>(direct, exact);
     if (nvec <= 32 || tiles_of<Split32>(M, nvec) <= kUnits) return split_kernel<O, Split32>(direct, exact);
+    if (tiles_of<Split64>(M, nvec) <= kUnits) return split_kernel<O, Split64>(direct, O::bytes == 4);
     if (tiles_of<Large>(M, nvec) >= kEnoughTiles) return tile_kernel<O, Large>(direct);
-    if (tiles_of<Medium>(M, nvec) >= kEnoughTiles) return tile_kernel<O, Medium>(direct);
-    if (tiles_of<Small>(M, nvec) >= kEnoughTiles) return tile_kernel<O, Small>(direct);
-    return split_kernel<O, Split64>(direct, O::bytes == 4);
+    return tile_kernel<O, Medium>(direct);
 }
 
 template <class D>
