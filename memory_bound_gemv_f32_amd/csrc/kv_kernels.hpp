@@ -443,6 +443,7 @@ template <int R>
 __device__ __forceinline__ bool tile_of(const Attend& p, int64_t place, Tile& t) {
     const Batch& q = p.batch;
     int64_t r0;
+    bool from_last = false;
     if (q.starts == nullptr) {  // one token each: so many places for its heads
         const int each = (p.group + R - 1) / R;
         t.b = (int)(place / each);
@@ -450,6 +451,7 @@ __device__ __forceinline__ bool tile_of(const Attend& p, int64_t place, Tile& t)
     } else {
         t.b = sequence_of(q, place, p.group, R, 1);
         r0 = (place - first_place(q, t.b, p.group, R, 1)) * R;
+        from_last = true;
     }
     t.start = start_of(q, t.b);
     const int stop = start_of(q, t.b + 1);
@@ -458,6 +460,9 @@ __device__ __forceinline__ bool tile_of(const Attend& p, int64_t place, Tile& t)
     t.len = q.lens[t.b];
     t.first = (int)((int64_t)t.len - (stop - t.start));
     t.rows = (stop - t.start) * p.group;
+    // a prompt's last rows see the most tokens: those workgroups start first
+    // (two 2048-token prompts 172 us in ascending order, 142 in this one)
+    if (from_last) r0 = (t.rows - 1) / R * R - r0;
     t.r0 = (int)r0;
     return r0 >= 0 && r0 < t.rows;
 }
