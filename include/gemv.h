@@ -359,7 +359,8 @@ gemv_status_t gemv_fp8_bf16(const uint8_t *W, int ldw, const float *w_scale,
  *   v_scale  the same
  *
  * A value is its byte times its block's scale, which is not negative.  Bytes
- * are int8 (-127..127) or e4m3.  A new cache needs no initial contents.
+ * are int8 (-127..127) or e4m3 (but its NaNs, 0x7F and 0xFF: a block of which a
+ * value is not finite has a NaN as its scale).  A new cache needs no initial contents.
  * ------------------------------------------------------------------------ */
 #define GEMV_KV_BLOCK 16
 
@@ -403,8 +404,8 @@ typedef struct {
  * nearest even.  A block that gets an infinity or a NaN has the
  * scale NaN and zero bytes, and reads as NaN until its first token is written
  * again.  Bytes and scales behind a sequence's last token are left as they
- * were.  Blocks that a call writes must belong to one sequence only (pages
- * shared by several sequences are for reading).
+ * were.  Blocks that a call writes must belong to one sequence only, and to one
+ * place of it (pages that several sequences or places share are for reading).
  * Errors: GEMV_ERROR_INVALID_VALUE for a cache or batch that is not as above,
  * negative sizes, a pitch below heads·dim, rows != sequences without starts, a
  * NULL or misaligned pointer. */
@@ -439,8 +440,9 @@ gemv_status_t gemv_kv_append_bf16(const gemv_kv_cache_t *cache, const uint16_t *
  *       only, and not on the lengths), 16-byte aligned; may be NULL where that is
  *       0; contract as for gemv_splitk_*.
  * Q and the cache's bytes enter the products exactly; scores, the softmax and
- * its sums are fp32; a softmax weight is rounded to Q's type before it meets V,
- * and the result once.  Deterministic: the order in which tokens are joined
+ * its sums are fp32; a softmax weight times its V scale, over the largest V scale
+ * that the row has seen, is rounded to fp16 before it meets V, and the result
+ * once to Q's type.  Deterministic: the order in which tokens are joined
  * depends on the sizes only.
  * Errors: as for gemv_kv_append_*, plus a q_heads that heads does not divide,
  * rows·q_heads past 2^31 - 1, a negative window or sinks, a scale that is not

@@ -145,6 +145,7 @@ gemv_run_family = _bind("gemv_run_family", [_i, _i, _vp, _i, _vp, _vp, _vp, _i, 
 gemv_test_refused_launch = _bind("gemv_test_refused_launch", [_st])
 
 FP8_BLOCK = 128
+_MOST = 0x7fffffff  # what an int argument holds
 KV_BLOCK = 16
 KV_INT8, KV_E4M3 = 0, 1
 
@@ -526,6 +527,15 @@ def _call(dev, stream, fn, *args):
         raise GemvError(rc, fn.__name__)
 
 
+def _empty(shape, dtype, device, stream):
+    """Memory for a call on ``stream`` (None: the current one): allocated
+    there, so that whoever had it, or has it next, is ordered with the call."""
+    if stream is None:
+        return _torch_runtime.empty(shape, dtype=dtype, device=device)
+    with _torch_runtime.cuda.stream(stream):
+        return _torch_runtime.empty(shape, dtype=dtype, device=device)
+
+
 def _rows(t, name, dev):
     """(rows, columns, row stride) of a matrix with unit column stride on
     device ``dev``."""
@@ -535,14 +545,16 @@ def _rows(t, name, dev):
     if dev < 0 or t.get_device() != dev:
         raise ValueError(f"{name} must be a device tensor, all on one device")
     rows, cols = shape
+    if rows > _MOST or cols > _MOST:
+        raise ValueError(f"{name} has more rows or columns than an int counts")
     if t.is_contiguous():
         return rows, cols, cols
     if cols > 1 and t.stride(1) != 1:
         raise ValueError(f"{name} must have unit column stride")
     # with one row, or no columns, the pitch is never used
     pitch = t.stride(0) if rows > 1 and cols > 0 else cols
-    if pitch < cols:
-        raise ValueError(f"{name}'s row stride is smaller than its rows")
+    if not cols <= pitch <= _MOST:
+        raise ValueError(f"{name}'s row stride is smaller than its rows, or more than an int counts")
     return rows, cols, pitch
 
 
@@ -566,7 +578,7 @@ def gemv_fp8_quantise(X, block_rows: int = 1, out=None, scale=None, *, stream=No
     rows, K, ldx = _rows(X, "X", dev)
     lines, blocks = -(-rows // block_rows), (K + FP8_BLOCK - 1) // FP8_BLOCK
     if out is None:
-        out = torch.empty((rows, K), dtype=torch.float8_e4m3fn, device=X.device)
+        out = _empty((rows, K), torch.float8_e4m3fn, X.device, stream)
         ldq = K
     else:
         if out.dtype not in _E4M3_BYTES:
@@ -575,7 +587,7 @@ def gemv_fp8_quantise(X, block_rows: int = 1, out=None, scale=None, *, stream=No
         if (have, across) != (rows, K):
             raise ValueError("out must have X's shape")
     if scale is None:
-        scale = torch.empty((lines, blocks), dtype=_F32, device=X.device)
+        scale = _empty((lines, blocks), _F32, X.device, stream)
         lds = blocks
     else:
         lds = _scales(scale, "scale", lines, blocks, dev)
@@ -605,7 +617,7 @@ def gemv_fp8(W, w_scale, X, x_scale, bias=None, out=None, *, out_dtype=None, str
         if out_dtype is None:
             out_dtype = _F32
         fn = _entry(_PRODUCT, out_dtype)
-        out = _torch_runtime.empty((nvec, M), dtype=out_dtype, device=W.device)
+        out = _empty((nvec, M), out_dtype, W.device, stream)
         ldy = M
     else:
         if out_dtype is not None and out.dtype != out_dtype:
@@ -683,7 +695,7 @@ def _kv_batch(cache, table, seq_lens, starts, rows):
     pitch = width
     if not table.is_contiguous():
         pitch = table.stride(0) if sequences > 1 else width
-        if (width > 1 and table.stride(1) != 1) or pitch < width:
+        if (width > 1 and table.stride(1) != 1) or not width <= pitch <= _MOST:
             raise ValueError("table must have unit column stride and a row stride of at least its width")
     if seq_lens.dtype is not _I32 or seq_lens.shape != (sequences,) or not seq_lens.is_contiguous():
         raise ValueError("seq_lens must be a contiguous int32 (sequences,) tensor")
@@ -712,8 +724,8 @@ def _heads(t, name, cache):
     if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
         raise ValueError(f"{name}'s heads must lie one behind the other in a row")
     pitch = t.stride(0) if rows > 1 else heads * dim
-    if pitch < heads * dim:
-        raise ValueError(f"{name}'s row stride is smaller than its rows")
+    if not heads * dim <= pitch <= _MOST:
+        raise ValueError(f"{name}'s row stride is smaller than its rows, or more than an int counts")
     return rows, heads, pitch
 
 
@@ -765,11 +777,12 @@ def gemv_kv_attend(Q, cache, table, seq_lens, starts=None, *, scale=None, window
     left as they were.  workspace: a device tensor of at least
     ``kv_attend_workspace_size(...)`` bytes, allocated here through torch when
     not given."""
-    torch = _torch_runtime
     fn = _entry(_ATTEND, Q.dtype)
+    if not (-_MOST <= window <= _MOST and -_MOST <= sinks <= _MOST):
+        raise ValueError("window and sinks must be what an int holds")
     rows, q_heads, ldq = _heads(Q, "Q", cache)
     if out is None:
-        out = torch.empty((rows, q_heads, cache.dim), dtype=Q.dtype, device=Q.device)
+        out = _empty((rows, q_heads, cache.dim), Q.dtype, Q.device, stream)
         ldo = q_heads * cache.dim
     else:
         if out.dtype is not Q.dtype or out.shape != Q.shape:
@@ -783,7 +796,7 @@ def gemv_kv_attend(Q, cache, table, seq_lens, starts=None, *, scale=None, window
             raise ValueError("workspace must be a contiguous tensor on the cache's device")
         need = workspace.numel() * workspace.element_size()
     elif need:
-        workspace = torch.empty(need // 4, dtype=_F32, device=Q.device)
+        workspace = _empty(need // 4, _F32, Q.device, stream)
     _call(cache._device, stream, fn, cache._ref, Q.data_ptr(), ldq, out.data_ptr(), ldo, q_heads, rows,
           ctypes.byref(batch), cache.dim ** -0.5 if scale is None else scale, window, sinks,
           workspace.data_ptr() if workspace is not None else None, need)

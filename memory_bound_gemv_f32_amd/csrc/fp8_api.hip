@@ -21,6 +21,7 @@ bool aligned(const void* p, int n) { return (uintptr_t)p % n == 0; }
 
 gemv_status_t launch(const void* fn, dim3 grid, int threads, int lds_bytes, void** argv,
                      hipStream_t stream) {
+    if ((uint64_t)grid.x * threads > 0xffffffffu) return GEMV_ERROR_INVALID_VALUE;  // more than a launch holds
     return finish(hipLaunchKernel(fn, grid, dim3((unsigned)threads), argv, (size_t)lds_bytes, stream));
 }
 
@@ -36,6 +37,9 @@ using Split16 = Split<64, 16, 3>;
 constexpr int kFewTokens = 16, kFewRows = 8192, kFewWaves = 16, kFewBlocks = 2;
 constexpr int kExactTokens = 32;  // up to so many, every result takes the exact steps
 constexpr int64_t kUnits = 256, kEnoughTiles = 192;
+// Of one launch, whose threads a 32-bit number counts: rows of W and tokens of
+// the product, wavefronts of the quantiser.
+constexpr int kMostRows = 1 << 20, kMostTokens = 1 << 16, kMostUnits = 1 << 25;
 
 // A kernel and what its launch needs.
 struct Tiled {
@@ -109,12 +113,21 @@ gemv_status_t quantise(const typename D::storage* X, int ldx, uint8_t* Q, int ld
     int64_t ldx64 = ldx, ldq64 = ldq, lds64 = lds;
     if (block_rows == 1) {
         int per_row = (int)ceil_div(K, 512);
-        int64_t units = (int64_t)rows * per_row;
-        const int64_t grid = ceil_div(units, fp8dev::kQuantWaves);
-        if (grid > 0x7fffffff) return GEMV_ERROR_INVALID_VALUE;
+        int64_t units = 0;
         void* argv[] = {&X, &ldx64, &Q, &ldq64, &scale, &lds64, &units, &per_row, &K};
-        return launch((const void*)&fp8dev::fp8_quantise_rows_kernel<D>, dim3((unsigned)grid),
-                      fp8dev::kQuantWaves * 64, 0, argv, stream);
+        const int most = kMostUnits / per_row;  // rows of a launch
+        for (int r = 0, n; r < rows; r += n) {
+            n = rows - r < most ? rows - r : most;
+            units = (int64_t)n * per_row;
+            const gemv_status_t st =
+                launch((const void*)&fp8dev::fp8_quantise_rows_kernel<D>,
+                       dim3((unsigned)ceil_div(units, fp8dev::kQuantWaves)), fp8dev::kQuantWaves * 64, 0, argv, stream);
+            if (st != GEMV_SUCCESS) return st;
+            X += n * ldx64;
+            Q += n * ldq64;
+            scale += n * lds64;
+        }
+        return GEMV_SUCCESS;
     }
     const dim3 grid((unsigned)ceil_div(K, GEMV_FP8_BLOCK), (unsigned)ceil_div(rows, GEMV_FP8_BLOCK));
     if (grid.y > 65535) return GEMV_ERROR_INVALID_VALUE;
@@ -142,35 +155,43 @@ gemv_status_t product(const uint8_t* W, int ldw, const float* w_scale, int ldws,
     // 32-bit offsets within 8 rows)
     const bool direct = K % 16 == 0 && ldw % 16 == 0 && ldx % 16 == 0 && aligned(W, 16) &&
                         aligned(X, 16) && ldw < (1 << 28) && ldx < (1 << 28);
-    int row_tiles = 0, tokens = nvec;
-    void* argv[] = {&W,    &ldw64, &w_scale, &ldws64, &X, &ldx64,  &x_scale, &ldxs64,
-                    &bias, &Y,     &ldy64,   &M,      &K, &tokens, &row_tiles};
     // few tokens of few rows: a workgroup for each 16 rows reads W straight into
     // registers (16 x 4096 x 4096: 7.6 us against 7.9 in LDS; 16 x 8192 x 4096: 13.2
     // against 12.0).  Also the empty sum, and scales too far apart for the
     // tiles' 32-bit offsets.
-    if ((nvec <= kFewTokens && M < kFewRows) || K == 0 || ldws >= (1 << 26) || ldxs >= (1 << 26)) {
-        constexpr int kMostTokens = 65535 * 16;  // of one launch
-        for (int t = 0; t < nvec; t += tokens) {
+    const bool few = (nvec <= kFewTokens && M < kFewRows) || K == 0 || ldws >= (1 << 26) || ldxs >= (1 << 26);
+    for (int m = 0, rows; m < M; m += rows) {
+        rows = M - m < kMostRows ? M - m : kMostRows;
+        for (int t = 0, tokens; t < nvec; t += tokens) {
             tokens = nvec - t < kMostTokens ? nvec - t : kMostTokens;
-            const dim3 grid((unsigned)ceil_div(M, 16), (unsigned)ceil_div(tokens, 16));
-            const gemv_status_t st =
-                launch((const void*)&fp8dev::fp8_few_kernel<O, kFewWaves, kFewBlocks>, grid, kFewWaves * 64, 0,
-                       argv, stream);
-            if (st != GEMV_SUCCESS) return st;
+            const uint8_t *w = W, *x = X;
+            const float *ws = w_scale, *xs = x_scale, *add = bias;
             if (K > 0) {
-                X += tokens * ldx64;
-                x_scale += tokens * ldxs64;
+                w += m * ldw64;
+                ws += m / GEMV_FP8_BLOCK * ldws64;
+                x += t * ldx64;
+                xs += t * ldxs64;
             }
-            Y += tokens * ldy64;
+            if (bias != nullptr) add += m;
+            typename O::storage* y = Y + t * ldy64 + m;
+            int row_tiles = 0;
+            void* argv[] = {&w,   &ldw64, &ws,    &ldws64, &x, &ldx64,  &xs,       &ldxs64,
+                            &add, &y,     &ldy64, &rows,   &K, &tokens, &row_tiles};
+            gemv_status_t st;
+            if (few) {
+                const dim3 grid((unsigned)ceil_div(rows, 16), (unsigned)ceil_div(tokens, 16));
+                st = launch((const void*)&fp8dev::fp8_few_kernel<O, kFewWaves, kFewBlocks>, grid, kFewWaves * 64, 0,
+                            argv, stream);
+            } else {
+                const Tiled k = tiled_kernel<O>(rows, tokens, direct);
+                row_tiles = (int)ceil_div(rows, k.block_m);
+                st = launch(k.fn, dim3((unsigned)(row_tiles * ceil_div(tokens, k.block_n))), k.threads, k.lds_bytes,
+                            argv, stream);
+            }
+            if (st != GEMV_SUCCESS) return st;
         }
-        return GEMV_SUCCESS;
     }
-    const Tiled k = tiled_kernel<O>(M, nvec, direct);
-    row_tiles = (int)ceil_div(M, k.block_m);
-    const int64_t grid = row_tiles * ceil_div(nvec, k.block_n);
-    if (grid > 0x7fffffff) return GEMV_ERROR_INVALID_VALUE;
-    return launch(k.fn, dim3((unsigned)grid), k.threads, k.lds_bytes, argv, stream);
+    return GEMV_SUCCESS;
 }
 
 }  // namespace

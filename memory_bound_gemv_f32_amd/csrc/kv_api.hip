@@ -23,6 +23,7 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 bool aligned(const void* p, int n) { return (uintptr_t)p % n == 0; }
 
 gemv_status_t launch(const void* fn, dim3 grid, int threads, void** argv, hipStream_t stream) {
+    if ((uint64_t)grid.x * threads > 0xffffffffu) return GEMV_ERROR_INVALID_VALUE;  // more than a launch holds
     return finish(hipLaunchKernel(fn, grid, dim3((unsigned)threads), argv, 0, stream));
 }
 

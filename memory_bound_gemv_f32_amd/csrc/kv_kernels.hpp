@@ -418,12 +418,12 @@ __device__ __forceinline__ Span span_of(const Attend& p, int min_pos, int max_po
     int end = max_pos + 1 < len ? max_pos + 1 : len;
     end = end < p.capacity ? end : p.capacity;
     Span s;
-    s.high = end > 0 ? (end + kChunk - 1) / kChunk : 0;
+    s.high = end > 0 ? (end - 1) / kChunk + 1 : 0;
     s.low = 0;
     s.first = 0;
     if (p.window > 0 && min_pos >= p.window) {
         s.low = (min_pos - p.window + 1) / kChunk;
-        const int sinks = (p.sinks + (kChunk - 1)) / kChunk;
+        const int sinks = p.sinks / kChunk + (p.sinks % kChunk != 0);
         s.first = sinks < s.low ? sinks : s.low;
     }
     if (s.low > s.high) s.low = s.high;

@@ -286,3 +286,38 @@ def test_refusals():
         lg.gemv_fp8_quantise(x, out=torch.empty(4, 299, dtype=torch.uint8, device="cuda"))
     with pytest.raises(ValueError):
         lg.gemv_fp8_quantise(x, scale=torch.empty(4, 2, device="cuda"))
+
+
+def test_more_rows_and_tokens_than_a_launch_takes():
+    """Sizes that are cut into several launches: the rows at the cuts are right."""
+    g = torch.Generator().manual_seed(5)
+    def bytes8(*shape):
+        return torch.randint(0, 0x70, shape, generator=g, dtype=torch.uint8).cuda()
+    M, K = (1 << 20) + 130, 128
+    W, X = bytes8(M, K), bytes8(3, K)
+    ws = torch.exp2(torch.randint(-3, 3, (-(-M // 128), 1), generator=g).float()).cuda()
+    xs = torch.ones(3, 1, device="cuda")
+    bias = torch.randn(M, generator=g).cuda()
+    y = lg.gemv_fp8(W, ws, X, xs, bias)
+    at = slice((1 << 20) - 256, M)
+    f8 = lambda t: t.view(torch.float8_e4m3fn)
+    want, size = product(f8(W[at]), ws[at.start // 128:], f8(X), xs, bias[at])
+    assert_close(y[:, at], want, product_bound(size, want, K, torch.float32))
+    n = (1 << 16) + 5
+    X, xs = bytes8(n, K), torch.exp2(torch.randint(-3, 3, (n, 1), generator=g).float()).cuda()
+    W, ws = W[:70], ws[:1]
+    y = lg.gemv_fp8(W, ws, X, xs)
+    at = slice((1 << 16) - 40, n)
+    want, size = product(f8(W), ws, f8(X[at]), xs[at])
+    assert_close(y[at], want, product_bound(size, want, K, torch.float32))
+    b = torch.randn(30, generator=g).cuda()
+    y = lg.gemv_fp8(W[:30, :0], ws[:, :0], X[:, :0], xs[:, :0], b)
+    assert torch.equal(y, b.expand(n, 30))
+    rows = (1 << 25) + 7
+    x = torch.zeros(rows, 16, dtype=torch.float16, device="cuda")
+    tail = torch.randn(40, 16, generator=g).to(torch.float16).cuda()
+    x[-40:] = tail
+    q, s = lg.gemv_fp8_quantise(x)
+    wq, wsc = quantise(tail, 1)
+    assert torch.equal(s[-40:].cpu(), torch.as_tensor(wsc, dtype=torch.float32)) and np.array_equal(decode(q[-40:]), wq)
+    assert (s[:-40] == 2.0 ** -126).all()

@@ -517,3 +517,56 @@ def test_calls_on_other_streams():
     torch.cuda.synchronize()
     for y in got:
         assert torch.equal(y, want)
+
+
+def test_call_on_a_given_stream_takes_its_memory_there():
+    """With ``stream`` the result and the workspace come from that stream's
+    memory, so that what else has had them, or has them next, is in order."""
+    side = torch.cuda.Stream()
+    cache = filled(64, 2, 64, 256, INT8, 3)
+    table = torch.arange(64, dtype=torch.int32, device="cuda")[None]
+    lens = torch.tensor([64 * 256], dtype=torch.int32, device="cuda")
+    q = values(1, 1, 8, 64, BF16)
+    need = lg.kv_attend_workspace_size(cache, 8, 1, 1, 64)
+    assert need > 0
+    want = lg.gemv_kv_attend(q, cache, table, lens)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    got = lg.gemv_kv_attend(q, cache, table, lens, stream=side)
+    x = torch.randn(2, 256, device="cuda")
+    torch.cuda.synchronize()
+    held = lg.gemv_fp8_quantise(x, stream=side)
+    weight = lg.gemv_fp8_quantise(x, 128, stream=side)
+    y = lg.gemv_fp8(*weight, *held, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    assert torch.equal(y, lg.gemv_fp8(*weight, *held))
+    own = [s for s in torch.cuda.memory_snapshot() if s["stream"] == side.cuda_stream]
+    for t in (got, *held, *weight, y):
+        assert any(s["address"] <= t.data_ptr() < s["address"] + s["total_size"] for s in own)
+    assert sum(s["total_size"] for s in own) >= need
+
+
+def test_attend_lengths_and_sinks_up_to_an_int():
+    """Positions up to 2^31 - 2 (one page that the whole table repeats), and
+    sinks that cover everything."""
+    cache = filled(1, 2, 64, 256, INT8, 4)
+    q = values(2, 1, 4, 64, F16)
+    top = 2**31 - 1
+    wide = torch.zeros(1, 2**31 // 256, dtype=torch.int32, device="cuda")
+    lens = torch.tensor([top], dtype=torch.int32, device="cuda")
+    here = torch.tensor([top % 256], dtype=torch.int32, device="cuda")
+    # the same tokens at positions 155 .. 254 of the page
+    got = lg.gemv_kv_attend(q, cache, wide, lens, window=100)
+    want = lg.gemv_kv_attend(q, cache, wide[:, :1].contiguous(), here, window=100)
+    assert torch.equal(got, want)
+    table = torch.zeros(1, 4, dtype=torch.int32, device="cuda")
+    lens[0] = 1000
+    want = lg.gemv_kv_attend(q, cache, table, lens)
+    for sinks in (1000, top - 64, top):
+        got = lg.gemv_kv_attend(q, cache, table, lens, window=70, sinks=sinks)
+        # (the same chunks in the same order)
+        assert torch.equal(got, want), sinks
+    for kw in (dict(window=2**31), dict(sinks=2**32 + 5), dict(window=5 - 2**32)):
+        with pytest.raises(ValueError):
+            lg.gemv_kv_attend(q, cache, table, lens, **kw)
