@@ -647,6 +647,9 @@ __global__ __launch_bounds__(kWavesOf<WS> * 64, DIM <= 128 ? 2 : 1) void kv_atte
         const bool whole = __all(there == kBlock) && hi <= min_pos &&
                            (p.window == 0 || max_pos - lo < p.window || hi < p.sinks);
 
+        // a wavefront that has products goes before one that weighs, whose vector
+        // instructions fit between (prompts up to 4 %)
+        if constexpr (WS == 1) __builtin_amdgcn_s_setprio(1);
         f32x4 s[RT][4];
 #pragma unroll
         for (int tt = 0; tt < 4; ++tt) {
@@ -666,6 +669,7 @@ __global__ __launch_bounds__(kWavesOf<WS> * 64, DIM <= 128 ? 2 : 1) void kv_atte
             load_k(it + WS, then, ahead);
             if (it + 2 * WS < end) next = look_up(it + 2 * WS);
         }
+        if constexpr (WS == 1) __builtin_amdgcn_s_setprio(0);
         // a block's keys have one scale, so the largest score of the lane's 16
         // is the largest product times it (a scale is not negative; a negative
         // softmax scale has been given to Q)
@@ -744,6 +748,7 @@ __global__ __launch_bounds__(kWavesOf<WS> * 64, DIM <= 128 ? 2 : 1) void kv_atte
 #pragma unroll
             for (int u = 0; u < kTiles; ++u) in.v[u] = first_bytes(in.v[u], there);
         }
+        if constexpr (WS == 1) __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int u = 0; u < kTiles; ++u) {
             const quad a0 = widen8<F, TF16>(in.v[u][0], in.v[u][1]), a1 = widen8<F, TF16>(in.v[u][2], in.v[u][3]);
@@ -753,6 +758,7 @@ __global__ __launch_bounds__(kWavesOf<WS> * 64, DIM <= 128 ? 2 : 1) void kv_atte
                 o[i][u] = gemvdev::mma_16x16x32(TF16{}, a1, pb[i][1], o[i][u]);
             }
         }
+        if constexpr (WS == 1) __builtin_amdgcn_s_setprio(0);
         now = then;
         it += WS;
         if (!kAhead && more) load_v(it, now, ahead);
