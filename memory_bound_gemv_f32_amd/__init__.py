@@ -527,13 +527,14 @@ def _call(dev, stream, fn, *args):
         raise GemvError(rc, fn.__name__)
 
 
-def _empty(shape, dtype, device, stream):
-    """Memory for a call on ``stream`` (None: the current one): allocated
-    there, so that whoever had it, or has it next, is ordered with the call."""
+def _empty(near, shape, dtype, stream):
+    """Memory on ``near``'s device for a call on ``stream`` (None: the current
+    one): allocated there, so that whoever had it, or has it next, is ordered
+    with the call."""
     if stream is None:
-        return _torch_runtime.empty(shape, dtype=dtype, device=device)
+        return near.new_empty(shape, dtype=dtype)
     with _torch_runtime.cuda.stream(stream):
-        return _torch_runtime.empty(shape, dtype=dtype, device=device)
+        return near.new_empty(shape, dtype=dtype)
 
 
 def _rows(t, name, dev):
@@ -570,7 +571,6 @@ def gemv_fp8_quantise(X, block_rows: int = 1, out=None, scale=None, *, stream=No
     stride) held in e4m3 with a float32 scale for every ``block_rows`` rows (1
     for activations, 128 for weights) and 128 columns.  Q is float8_e4m3fn
     (rows, K), scale (ceil(rows / block_rows), ceil(K / 128))."""
-    torch = _torch_runtime
     if block_rows != 1 and block_rows != FP8_BLOCK:
         raise ValueError("block_rows must be 1 or 128")
     fn = _entry(_QUANTISE, X.dtype)
@@ -578,7 +578,7 @@ def gemv_fp8_quantise(X, block_rows: int = 1, out=None, scale=None, *, stream=No
     rows, K, ldx = _rows(X, "X", dev)
     lines, blocks = -(-rows // block_rows), (K + FP8_BLOCK - 1) // FP8_BLOCK
     if out is None:
-        out = _empty((rows, K), torch.float8_e4m3fn, X.device, stream)
+        out = _empty(X, (rows, K), _torch_runtime.float8_e4m3fn, stream)
         ldq = K
     else:
         if out.dtype not in _E4M3_BYTES:
@@ -587,7 +587,7 @@ def gemv_fp8_quantise(X, block_rows: int = 1, out=None, scale=None, *, stream=No
         if (have, across) != (rows, K):
             raise ValueError("out must have X's shape")
     if scale is None:
-        scale = _empty((lines, blocks), _F32, X.device, stream)
+        scale = _empty(X, (lines, blocks), _F32, stream)
         lds = blocks
     else:
         lds = _scales(scale, "scale", lines, blocks, dev)
@@ -617,7 +617,7 @@ def gemv_fp8(W, w_scale, X, x_scale, bias=None, out=None, *, out_dtype=None, str
         if out_dtype is None:
             out_dtype = _F32
         fn = _entry(_PRODUCT, out_dtype)
-        out = _empty((nvec, M), out_dtype, W.device, stream)
+        out = _empty(W, (nvec, M), out_dtype, stream)
         ldy = M
     else:
         if out_dtype is not None and out.dtype != out_dtype:
@@ -782,7 +782,7 @@ def gemv_kv_attend(Q, cache, table, seq_lens, starts=None, *, scale=None, window
         raise ValueError("window and sinks must be what an int holds")
     rows, q_heads, ldq = _heads(Q, "Q", cache)
     if out is None:
-        out = _empty((rows, q_heads, cache.dim), Q.dtype, Q.device, stream)
+        out = _empty(Q, (rows, q_heads, cache.dim), Q.dtype, stream)
         ldo = q_heads * cache.dim
     else:
         if out.dtype is not Q.dtype or out.shape != Q.shape:
@@ -796,7 +796,7 @@ def gemv_kv_attend(Q, cache, table, seq_lens, starts=None, *, scale=None, window
             raise ValueError("workspace must be a contiguous tensor on the cache's device")
         need = workspace.numel() * workspace.element_size()
     elif need:
-        workspace = _empty(need // 4, _F32, Q.device, stream)
+        workspace = _empty(Q, need // 4, _F32, stream)
     _call(cache._device, stream, fn, cache._ref, Q.data_ptr(), ldq, out.data_ptr(), ldo, q_heads, rows,
           ctypes.byref(batch), cache.dim ** -0.5 if scale is None else scale, window, sinks,
           workspace.data_ptr() if workspace is not None else None, need)
