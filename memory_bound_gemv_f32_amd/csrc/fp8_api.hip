@@ -157,9 +157,12 @@ gemv_status_t product(const uint8_t* W, int ldw, const float* w_scale, int ldws,
                         aligned(X, 16) && ldw < (1 << 28) && ldx < (1 << 28);
     // few tokens of few rows: a workgroup for each 16 rows reads W straight into
     // registers (16 x 4096 x 4096: 7.6 us against 7.9 in LDS; 16 x 8192 x 4096: 13.2
-    // against 12.0).  Also the empty sum, and scales too far apart for the
-    // tiles' 32-bit offsets.
-    const bool few = (nvec <= kFewTokens && M < kFewRows) || K == 0 || ldws >= (1 << 26) || ldxs >= (1 << 26);
+    // against 12.0), and so wherever each of these, with 16 tokens, has a compute
+    // unit (32 x 512 x 8192: 12.1 against 14.3; 30 x 1024 x 11008: 14.7 against
+    // 17.9; 64 x 1024 x 4096: 9.1 against 9.4).  Also the empty sum, and scales too
+    // far apart for the tiles' 32-bit offsets.
+    const bool few = (nvec <= kFewTokens && M < kFewRows) || ceil_div(M, 16) * ceil_div(nvec, 16) <= kUnits ||
+                     K == 0 || ldws >= (1 << 26) || ldxs >= (1 << 26);
     for (int m = 0, rows; m < M; m += rows) {
         rows = M - m < kMostRows ? M - m : kMostRows;
         for (int t = 0, tokens; t < nvec; t += tokens) {

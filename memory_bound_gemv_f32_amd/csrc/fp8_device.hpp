@@ -34,6 +34,21 @@ __device__ __forceinline__ quad load_bytes(const uint8_t* p, int n) {
     return v;
 }
 
+// The 16 bytes from column `at` of a row of K on, one load: near the row's end
+// the row's last 16, moved down.
+__device__ __forceinline__ quad load_end(const uint8_t* row, int64_t at, int K) {
+    if (K < 16) return load_bytes(row + at, (int)(K - at));
+    const int64_t from = at < K - 16 ? at : K - 16;
+    const int down = (int)(at - from);
+    quad v = *reinterpret_cast<const quad_any*>(row + from);
+    if (down & 4) v = quad{v[1], v[2], v[3], 0u};
+    if (down & 8) v = quad{v[2], v[3], 0u, 0u};
+    if (down >= 16) v = quad{0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __builtin_amdgcn_alignbyte(i < 3 ? v[i + 1] : 0u, v[i], down & 3);
+    return v;
+}
+
 // Rounds an fp32 result to the output type (to nearest even).
 __device__ __forceinline__ float narrow(TF32, float v) { return v; }
 __device__ __forceinline__ uint16_t narrow(TF16, float v) {

@@ -192,20 +192,18 @@ __device__ __forceinline__ i32x8 join(quad lo, quad hi) {
 // The lane's 32 bytes of a block that starts at column k of the row at p.
 __device__ __forceinline__ i32x8 load_block(const uint8_t* p, int k, int group, int K) {
     const uint8_t* at = p + k + 16 * group;
-    const int n = K - k - 16 * group;
     if (K - k >= kScaleBlock)
         return join(*reinterpret_cast<const quad_any*>(at),
                     *reinterpret_cast<const quad_any*>(at + 64));
-    return join(load_bytes(at, n), load_bytes(at + 64, n - 64));
+    return join(load_end(p, (int64_t)k + 16 * group, K), load_end(p, (int64_t)k + 16 * group + 64, K));
 }
 
-// Four neighbouring results of a token, from row m on; `vec`: they may be
-// stored at once.
+// Four neighbouring results of a token, from row m on, at any alignment.
 template <class O>
-__device__ __forceinline__ void store_row4(void* Y, int64_t at, int m, int M, bool vec, f32x4 v) {
+__device__ __forceinline__ void store_row4(void* Y, int64_t at, int m, int M, f32x4 v) {
     typename O::storage* y = static_cast<typename O::storage*>(Y) + at + m;
-    if (vec && m + 4 <= M) {
-        struct alignas(4 * O::bytes) Four {
+    if (m + 4 <= M) {
+        struct __attribute__((packed, aligned(O::bytes))) Four {
             typename O::storage v[4];
         };
         *reinterpret_cast<Four*>(y) = Four{{narrow(O{}, v[0]), narrow(O{}, v[1]), narrow(O{}, v[2]), narrow(O{}, v[3])}};
@@ -271,7 +269,7 @@ __global__ __launch_bounds__(W * 64) void fp8_few_kernel(
     if (bias)
 #pragma unroll
         for (int n = 0; n < 4; ++n) v[n] += bias[m + n < M ? m + n : M - 1];
-    store_row4<O>(Y, (int64_t)(t0 + r) * ldy, m, M, ldy % 4 == 0 && (uintptr_t)Y % (4 * O::bytes) == 0, v);
+    store_row4<O>(Y, (int64_t)(t0 + r) * ldy, m, M, v);
 }
 
 // ---------------------------------------------------------------------------
@@ -288,8 +286,8 @@ __global__ __launch_bounds__(W * 64) void fp8_few_kernel(
 // each block's sum, waited for each other in turn.)
 //
 // DIRECT, for aligned rows of whole 16-byte pieces; anything else passes
-// through registers, byte by byte where a piece is not whole or not all of the
-// row: 2000 x 4096 x 4112 bf16 50 us, 2000 x 4096 x 4100 102.
+// through registers, one block ahead: 2000 x 4096 x 4112 bf16 50 us, 2000 x 4096
+// x 4100 86.
 //
 // 4096 x 14336 x 4096 bf16 takes 266 to 286 us from box to box (1.7 to 1.8
 // PFLOP/s; the library's largest product of e4m3 without block scales reaches
@@ -369,10 +367,10 @@ __device__ __forceinline__ f32x4 block_sum(const Operand<false>& a, const Operan
 // The 16-byte piece at byte `piece` of block b of a row of K bytes, from any
 // address; what lies behind the row reads as zero.
 __device__ __forceinline__ quad piece_of(const uint8_t* row, int b, int piece, int K) {
-    const uint8_t* at = row + (int64_t)b * kScaleBlock + piece;
-    const int left = K - b * kScaleBlock;  // uniform: of the row, from the block on
-    if (left >= kScaleBlock) return *reinterpret_cast<const quad_any*>(at);
-    return load_bytes(at, left - piece);
+    const int64_t at = (int64_t)b * kScaleBlock + piece;
+    // (uniform)
+    if (K - b * kScaleBlock >= kScaleBlock) return *reinterpret_cast<const quad_any*>(row + at);
+    return load_end(row, at, K);
 }
 
 // A last block of fewer columns, in whole pieces, loaded straight into LDS: the
@@ -655,14 +653,13 @@ __global__ __launch_bounds__(C::kWaves * 64, DIRECT ? C::kOccupancy : 2) void fp
     }
     __syncthreads();
     constexpr int kPer = 16 / O::bytes, kAcross = C::BM / kPer;  // a lane's values, the lanes of a token
-    const bool vec = ldy % kPer == 0 && (uintptr_t)Y % 16 == 0;
     const int m = threadIdx.x % kAcross * kPer;
     const int left_m = M - row0 - m;
     for (int t = threadIdx.x / kAcross; t < C::BN && t0 + t < T; t += C::kWaves * 64 / kAcross) {
         const uint8_t* from = lds + t * kPitch + m * O::bytes;
         S* to = static_cast<S*>(Y) + (int64_t)(t0 + t) * ldy + row0 + m;
-        if (vec && left_m >= kPer)
-            *reinterpret_cast<quad*>(to) = *reinterpret_cast<const quad*>(from);
+        if (left_m >= kPer)
+            *reinterpret_cast<quad_any*>(to) = *reinterpret_cast<const quad*>(from);
         else
             for (int e = 0; e < kPer && e < left_m; ++e) to[e] = reinterpret_cast<const S*>(from)[e];
     }
@@ -846,7 +843,6 @@ __global__ __launch_bounds__(C::kWaves * 64) void fp8_split_kernel(
         for (int j = 0; j < C::NN; ++j)
             *reinterpret_cast<f32x4*>(sums + (ks * C::BN + wn + 16 * j + r) * C::kPitch + wm + 16 * i + 4 * g) = acc[i][j];
     __syncthreads();
-    const bool vec = ldy % 4 == 0 && (uintptr_t)Y % (4 * O::bytes) == 0;
     constexpr int kLine = C::BM / 4;  // lanes of a token
     for (int e = threadIdx.x; e < C::BN * kLine; e += C::kWaves * 64) {
         const int t = e / kLine, m = e % kLine * 4;
@@ -857,7 +853,7 @@ __global__ __launch_bounds__(C::kWaves * 64) void fp8_split_kernel(
         if (bias)
 #pragma unroll
             for (int n = 0; n < 4; ++n) v[n] += bias[row0 + m + n < M ? row0 + m + n : M - 1];
-        store_row4<O>(Y, (int64_t)(t0 + t) * ldy, row0 + m, M, vec, v);
+        store_row4<O>(Y, (int64_t)(t0 + t) * ldy, row0 + m, M, v);
     }
 }
 
