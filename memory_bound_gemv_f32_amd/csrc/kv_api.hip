@@ -89,7 +89,12 @@ struct Mapping {
 // sequence of 131071 tokens, 8 heads: 59 | 58 | 54 | 56 | 51 with splits of 8 | 12
 // | 16 | 24 | 32; 64 sequences of up to 8192: 127 | 113 | 120 | 114 | 137.  The
 // longest contexts and largest batches get longer ones, so that the workspace
-// stays at 8192 workgroups' rows.
+// stays at 8192 workgroups' rows.  Wavefronts with rows of their own (prompts) have
+// many rows, whose partial results cost a write and a read each, so they are split
+// only into one round of workgroups, four of theirs to a compute unit (256 tokens over 16384,
+// 32 heads: 154 us in splits of 12, 126 in one round; 9 x 29 over up to 42563, 5
+// heads: 83 and 54), and not at all once a quarter of that has a workgroup.
+constexpr int64_t kOwnSlots = 1024, kLeastOwnSplit = 4;
 constexpr int64_t kLeastSplit = 8, kOneRoundSplit = 32, kSplit = 12, kSlots = 512, kMostWorkgroups = 8192;
 
 Mapping map_attend(int q_heads, int heads, int dim, int rows, int sequences, bool one_each, int64_t capacity,
@@ -112,13 +117,14 @@ Mapping map_attend(int q_heads, int heads, int dim, int rows, int sequences, boo
         if (in_window < chunks) chunks = in_window;
     }
     const int64_t all = m.places * heads * chunks;
-    int64_t each = ceil_div(all, kSlots);
-    each = each > kOneRoundSplit ? kSplit : each < kLeastSplit ? kLeastSplit : each;
+    const bool own = m.waves_share == 1;
+    const int64_t least = own ? kLeastOwnSplit : kLeastSplit;
+    int64_t each = ceil_div(all, own ? kOwnSlots : kSlots);
+    each = !own && each > kOneRoundSplit ? kSplit : each < least ? least : each;
     if (each < ceil_div(all, kMostWorkgroups)) each = ceil_div(all, kMostWorkgroups);
     if (each < ceil_div(chunks, kvdev::kMaxSplits)) each = ceil_div(chunks, kvdev::kMaxSplits);
-    // a split that would save little; many rows, whose partial results cost more than they save once
-    // half the slots have a workgroup
-    if (chunks < 2 * kLeastSplit || (m.waves_share == 1 && m.places * heads >= kSlots / 2)) each = chunks;
+    // (a single split would save little)
+    if (chunks < 2 * least || (own && m.places * heads >= kOwnSlots / 4)) each = chunks;
     m.splits = each > 0 ? (int)ceil_div(chunks, each) : 1;
     if (m.splits < 1) m.splits = 1;
     m.split_chunks = (int)each;

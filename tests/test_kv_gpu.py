@@ -570,3 +570,17 @@ def test_attend_lengths_and_sinks_up_to_an_int():
     for kw in (dict(window=2**31), dict(sinks=2**32 + 5), dict(window=5 - 2**32)):
         with pytest.raises(ValueError):
             lg.gemv_kv_attend(q, cache, table, lens, **kw)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (600, 20)])
+def test_attend_prompts_split_over_tokens(dim, window, sinks):
+    """Wavefronts with rows of their own whose tokens several workgroups share;
+    a short sequence beside a long one."""
+    batch = Batch([1500, 3, 790], [45, 3, 60], 64, np.random.default_rng(dim))
+    cache = filled(batch.pages, 1, dim, 64, INT8, 1)
+    table = batch.tensors()[0]
+    assert lg.kv_attend_workspace_size(cache, 2, batch.rows, 3, table.shape[1], one_each=False, window=window,
+                                       sinks=sinks) > 0
+    for form, dtype in ((INT8, F16), (E4M3, BF16)):
+        check_attend(batch, 1, 2, dim, 64, form, dtype, window=window, sinks=sinks, seed=dim)
