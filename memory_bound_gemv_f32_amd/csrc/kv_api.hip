@@ -94,7 +94,7 @@ struct Mapping {
 // only into one round of workgroups, four of theirs to a compute unit (256 tokens over 16384,
 // 32 heads: 154 us in splits of 12, 126 in one round; 9 x 29 over up to 42563, 5
 // heads: 83 and 54), and not at all once a quarter of that has a workgroup.
-constexpr int64_t kOwnSlots = 1024, kLeastOwnSplit = 4;
+constexpr int64_t kOwnSlots = 1024, kLeastLongSplit = 4;
 constexpr int64_t kLeastSplit = 8, kOneRoundSplit = 32, kSplit = 12, kSlots = 512, kMostWorkgroups = 8192;
 
 Mapping map_attend(int q_heads, int heads, int dim, int rows, int sequences, bool one_each, int64_t capacity,
@@ -118,13 +118,15 @@ Mapping map_attend(int q_heads, int heads, int dim, int rows, int sequences, boo
     }
     const int64_t all = m.places * heads * chunks;
     const bool own = m.waves_share == 1;
-    const int64_t least = own ? kLeastOwnSplit : kLeastSplit;
+    // (a chunk of dim 256 takes long: 1 x 28767 tokens, one head, 23.6 us in splits of
+    // 8 chunks, 19.5 of 4; 4 x 4000, 4 heads, 20.8 and 16.6)
+    const int64_t least = own || dim > 128 ? kLeastLongSplit : kLeastSplit;
     int64_t each = ceil_div(all, own ? kOwnSlots : kSlots);
     each = !own && each > kOneRoundSplit ? kSplit : each < least ? least : each;
     if (each < ceil_div(all, kMostWorkgroups)) each = ceil_div(all, kMostWorkgroups);
     if (each < ceil_div(chunks, kvdev::kMaxSplits)) each = ceil_div(chunks, kvdev::kMaxSplits);
     // (a single split would save little)
-    if (chunks < 2 * least || (own && m.places * heads >= kOwnSlots / 4)) each = chunks;
+    if (chunks < 2 * (own ? kLeastLongSplit : kLeastSplit) || (own && m.places * heads >= kOwnSlots / 4)) each = chunks;
     m.splits = each > 0 ? (int)ceil_div(chunks, each) : 1;
     if (m.splits < 1) m.splits = 1;
     m.split_chunks = (int)each;
