@@ -300,8 +300,8 @@ __global__ __launch_bounds__(64) void kv_append_kernel(Cache c, Batch q,
 // its join (5.3 TB/s), 64 sequences of up to 8192 113 us (4.9 TB/s), 4 with a
 // window of 512 10.9 us, which is latency.  Prompts are bound by the vector ALUs,
 // which widen K and V for every 32 rows and take 7 instructions to each
-// matrix-core one: 2160 tokens over contexts of up to 4096, 32 heads, 167 to 178
-// us, 635 to 590 TFLOP/s.  (Wider row tiles would share the widening, but 32
+// matrix-core one: 2160 tokens over contexts of up to 4096, 32 heads, 161 to 178
+// us, 660 to 590 TFLOP/s.  (Wider row tiles would share the widening, but 32
 // rows of dim 128 fill 235 registers as it is.)
 //
 // K and V are widened exactly (e4m3 and int8 both fit fp16 and bf16); a
