@@ -15,10 +15,12 @@ using kvdev::Int8;
 using kvdev::TBF16;
 using kvdev::TF16;
 using kvdev::TF32;
+using kvplan::capacity_of;
+using kvplan::map_attend;
+using kvplan::Mapping;
+using kvplan::workspace_of;
 
 static_assert(GEMV_KV_BLOCK == kvdev::kBlock, "the header states the block");
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 bool aligned(const void* p, int n) { return (uintptr_t)p % n == 0; }
 
@@ -69,86 +71,6 @@ gemv_status_t append(int dim, const kvdev::Cache& c, const kvdev::Batch& q, cons
                      : dim == 128 ? (const void*)&kvdev::kv_append_kernel<D, F, 128>
                                   : (const void*)&kvdev::kv_append_kernel<D, F, 256>;
     return launch(fn, dim3((unsigned)places, (unsigned)c.heads, 2), 64, argv, stream);
-}
-
-// How an attention call is mapped: the rows of a workgroup, whether its
-// wavefronts share them, and how many workgroups share a row tile's tokens.
-struct Mapping {
-    int row_tiles;     // 16-row tiles of a wavefront
-    int waves_share;   // 4 or 8: so many wavefronts take the chunks of the same rows in turn; 1: own rows each
-    int group_rows;    // rows of a workgroup
-    int place_rows;    // rows of it that can be there
-    int splits, split_chunks;
-    int64_t places;
-};
-
-// A split is a workgroup's work.  Where all of it fits the 512 slots (two
-// workgroups for each compute unit) in splits of at most 32 chunks (2048 tokens),
-// that many, of at least 8 (less is mostly start-up); else splits of 12, short
-// enough that the last round of workgroups is not long.  Measured, us: one
-// sequence of 131071 tokens, 8 heads: 59 | 58 | 54 | 56 | 51 with splits of 8 | 12
-// | 16 | 24 | 32; 64 sequences of up to 8192: 127 | 113 | 120 | 114 | 137.  The
-// longest contexts and largest batches get longer ones, so that the workspace
-// stays at 8192 workgroups' rows.  Wavefronts with rows of their own (prompts) have
-// many rows, whose partial results cost a write and a read each, so they are split
-// only into one round of workgroups, four of theirs to a compute unit (256 tokens over 16384,
-// 32 heads: 154 us in splits of 12, 126 in one round; 9 x 29 over up to 42563, 5
-// heads: 83 and 54), and not at all once a quarter of that has a workgroup.
-constexpr int64_t kOwnSlots = 1024, kLeastLongSplit = 4;
-constexpr int64_t kLeastSplit = 8, kOneRoundSplit = 32, kSplit = 12, kSlots = 512, kMostWorkgroups = 8192;
-
-Mapping map_attend(int q_heads, int heads, int dim, int rows, int sequences, bool one_each, int64_t capacity,
-                   int window, int sinks) {
-    Mapping m;
-    const int group = q_heads / heads;
-    const int64_t per_sequence = one_each ? group : ceil_div((int64_t)rows * group, sequences);
-    m.waves_share = per_sequence <= 32 ? 4 : 1;
-    m.row_tiles = per_sequence <= 16 || dim > 128 ? 1 : 2;  // (two of dim 256 would not fit the registers)
-    m.group_rows = 16 * m.row_tiles * (m.waves_share == 1 ? kvdev::kOwnWaves : 1);
-    m.places = one_each ? sequences * ceil_div(group, m.group_rows)
-                        : (int64_t)rows * group / m.group_rows + sequences;
-    m.place_rows = one_each && group < m.group_rows ? group : m.group_rows;
-    // chunks that a row tile can see
-    int64_t chunks = ceil_div(capacity, kvdev::kChunk);
-    if (window > 0) {
-        const int64_t tokens = ceil_div(m.group_rows, group) + 1;
-        const int64_t in_window = ceil_div((int64_t)window + tokens, kvdev::kChunk) + 1 +
-                                  ceil_div(sinks, kvdev::kChunk);
-        if (in_window < chunks) chunks = in_window;
-    }
-    const int64_t all = m.places * heads * chunks;
-    const bool own = m.waves_share == 1;
-    // (a chunk of dim 256 takes long: 1 x 28767 tokens, one head, 23.6 us in splits of
-    // 8 chunks, 19.5 of 4; 4 x 4000, 4 heads, 20.8 and 16.6)
-    const int64_t least = own || dim > 128 ? kLeastLongSplit : kLeastSplit;
-    int64_t each = ceil_div(all, own ? kOwnSlots : kSlots);
-    each = !own && each > kOneRoundSplit ? kSplit : each < least ? least : each;
-    if (each < ceil_div(all, kMostWorkgroups)) each = ceil_div(all, kMostWorkgroups);
-    if (each < ceil_div(chunks, kvdev::kMaxSplits)) each = ceil_div(chunks, kvdev::kMaxSplits);
-    // (a single split would save little)
-    if (chunks < 2 * (own ? kLeastLongSplit : kLeastSplit) || (own && m.places * heads >= kOwnSlots / 4)) each = chunks;
-    m.splits = each > 0 ? (int)ceil_div(chunks, each) : 1;
-    if (m.splits < 1) m.splits = 1;
-    m.split_chunks = (int)each;
-    // No more than a workgroup for each compute unit, and latency is all: eight
-    // wavefronts (of dim 256 too large for the registers) halve the chunks that wait
-    // for each other (4 sequences, window 512: 13.8 us with four, 12.2 with eight;
-    // 4 x 4000 tokens, in two launches: 13.7 and 13.2).
-    if (dim <= 128 && m.waves_share == 4 && m.row_tiles == 1 && each > 4 &&
-        m.places * heads * m.splits <= kSlots / 2)
-        m.waves_share = 8;
-    return m;
-}
-
-size_t workspace_of(const Mapping& m, int heads, int dim) {
-    if (m.splits == 1) return 0;
-    const size_t parts = (size_t)m.places * heads * m.splits * m.place_rows;
-    return (parts * (dim + 2) * sizeof(float) + 15) / 16 * 16;
-}
-
-int64_t capacity_of(int64_t table_width, int page_size) {
-    const int64_t n = table_width * page_size;
-    return n < 0x7fffffff ? n : 0x7fffffff;
 }
 
 template <class T, class F, int DIM>

@@ -10,6 +10,7 @@
 #pragma once
 
 #include "fp8_device.hpp"
+#include "kv_plan.hpp"
 
 namespace kvdev {
 
@@ -22,7 +23,7 @@ using fp8dev::TF16;
 using fp8dev::TF32;
 using fp8dev::widen;
 
-constexpr int kBlock = 16;  // tokens that share a scale
+using kvplan::kBlock;
 
 // The two 8-bit formats: the largest magnitude that a scale maps to.
 struct Int8 {
@@ -386,11 +387,11 @@ __device__ __forceinline__ quad load_once(const uint8_t* p) {
 __device__ __forceinline__ float finite_base(float m) { return m == -__builtin_inff() ? 0.0f : m; }
 constexpr float kSlack = 8.0f;
 
-constexpr int kChunk = 64;    // tokens of a step: four blocks
-// Wavefronts of a workgroup: 4 or 8 that share their rows, or 2 with rows of their
-// own (4 of those would read the same bytes more often from the same cache, but
-// leave fewer and longer workgroups: 176 us against 183 for four prompts of up to 1024 tokens).
-constexpr int kShareWaves = 4, kOwnWaves = 2;
+using kvplan::kChunk;
+using kvplan::kMaxSplits;
+using kvplan::kOwnWaves;
+using kvplan::kShareWaves;
+using kvplan::Span;
 template <int WS>
 constexpr int kWavesOf = WS == 1 ? kOwnWaves : WS;
 
@@ -418,27 +419,9 @@ struct Attend {
     float* partial;     // see partial_at
 };
 
-// What a row tile sees: chunks [0, first) hold the first tokens that stay
-// visible, [low, high) the window (or everything up to the last row).
-struct Span {
-    int first, low, high;
-    __device__ __forceinline__ int count() const { return first + high - low; }
-    __device__ __forceinline__ int chunk(int i) const { return i < first ? i : i - first + low; }
-};
+// What a row tile sees of the sequence's tokens.
 __device__ __forceinline__ Span span_of(const Attend& p, int min_pos, int max_pos, int len) {
-    int end = max_pos + 1 < len ? max_pos + 1 : len;
-    end = end < p.capacity ? end : p.capacity;
-    Span s;
-    s.high = end > 0 ? (end - 1) / kChunk + 1 : 0;
-    s.low = 0;
-    s.first = 0;
-    if (p.window > 0 && min_pos >= p.window) {
-        s.low = (min_pos - p.window + 1) / kChunk;
-        const int sinks = p.sinks / kChunk + (p.sinks % kChunk != 0);
-        s.first = sinks < s.low ? sinks : s.low;
-    }
-    if (s.low > s.high) s.low = s.high;
-    return s;
+    return kvplan::span_of(p.window, p.sinks, p.capacity, min_pos, max_pos, len);
 }
 
 // Rows of a sequence that a workgroup takes: from row r0 on.
@@ -847,7 +830,6 @@ __global__ __launch_bounds__(kWavesOf<WS> * 64, DIM <= 128 ? 2 : 1) void kv_atte
 // of its wavefronts): the splits' maxima and sums give each its weight, then the
 // wavefronts add the weighted rows in turn and join in LDS, in a fixed order.
 // Bound by latency: 4.5 us for 32 rows of 64 splits, 7.0 for 2048 rows of up to 11.
-constexpr int kMaxSplits = 512;
 template <class T, int DIM, int R, int RW>
 __global__ __launch_bounds__(kShareWaves * 64) void kv_join_kernel(Attend p, int64_t places) {
     constexpr int kPer = DIM / 64;
