@@ -845,7 +845,8 @@ __global__ __launch_bounds__(kShareWaves * 64) void kv_join_kernel(Attend p, int
     // the splits that its wavefront's rows have (split 0 always leaves its rows)
     const int r0 = t.r0 + r / RW * RW, last = (r0 + RW < t.rows ? r0 + RW : t.rows) - 1;
     const int chunks = span_of(p, t.first + r0 / p.group, t.first + last / p.group, t.len).count();
-    const int splits = chunks > p.split_chunks ? (chunks + p.split_chunks - 1) / p.split_chunks : 1;
+    int splits = chunks > p.split_chunks ? (chunks + p.split_chunks - 1) / p.split_chunks : 1;
+    splits = splits < p.splits ? splits : p.splits;  // (the partial results end there)
     const Partial in = partial_at<DIM>(p, places, (place * c.heads + head) * p.splits);
     // every wavefront reduces the maxima and sums for itself
     float top = -__builtin_inff();

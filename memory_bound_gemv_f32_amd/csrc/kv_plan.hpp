@@ -28,7 +28,9 @@ struct Span {
     constexpr int chunk(int i) const { return i < first ? i : i - first + low; }
 };
 // Of rows at positions min_pos to max_pos of a sequence of len tokens, whose row
-// of the table can hold `capacity` of them.
+// of the table can hold `capacity` of them: tokens past that are not there, so
+// no chunk lies past it, whatever the length says, and there are no more chunks
+// than map_attend counts.
 constexpr Span span_of(int window, int sinks, int capacity, int min_pos, int max_pos, int len) {
     int end = max_pos + 1 < len ? max_pos + 1 : len;
     end = end < capacity ? end : capacity;
@@ -36,10 +38,10 @@ constexpr Span span_of(int window, int sinks, int capacity, int min_pos, int max
     s.high = end > 0 ? (end - 1) / kChunk + 1 : 0;
     if (window > 0 && min_pos >= window) {
         s.low = (min_pos - window + 1) / kChunk;
+        if (s.low > s.high) s.low = s.high;
         const int in_sinks = sinks / kChunk + (sinks % kChunk != 0);
         s.first = in_sinks < s.low ? in_sinks : s.low;
     }
-    if (s.low > s.high) s.low = s.high;
     return s;
 }
 

@@ -1,0 +1,45 @@
+"""The attention over the paged 8-bit cache at the ends of its range, against
+the reference in 64 bits (needs a GPU)."""
+
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import memory_bound_gemv_f32_amd as lg
+from fp8_helpers import Batch
+from test_kv_gpu import BF16, E4M3, F16, INT8, check_attend, filled, values
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+@pytest.mark.parametrize("new", [1, 3, 70])
+@pytest.mark.parametrize("window,sinks", [(16, 4), (500, 40), (16, 4000), (300, 10 ** 6), (2000, 130), (0, 0)])
+def test_sequences_longer_than_their_table(window, sinks, new):
+    """Tokens past a sequence's row of the table are not there: under a window
+    with first tokens that stay visible too, in calls that are split over their
+    tokens and in calls that are not."""
+    for width, lens in ((16, [10000, 700, 1030]), (32, [2500, 2049, 90]), (1, [200, 64, 33])):
+        batch = Batch(lens, [min(new, n) for n in lens], 64, np.random.default_rng(width))
+        for form, dtype in ((INT8, BF16), (E4M3, F16)):
+            check_attend(batch, 2, 4, 128, 64, form, dtype, window=window, sinks=sinks, one_each=new == 1,
+                         table=batch.table[:, :width].copy())
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (16, 4), (16, 2 ** 31 - 1)])
+def test_a_table_of_no_pages(window, sinks):
+    cache = filled(4, 2, 128, 64, INT8, 1)
+    table = torch.zeros(2, 0, dtype=torch.int32, device="cuda")
+    for lens in ([100, 5], [2 ** 31 - 1, 1]):
+        lens = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        for starts, rows in ((None, 2), (torch.tensor([0, 3, 4], dtype=torch.int32, device="cuda"), 4)):
+            out = torch.full((rows, 8, 128), 9.0, dtype=F16, device="cuda")
+            lg.gemv_kv_attend(values(1, rows, 8, 128, F16), cache, table, lens, starts, window=window, sinks=sinks, out=out)
+            assert (out == 0).all()
