@@ -534,8 +534,8 @@ __global__ __launch_bounds__(kWavesOf<WS> * 64, DIM <= 128 ? 2 : 1) void kv_atte
 
     f32x4 o[RT][kTiles];
     float m[RT], l[RT];
-    // the largest finite V scale that the row has seen, and its reciprocal (0
-    // while that is 0): o is in its unit
+    // the largest finite V scale that the row has seen (0 until one is above 0),
+    // and its reciprocal: o is in its unit
     float vref[RT], vinv[RT];
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
@@ -679,8 +679,9 @@ __global__ __launch_bounds__(kWavesOf<WS> * 64, DIM <= 128 ? 2 : 1) void kv_atte
                     scale = max_of_groups(sees != 0 ? finite : 0.0f);
                 }
                 if (__any(scale > vref[i])) {
-                    const float unit = fmaxf(vref[i], scale);
-                    vinv[i] = unit > 0.0f ? 1.0f / unit : 0.0f;
+                    // (of no less than the smallest normal fp32, whose reciprocal is finite)
+                    const float unit = fmaxf(fmaxf(vref[i], scale), fp8dev::kSmallestScale);
+                    vinv[i] = 1.0f / unit;
                     const float down = vref[i] * vinv[i];
 #pragma unroll
                     for (int u = 0; u < kTiles; ++u) o[i][u] *= down;

@@ -43,3 +43,18 @@ def test_a_table_of_no_pages(window, sinks):
             out = torch.full((rows, 8, 128), 9.0, dtype=F16, device="cuda")
             lg.gemv_kv_attend(values(1, rows, 8, 128, F16), cache, table, lens, starts, window=window, sinks=sinks, out=out)
             assert (out == 0).all()
+
+
+@pytest.mark.parametrize("one_each", [True, False])
+@pytest.mark.parametrize("form", [INT8, E4M3])
+def test_value_scales_of_any_size(form, one_each):
+    """A caller's own scales, down to the smallest subnormal fp32 and zero: a
+    block of tiny values in front, alone or behind ordinary ones."""
+    for tiny in (0.0, 2.0 ** -149, 2.0 ** -140, 2.0 ** -128, 2.0 ** -127, 2.0 ** -126):
+        for where in (slice(0, 1), slice(0, None), slice(3, None)):
+            batch = Batch([150, 64], [1, 1] if one_each else [40, 3], 16, np.random.default_rng(3))
+            cache = filled(batch.pages, 1, 64, 16, form, 3)
+            for b in range(2):
+                pages = torch.tensor(batch.table[b][batch.table[b] >= 0][where].astype(np.int64), device="cuda")
+                cache.v_scale[pages] = tiny
+            check_attend(batch, 1, 4, 64, 16, form, BF16, one_each=one_each, cache=cache)
