@@ -678,11 +678,14 @@ __global__ __launch_bounds__(kWavesOf<WS> * 64, DIM <= 128 ? 2 : 1) void kv_atte
                         if (!(sees >> e & 1)) s[i][e >> 2][e & 3] = -__builtin_inff();
                     scale = max_of_groups(sees != 0 ? finite : 0.0f);
                 }
-                if (__any(scale > vref[i])) {
+                // (what follows changes only the rows whose own it is: a row's bits do
+                // not depend on what its neighbours see)
+                const bool grows = scale > vref[i];
+                if (__any(grows)) {
                     // (of no less than the smallest normal fp32, whose reciprocal is finite)
-                    const float unit = fmaxf(fmaxf(vref[i], scale), fp8dev::kSmallestScale);
-                    vinv[i] = 1.0f / unit;
-                    const float down = vref[i] * vinv[i];
+                    const float unit = grows ? fmaxf(scale, fp8dev::kSmallestScale) : vref[i];
+                    vinv[i] = grows ? 1.0f / unit : vinv[i];
+                    const float down = grows ? vref[i] * vinv[i] : 1.0f;
 #pragma unroll
                     for (int u = 0; u < kTiles; ++u) o[i][u] *= down;
                     vref[i] = unit;
@@ -696,8 +699,9 @@ __global__ __launch_bounds__(kWavesOf<WS> * 64, DIM <= 128 ? 2 : 1) void kv_atte
                 // the base of the exponents follows the maximum only where that
                 // has grown past it by kSlack: most chunks leave it, and o and l
                 // with it, as they are, and no weight passes 2^kSlack
-                if (__any(top > m[i] + kSlack)) {
-                    const float to = fmaxf(m[i], top);
+                const bool higher = top > m[i] + kSlack;
+                if (__any(higher)) {
+                    const float to = higher ? top : m[i];
                     const float down = __builtin_amdgcn_exp2f(m[i] - finite_base(to));
                     l[i] *= down;
 #pragma unroll

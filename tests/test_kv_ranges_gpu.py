@@ -58,3 +58,27 @@ def test_value_scales_of_any_size(form, one_each):
                 pages = torch.tensor(batch.table[b][batch.table[b] >= 0][where].astype(np.int64), device="cuda")
                 cache.v_scale[pages] = tiny
             check_attend(batch, 1, 4, 64, 16, form, BF16, one_each=one_each, cache=cache)
+
+
+@pytest.mark.parametrize("new,group", [([30, 1, 1, 1], 1), ([30, 2], 2), ([60, 3], 2)])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_later_tokens_do_not_change_a_rows_bits(dim, new, group):
+    """Of a row that does not see a block not even the rounding depends on it:
+    not where the rows next to it do, in the same step, and find a far larger
+    score or value scale there."""
+    batch = Batch([9 * 64, 70, 70, 70][:len(new)], new, 16, np.random.default_rng(5))
+    for form, dtype in ((INT8, BF16), (E4M3, F16)):
+        cache = filled(batch.pages, 1, dim, 16, form, 5)
+        cache.k_scale.mul_(0.25)
+        Q = values(6, batch.rows, group, dim, dtype)
+        args = (Q, cache, *batch.tensors())
+        plain = lg.gemv_kv_attend(*args)
+        last = int(batch.table[0, 9 * 4 - 1])  # positions 560 to 575, of which rows from new - 16 on see some
+        for name, by in (("k_scale", 64.0), ("v_scale", 64.0), ("v_scale", 2.0 ** 21)):
+            keep = getattr(cache, name)[last].clone()
+            getattr(cache, name)[last] *= by
+            got = lg.gemv_kv_attend(*args)
+            getattr(cache, name)[last] = keep
+            assert not torch.equal(got[new[0] - 16:new[0]], plain[new[0] - 16:new[0]])
+            assert torch.equal(got[:new[0] - 16], plain[:new[0] - 16]), (name, by)
+            assert torch.equal(got[new[0]:], plain[new[0]:]), (name, by)
