@@ -440,9 +440,9 @@ gemv_status_t gemv_kv_append_bf16(const gemv_kv_cache_t *cache, const uint16_t *
  *       only, and not on the lengths), 16-byte aligned; may be NULL where that is
  *       0; contract as for gemv_splitk_*.
  * Q and the cache's bytes enter the products exactly; scores, the softmax and
- * its sums are fp32; a softmax weight times its V scale, over the largest V scale
- * that the row has seen, is rounded to fp16 before it meets V, and the result
- * once to Q's type.  Deterministic: the order in which tokens are joined
+ * its sums are fp32; a softmax weight times its V scale is rounded before it
+ * meets V, to fp16's 11 bits where it is at least 2^-20 of the row's largest
+ * such product and to within 2^-31 of that below, and the result once to Q's type.  Deterministic: the order in which tokens are joined
  * depends on the sizes only.
  * Errors: as for gemv_kv_append_*, plus a q_heads that heads does not divide,
  * rows·q_heads past 2^31 - 1, a negative window or sinks, a scale that is not

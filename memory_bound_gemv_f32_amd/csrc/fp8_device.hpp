@@ -49,6 +49,12 @@ __device__ __forceinline__ quad load_end(const uint8_t* row, int64_t at, int K) 
     return v;
 }
 
+// What follows from v is not kept in registers from before a loop on.
+__device__ __forceinline__ int worked_out_here(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
 // Rounds an fp32 result to the output type (to nearest even).
 __device__ __forceinline__ float narrow(TF32, float v) { return v; }
 __device__ __forceinline__ uint16_t narrow(TF16, float v) {

@@ -338,12 +338,6 @@ __device__ __forceinline__ f32x4 mma_16x16x128(i32x8 a, i32x8 b) {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, zero, 0, 0, 0, 0, 0, 0);
 }
 
-// What follows from v is not kept in registers from before a loop on.
-__device__ __forceinline__ int worked_out_here(int v) {
-    asm volatile("" : "+v"(v));
-    return v;
-}
-
 // An operand of a block as its matrix-core steps take it.
 template <bool EXACT>
 struct Operand;

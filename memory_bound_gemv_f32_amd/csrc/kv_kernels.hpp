@@ -307,10 +307,14 @@ __global__ __launch_bounds__(64) void kv_append_kernel(Cache c, Batch q,
 //
 // K and V are widened exactly (e4m3 and int8 both fit fp16 and bf16); a
 // block's scales are one number a lane: K's multiplies S in fp32, V's
-// multiplies P.  K meets Q in Q's type, P meets V in fp16, whatever Q is: P
-// times its block's V scale over the largest such scale that its row has seen is at most 1,
-// so fp16 holds it with its full 11 bits (bf16 would keep 8), and what falls
-// below fp16's range is 2^-24 of the row's largest term.
+// multiplies P.  K meets Q in Q's type, P meets V in fp16 (11 bits, where bf16
+// keeps 8), whatever Q is: a term, P times its block's V scale, is held in a
+// unit of its row, a power of two that follows the row's largest term: at most 2^-6
+// of it when it is set, and set anew once a term passes 2^14 units.  So terms keep
+// fp16's 11 bits down to 2^-20 of the row's largest, and below that are within half of fp16's
+// smallest step, 2^-31 of it (the sum l counts P in fp32).  The unit follows the
+// terms and not the V scales alone: a block with a large scale and no weight
+// would push the terms that matter out of fp16's range.
 // ---------------------------------------------------------------------------
 
 using fp8dev::bf16x2;
@@ -386,6 +390,17 @@ __device__ __forceinline__ quad load_once(const uint8_t* p) {
 // against 0.
 __device__ __forceinline__ float finite_base(float m) { return m == -__builtin_inff() ? 0.0f : m; }
 constexpr float kSlack = 8.0f;
+// A row's unit in its largest term when it is set, and the largest term in that
+// unit that it is kept for (fp16 ends at 2^16; the factor of 4 is for terms past
+// 2^127, which a caller's scales can make).
+constexpr float kUnitOfLargest = 0x1p-6f, kMostUnits = 0x1p14f;
+// The power of two at or below v, 2^-126 at least, and the reciprocal of one up to 2^126.
+__device__ __forceinline__ float unit_of(float v) {
+    return gemvdev::f32_of(__builtin_bit_cast(uint32_t, fmaxf(v, fp8dev::kSmallestScale)) & 0x7f800000u);
+}
+__device__ __forceinline__ float inverse(float unit) {
+    return gemvdev::f32_of(0x7f000000u - __builtin_bit_cast(uint32_t, unit));
+}
 
 using kvplan::kChunk;
 using kvplan::kMaxSplits;
@@ -461,8 +476,8 @@ __device__ __forceinline__ bool tile_of(const Attend& p, int64_t place, Tile& t)
     return r0 >= 0 && r0 < t.rows;
 }
 
-// splits > 1: each split of a place and head leaves p.rows rows, unnormalised,
-// and their m and l: first all (m, l), then all rows.
+// splits > 1: each split of a place and head leaves p.rows rows, each as the result
+// over its own tokens, and their m and l: first all (m, l), then all rows.
 struct Partial {
     float* ml;
     float* rows;
@@ -534,13 +549,11 @@ __global__ __launch_bounds__(kWavesOf<WS> * 64, DIM <= 128 ? 2 : 1) void kv_atte
 
     f32x4 o[RT][kTiles];
     float m[RT], l[RT];
-    // the largest finite V scale that the row has seen (0 until one is above 0),
-    // and its reciprocal: o is in its unit
-    float vref[RT], vinv[RT];
+    // the unit of the row's terms, relative to the base m of its exponents: o is in it
+    float unit[RT];
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
-        vref[i] = 0.0f;
-        vinv[i] = 0.0f;
+        unit[i] = fp8dev::kSmallestScale;
         m[i] = -__builtin_inff();
         l[i] = 0.0f;
 #pragma unroll
@@ -658,8 +671,8 @@ __global__ __launch_bounds__(kWavesOf<WS> * 64, DIM <= 128 ? 2 : 1) void kv_atte
         // softmax scale has been given to Q)
         const float ks = in.kscale * p.scale;
         const float vs = held ? in.vscale : 0.0f;
-        const float finite = vs < __builtin_inff() ? vs : 0.0f;
-        const float largest = max_of_groups(finite);
+        const bool finite = vs < __builtin_inff();
+        const float vfinite = finite ? vs : 0.0f;
 
         quad pb[RT][2];
         const auto weigh = [&](auto all_seen) {
@@ -667,7 +680,6 @@ __global__ __launch_bounds__(kWavesOf<WS> * 64, DIM <= 128 ? 2 : 1) void kv_atte
 #pragma unroll
             for (int i = 0; i < RT; ++i) {
                 uint32_t sees = 0xffffu;  // tokens of block g that the lane's row sees
-                float scale = largest;    // (of blocks that the row does not see, none)
                 if constexpr (!WHOLE) {
                     const int j = vb * kBlock;
                     sees = first_bits(there) & first_bits(pos[i] + 1 - j);
@@ -676,39 +688,39 @@ __global__ __launch_bounds__(kWavesOf<WS> * 64, DIM <= 128 ? 2 : 1) void kv_atte
 #pragma unroll
                     for (int e = 0; e < kBlock; ++e)
                         if (!(sees >> e & 1)) s[i][e >> 2][e & 3] = -__builtin_inff();
-                    scale = max_of_groups(sees != 0 ? finite : 0.0f);
-                }
-                // (what follows changes only the rows whose own it is: a row's bits do
-                // not depend on what its neighbours see)
-                const bool grows = scale > vref[i];
-                if (__any(grows)) {
-                    // (of no less than the smallest normal fp32, whose reciprocal is finite)
-                    const float unit = grows ? fmaxf(scale, fp8dev::kSmallestScale) : vref[i];
-                    vinv[i] = grows ? 1.0f / unit : vinv[i];
-                    const float down = grows ? vref[i] * vinv[i] : 1.0f;
-#pragma unroll
-                    for (int u = 0; u < kTiles; ++u) o[i][u] *= down;
-                    vref[i] = unit;
                 }
                 float top = s[i][0][0];
 #pragma unroll
                 for (int e = 1; e < kBlock; ++e) top = fmaxf(top, s[i][e >> 2][e & 3]);
                 // (a lane that sees nothing has top = -inf; ks = 0 would make that a NaN)
                 top = WHOLE || sees != 0 ? top * ks : -__builtin_inff();
-                top = max_of_groups(top);
                 // the base of the exponents follows the maximum only where that
                 // has grown past it by kSlack: most chunks leave it, and o and l
                 // with it, as they are, and no weight passes 2^kSlack
-                const bool higher = top > m[i] + kSlack;
-                if (__any(higher)) {
-                    const float to = higher ? top : m[i];
-                    const float down = __builtin_amdgcn_exp2f(m[i] - finite_base(to));
-                    l[i] *= down;
+                const float most = max_of_groups(top);
+                const bool higher = most > m[i] + kSlack;
+                const float to = higher ? most : m[i];
+                const float base = finite_base(to);
+                // the largest term of the lane's block (a scale that is not finite
+                // makes the row NaN by itself)
+                const float own = __builtin_amdgcn_exp2f(top - base) * vfinite;
+                if (__any(higher || own * (1.0f / kMostUnits) > unit[i])) {
+                    // (only the rows whose own it is change: a row's bits do not
+                    // depend on what its neighbours see)
+                    const float term = max_of_groups(own);
+                    const bool grows = higher || term > unit[i] * kMostUnits;
+                    const float down = __builtin_amdgcn_exp2f(m[i] - base);
+                    l[i] *= down;  // (1 where the base stays)
+                    const float kept = unit[i] * down;
+                    if (grows) unit[i] = unit_of(fmaxf(fminf(term, 0x1p127f) * kUnitOfLargest, kept));
+                    const float by = grows ? kept * inverse(unit[i]) : 1.0f;
 #pragma unroll
-                    for (int u = 0; u < kTiles; ++u) o[i][u] *= down;
+                    for (int u = 0; u < kTiles; ++u) o[i][u] *= by;
                     m[i] = to;
                 }
-                const float base = finite_base(m[i]), by = vs * vinv[i];
+                // (a scale so far above the unit that their ratio overflows meets
+                // weights of next to nothing only)
+                const float by = finite ? fminf(vfinite * inverse(unit[i]), 0x1p127f) : vs;
                 float sum = 0.0f;
 #pragma unroll
                 for (int e = 0; e < kBlock; ++e) {
@@ -728,7 +740,9 @@ __global__ __launch_bounds__(kWavesOf<WS> * 64, DIM <= 128 ? 2 : 1) void kv_atte
                 }
             }
         };
-        if (whole)
+        // (heads of 256 always take the masks, which they have the time for: with both
+        // forms their registers do not hold everything)
+        if (whole && DIM <= 128)
             weigh(std::true_type{});
         else
             weigh(std::false_type{});
@@ -759,15 +773,11 @@ __global__ __launch_bounds__(kWavesOf<WS> * 64, DIM <= 128 ? 2 : 1) void kv_atte
     }
 
 #pragma unroll
-    for (int i = 0; i < RT; ++i) {
-        l[i] = sum_of_groups(l[i]);
-#pragma unroll
-        for (int u = 0; u < kTiles; ++u) o[i][u] *= vref[i];
-    }
+    for (int i = 0; i < RT; ++i) l[i] = sum_of_groups(l[i]);
     if constexpr (WS > 1) {
         // the upper half of the wavefronts joins the lower, and so on
         __shared__ f32x4 rows[WS / 2][RT][kTiles][64];
-        __shared__ float stat[WS / 2][RT][2][64];
+        __shared__ float stat[WS / 2][RT][3][64];
 #pragma unroll
         for (int round = WS / 2; round >= 1; round /= 2) {
             const int slot = wave - round;
@@ -777,6 +787,7 @@ __global__ __launch_bounds__(kWavesOf<WS> * 64, DIM <= 128 ? 2 : 1) void kv_atte
                 for (int i = 0; i < RT; ++i) {
                     stat[slot][i][0][lane] = m[i];
                     stat[slot][i][1][lane] = l[i];
+                    stat[slot][i][2][lane] = unit[i];
 #pragma unroll
                     for (int u = 0; u < kTiles; ++u) rows[slot][i][u][lane] = o[i][u];
                 }
@@ -791,23 +802,30 @@ __global__ __launch_bounds__(kWavesOf<WS> * 64, DIM <= 128 ? 2 : 1) void kv_atte
                     const float b = __builtin_amdgcn_exp2f(m2 - base);
                     m[i] = top;
                     l[i] = l[i] * a + stat[wave][i][1][lane] * b;
+                    const float own = unit[i] * a, other = stat[wave][i][2][lane] * b;
+                    unit[i] = unit_of(fmaxf(own, other));
+                    const float in = inverse(unit[i]), by = own * in, by2 = other * in;
 #pragma unroll
-                    for (int u = 0; u < kTiles; ++u) o[i][u] = o[i][u] * a + rows[wave][i][u][lane] * b;
+                    for (int u = 0; u < kTiles; ++u) o[i][u] = o[i][u] * by + rows[wave][i][u][lane] * by2;
                 }
             }
         }
         if (wave != 0) return;
     }
 
+    // (the unit over the sum before o meets either: the result is within V's
+    // range, o in V's unit need not be)
+    float result[RT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) result[i] = l[i] == 0.0f ? 0.0f : unit[i] * (1.0f / l[i]);
     if (p.splits == 1) {
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
             if (r0 + 16 * i + n > last) continue;
-            const float by = l[i] == 0.0f ? 0.0f : 1.0f / l[i];
             uint16_t* dst = p.O + row[i] * p.ldo + (int64_t)qhead[i] * DIM + 4 * g;
 #pragma unroll
             for (int u = 0; u < kTiles; ++u) {
-                const f32x4 x = o[i][u] * by;
+                const f32x4 x = o[i][u] * result[i];
                 fp8dev::u32x2 w;
                 w[0] = pack(T{}, x[0], x[1]);
                 w[1] = pack(T{}, x[2], x[3]);
@@ -827,7 +845,7 @@ __global__ __launch_bounds__(kWavesOf<WS> * 64, DIM <= 128 ? 2 : 1) void kv_atte
         }
 #pragma unroll
         for (int u = 0; u < kTiles; ++u)
-            *reinterpret_cast<f32x4*>(out.rows + (int64_t)r * DIM + 16 * u + 4 * g) = o[i][u];
+            *reinterpret_cast<f32x4*>(out.rows + (int64_t)r * DIM + 16 * u + 4 * g) = o[i][u] * result[i];
     }
 }
 
@@ -861,8 +879,8 @@ __global__ __launch_bounds__(kShareWaves * 64) void kv_join_kernel(Attend p, int
     for (int s = lane; s < splits; s += 64) {
         const float ls = in.ml[(s * p.rows + r) * 2 + 1];
         // a split in which the row sees nothing adds nothing, whatever its row holds
-        const float w = ls == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(in.ml[(s * p.rows + r) * 2] - base);
-        l += ls == 0.0f ? 0.0f : w * ls;
+        const float w = ls == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(in.ml[(s * p.rows + r) * 2] - base) * ls;
+        l += w;
         if (wave == 0) weight[s] = ls == 0.0f ? -1.0f : w;
     }
     l = gemvdev::segment_sum<64>(l);
