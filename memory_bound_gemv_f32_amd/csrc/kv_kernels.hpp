@@ -884,6 +884,7 @@ __global__ __launch_bounds__(kShareWaves * 64) void kv_join_kernel(Attend p, int
         if (wave == 0) weight[s] = ls == 0.0f ? -1.0f : w;
     }
     l = gemvdev::segment_sum<64>(l);
+    const float by = l == 0.0f ? 0.0f : 1.0f / l;
     __syncthreads();
     float o[kPer];
 #pragma unroll
@@ -895,13 +896,12 @@ __global__ __launch_bounds__(kShareWaves * 64) void kv_join_kernel(Attend p, int
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const float x = row[i * 64 + lane];
-            o[i] += w == -1.0f ? 0.0f : x * w;
+            o[i] += w == -1.0f ? 0.0f : x * (w * by);
         }
     }
 #pragma unroll
     for (int i = 0; i < kPer; ++i) part[wave][i * 64 + lane] = o[i];
     __syncthreads();
-    const float by = l == 0.0f ? 0.0f : 1.0f / l;
     const int token = (t.r0 + r) / p.group;
     uint16_t* dst = p.O + ((int64_t)t.start + token) * p.ldo +
                     (int64_t)(head * p.group + (t.r0 + r - token * p.group)) * DIM;
@@ -909,7 +909,7 @@ __global__ __launch_bounds__(kShareWaves * 64) void kv_join_kernel(Attend p, int
         float v = part[0][d];
 #pragma unroll
         for (int w = 1; w < kShareWaves; ++w) v += part[w][d];
-        dst[d] = fp8dev::narrow(T{}, v * by);
+        dst[d] = fp8dev::narrow(T{}, v);
     }
 }
 

@@ -183,3 +183,14 @@ def test_a_long_tail_of_small_weights_counts(lens, new):
         for dtype in (F16, BF16):
             Q = torch.ones(batch.rows, 2, dim, dtype=dtype, device="cuda")
             check_terms(cache, batch, Q, all(m == 1 for m in new))
+
+
+def test_results_near_the_largest_number():
+    """Values near fp32's largest, of which the result is the mean and not the sum."""
+    for form, byte in ((INT8, 127), (E4M3, 0x7E)):
+        for lens, new in (([300, 40], [1, 1]), ([9000], [1]), ([300, 40], [60, 2])):
+            batch = Batch(lens, new, 16, np.random.default_rng(2))
+            cache = filled(batch.pages, 1, 64, 16, form, 2)
+            cache.v.view(torch.uint8).fill_(byte)
+            cache.v_scale.fill_(2.0 ** (120 if form == INT8 else 118))
+            check_terms(cache, batch, values(3, batch.rows, 2, 64, BF16), all(m == 1 for m in new))
