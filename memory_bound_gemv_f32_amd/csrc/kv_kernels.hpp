@@ -484,8 +484,8 @@ struct Partial {
 };
 template <int DIM>
 __device__ __forceinline__ Partial partial_at(const Attend& p, int64_t places, int64_t part) {
-    const int64_t parts = places * p.cache.heads * p.splits;
-    return Partial{p.partial + part * p.rows * 2, p.partial + parts * p.rows * 2 + part * p.rows * DIM};
+    const int64_t rows = places * p.cache.heads * p.splits * p.rows;
+    return Partial{p.partial + part * p.rows * 2, p.partial + kvplan::stats_floats(rows) + part * p.rows * DIM};
 }
 
 // WS > 1: the workgroup's wavefronts take the chunks of one row tile in turn

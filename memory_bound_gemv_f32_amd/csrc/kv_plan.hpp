@@ -116,10 +116,14 @@ inline Mapping map_attend(int q_heads, int heads, int dim, int rows, int sequenc
     return m;
 }
 
+// The workspace holds so many partial rows' maxima and sums, then the rows, which
+// are stored in 16-byte pieces: the first part in floats.
+constexpr int64_t stats_floats(int64_t rows) { return (rows * 2 + 3) / 4 * 4; }
+
 inline size_t workspace_of(const Mapping& m, int heads, int dim) {
     if (m.splits == 1) return 0;
-    const size_t parts = (size_t)m.places * heads * m.splits * m.place_rows;
-    return (parts * (dim + 2) * sizeof(float) + 15) / 16 * 16;
+    const int64_t rows = m.places * heads * m.splits * m.place_rows;
+    return (size_t)(stats_floats(rows) + rows * dim) * sizeof(float);
 }
 
 inline int64_t capacity_of(int64_t table_width, int page_size) {

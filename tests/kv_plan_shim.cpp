@@ -24,4 +24,13 @@ void shim_map(int q_heads, int heads, int dim, int rows, int sequences, int one_
     for (int i = 0; i < 7; ++i) out[i] = all[i];
 }
 
+// floats before the first partial row, workspace bytes
+void shim_workspace(int q_heads, int heads, int dim, int rows, int sequences, int one_each, long long capacity,
+                    int window, int sinks, long long* out) {
+    const kvplan::Mapping m =
+        kvplan::map_attend(q_heads, heads, dim, rows, sequences, one_each != 0, capacity, window, sinks);
+    out[0] = kvplan::stats_floats(m.places * heads * m.splits * m.place_rows);
+    out[1] = (long long)kvplan::workspace_of(m, heads, dim);
+}
+
 }  // extern "C"

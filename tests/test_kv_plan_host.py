@@ -29,6 +29,8 @@ def build_shim(folder) -> ctypes.CDLL:
     lib.shim_map.argtypes = [ctypes.c_int] * 6 + [ctypes.c_longlong] + [ctypes.c_int] * 2 + [
         ctypes.POINTER(ctypes.c_longlong)]
     lib.shim_map.restype = None
+    lib.shim_workspace.argtypes = lib.shim_map.argtypes
+    lib.shim_workspace.restype = None
     return lib
 
 
@@ -114,3 +116,26 @@ def test_no_row_tile_has_more_chunks_than_the_launch(shim):
             first, lo, hi = span(shim, window, sinks, capacity, low, high, length)
             assert first + hi - lo <= m["splits"] * m["split_chunks"], (m, window, sinks, capacity, low, high, length)
     assert split > 500
+
+
+def test_partial_rows_are_aligned_and_fit_the_workspace(shim):
+    """The rows of the workspace start at 16 bytes (they are stored in pieces of
+    that), behind every row's maximum and sum, and end with it."""
+    rng = random.Random(3)
+    odd = 0
+    for _ in range(4000):
+        heads, group, dim = rng.choice((1, 2, 3)), rng.choice((1, 3, 4, 5)), rng.choice((64, 128, 256))
+        sequences, capacity = rng.choice((1, 1, 3, 7)), rng.randrange(0, 1 << 17, 16)
+        one = rng.random() < 0.7
+        rows = sequences if one else sequences * rng.choice((1, 3, 50))
+        args = (heads * group, heads, dim, rows, sequences, one, capacity)
+        m = mapping(shim, *args)
+        if m["splits"] == 1:
+            continue
+        out = (ctypes.c_longlong * 2)()
+        shim.shim_workspace(*args[:5], int(one), capacity, 0, 0, out)
+        parts = m["places"] * heads * m["splits"] * m["place_rows"]
+        odd += parts % 2
+        assert out[0] % 4 == 0 and out[0] >= 2 * parts, (args, m)
+        assert out[1] % 16 == 0 and out[1] == 4 * (out[0] + parts * dim), (args, m)
+    assert odd > 20
