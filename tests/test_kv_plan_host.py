@@ -11,6 +11,8 @@ from pathlib import Path
 
 import pytest
 
+from kv_variants import CASES
+
 TESTS = Path(__file__).resolve().parent
 CHUNK, MAX_SPLITS, MOST = 64, 512, 2 ** 31 - 1
 FIELDS = ("row_tiles", "waves_share", "group_rows", "place_rows", "splits", "split_chunks", "places")
@@ -139,3 +141,18 @@ def test_partial_rows_are_aligned_and_fit_the_workspace(shim):
         assert out[0] % 4 == 0 and out[0] >= 2 * parts, (args, m)
         assert out[1] % 16 == 0 and out[1] == 4 * (out[0] + parts * dim), (args, m)
     assert odd > 20
+
+
+@pytest.mark.parametrize("name", CASES)
+def test_each_mapping_has_its_case(shim, name):
+    """The cases that the GPU tests run against the reference have the mapping
+    that they are there for (heads of 256 have one row tile and no eight wavefronts)."""
+    lens, new, heads, group, page, window, sinks, waves, tiles, split = CASES[name]
+    capacity = -(-max(lens) // page) * page
+    for dim in (64, 128, 256):
+        rows = len(lens) if new is None else sum(new)
+        m = mapping(shim, heads * group, heads, dim, rows, len(lens), new is None, capacity, window, sinks)
+        if dim == 256:
+            assert m["row_tiles"] == 1 and m["waves_share"] == (1 if waves == 1 else 4), m
+        else:
+            assert (m["waves_share"], m["row_tiles"], m["splits"] > 1) == (waves, tiles, split), m
