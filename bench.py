@@ -38,6 +38,7 @@ import argparse
 import json
 import math
 import os
+import re
 import statistics
 import sys
 import time
@@ -129,15 +130,24 @@ def source_code_only(text: str) -> str:
 
 
 def kernel_source_hash() -> str:
-    """Hash of every HIP / host source of the library, comments and layout
-    aside: counter figures taken from one version of the code are not
-    reported for another."""
+    """Hash of the sources that the workloads' kernels are built from, comments
+    and layout aside: gemv_api.hip and what it includes from its folder, not
+    the library's other operators.  Counter figures taken from one version of
+    the code are not reported for another."""
     import hashlib
     csrc = os.path.join(ROOT, "memory_bound_gemv_f32_amd", "csrc")
-    h = hashlib.sha256()
-    for name in sorted(os.listdir(csrc)):
+    code, wanted = {}, ["gemv_api.hip"]
+    while wanted:
+        name = wanted.pop()
+        if name in code:
+            continue
         with open(os.path.join(csrc, name), encoding="utf-8") as f:
-            h.update(name.encode() + b"\0" + source_code_only(f.read()).encode())
+            code[name] = source_code_only(f.read())
+        wanted += [i for i in re.findall(r'#include "([^"]+)"', code[name])
+                   if os.path.exists(os.path.join(csrc, i)) and "/" not in i]
+    h = hashlib.sha256()
+    for name in sorted(code):
+        h.update(name.encode() + b"\0" + code[name].encode())
     return h.hexdigest()[:16]
 
 

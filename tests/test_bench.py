@@ -68,3 +68,24 @@ def test_source_hash_ignores_comments_and_layout():
     assert bench.source_code_only("a = 1; // x") != bench.source_code_only("a = 2; // x")
     assert '"// not a comment"' in bench.source_code_only(code)
     assert bench.source_code_only("x /* a */ y") == "x y"
+
+
+def test_source_hash_is_of_the_workloads_own_kernels(tmp_path, monkeypatch):
+    """Another operator's sources do not take the stored counter figures away;
+    a change to the kernels, in whichever included file, does."""
+    import shutil
+    csrc = tmp_path / "memory_bound_gemv_f32_amd" / "csrc"
+    shutil.copytree(ROOT / "memory_bound_gemv_f32_amd" / "csrc", csrc)
+    before = bench.kernel_source_hash()
+    monkeypatch.setattr(bench, "ROOT", str(tmp_path))
+    assert bench.kernel_source_hash() == before
+    (csrc / "another_api.hip").write_text("int another;\n")
+    with open(csrc / "kv_kernels.hpp", "a") as f:
+        f.write("int one_more;\n")
+    assert bench.kernel_source_hash() == before
+    for name in ("gemv_api.hip", "gemv_kernels.hpp", "gemv_device.hpp", "gemv_plan.hpp"):
+        text = (csrc / name).read_text()
+        (csrc / name).write_text(text + "int one_more;\n")
+        assert bench.kernel_source_hash() != before, name
+        (csrc / name).write_text(text)
+    assert bench.kernel_source_hash() == before
