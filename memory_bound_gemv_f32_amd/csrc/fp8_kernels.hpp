@@ -216,9 +216,12 @@ __device__ __forceinline__ void store_row4(void* Y, int64_t at, int m, int M, f3
 
 // Few tokens of few rows: 16 rows of W by 16 tokens to a workgroup; its
 // wavefronts take the scale blocks in turn, U at a time with all their loads in
-// flight, and add their sums in LDS, in a fixed order.  W, which is read once,
-// goes past the caches.  Bound by latency: 1 x 1024 x 4096 takes 5.4 us, of
-// which W's 4 MiB are 0.9; 1 x 4096 x 4096 5.8, 16 x 4096 x 4096 7.6.
+// flight, and add their sums in LDS, in a fixed order.  W is loaded through the
+// caches: several token tiles read it again (past them 30 x 1024 x 11008 takes
+// 14.6 us against 13.3, 4000 x 16 x 11008 17.4 against 13.0), and a single one
+// loses nothing by it (1 x 4096 x 4096 6.2 and 5.8).  Bound by latency: of W
+// from memory, 1 x 1024 x 4096 takes 5.1 us, of which its 4 MiB are 0.9; 16 x
+// 4096 x 4096 7.8.
 template <class O, int W, int U>
 __global__ __launch_bounds__(W * 64) void fp8_few_kernel(
     const uint8_t* A, int64_t lda, const float* as, int64_t ldas, const uint8_t* X, int64_t ldx,
@@ -248,8 +251,7 @@ __global__ __launch_bounds__(W * 64) void fp8_few_kernel(
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t k = (int64_t)(b + u * W) * kScaleBlock + 16 * group;
-            af[u] = join(__builtin_nontemporal_load(reinterpret_cast<const quad_any*>(a + k)),
-                         __builtin_nontemporal_load(reinterpret_cast<const quad_any*>(a + k + 64)));
+            af[u] = join(*reinterpret_cast<const quad_any*>(a + k), *reinterpret_cast<const quad_any*>(a + k + 64));
             xf[u] = join(*reinterpret_cast<const quad_any*>(x + k), *reinterpret_cast<const quad_any*>(x + k + 64));
             s[u] = asr[b + u * W] * xsr[b + u * W];
         }
