@@ -309,20 +309,24 @@ __global__ __launch_bounds__(W * 64) void fp8_few_kernel(
 // to LDS from `lds` on in lane order (base and lds uniform).  The caller waits
 // (wait_loads): written as instructions, because the compiler, which cannot
 // tell the stages apart, would wait for all of them before it reads any.
-// There is no register result; m0 holds the LDS address and nothing else here
-// uses it.
+// There is no register result.  m0, which takes the LDS address, is declared as
+// written; the compiler warns that it keeps that register to itself and will not
+// preserve it, which nothing here asks for.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void lds_load16(const uint8_t* base, uint32_t offset, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                  :
                  : "s"(lds), "v"(offset), "s"(base)
-                 : "memory");
+                 : "m0", "memory");
 }
 __device__ __forceinline__ void lds_load4(const float* base, uint32_t offset, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
                  :
                  : "s"(lds), "v"(offset), "s"(base)
-                 : "memory");
+                 : "m0", "memory");
 }
+#pragma clang diagnostic pop
 template <int N>
 __device__ __forceinline__ void wait_loads() {
     asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");

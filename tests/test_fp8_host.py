@@ -155,3 +155,16 @@ def test_kernels_use_no_scratch(kernels):
         waves = max(1, -(-int(f["max_flat_workgroup_size"]) // 256))
         assert int(f["vgpr_count"]) <= 512 // waves, name
         assert int(f["group_segment_fixed_size"]) <= 160 * 1024, name
+
+
+def test_assembly_declares_what_it_writes():
+    """Every statement that writes m0 names it, and memory, to the compiler."""
+    found = 0
+    for source in sorted(lg.LIBRARY.parent.joinpath("csrc").iterdir()):
+        for statement in re.findall(r"asm volatile\((.*?)\);", source.read_text(), re.S):
+            text, *operands = statement.split("\n")
+            if re.search(r"s_mov_b32 m0", text):
+                found += 1
+                clobbers = " ".join(operands).rsplit(":", 1)[1]
+                assert '"m0"' in clobbers and '"memory"' in clobbers, (source.name, statement)
+    assert found == 2
