@@ -408,7 +408,8 @@ typedef struct {
  * place of it (pages that several sequences or places share are for reading).
  * Errors: GEMV_ERROR_INVALID_VALUE for a cache or batch that is not as above,
  * negative sizes, a pitch below heads·dim, rows != sequences without starts, a
- * NULL or misaligned pointer. */
+ * NULL or misaligned pointer, and more blocks than one launch holds (never with
+ * up to 2^24 sequences and 2^28 rows). */
 gemv_status_t gemv_kv_append_f32(const gemv_kv_cache_t *cache, const float *K,
                                 int ldk, const float *V, int ldv, int rows,
                                 const gemv_kv_batch_t *batch,
@@ -446,7 +447,9 @@ gemv_status_t gemv_kv_append_bf16(const gemv_kv_cache_t *cache, const uint16_t *
  * depends on the sizes only.
  * Errors: as for gemv_kv_append_*, plus a q_heads that heads does not divide,
  * rows·q_heads past 2^31 - 1, a negative window or sinks, a scale that is not
- * finite, and a workspace that is too small. */
+ * finite, a workspace that is too small, and more workgroups than one launch
+ * holds (never with sequences·heads up to 2^22 and rows·q_heads up to 2^29).
+ * gemv_kv_attend_workspace_size refuses the sizes that a call refuses. */
 gemv_status_t gemv_kv_attend_workspace_size(int q_heads, int heads, int dim,
                                             int rows, int sequences,
                                             int one_each, int table_width,

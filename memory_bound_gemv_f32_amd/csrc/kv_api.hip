@@ -32,13 +32,18 @@ gemv_status_t launch(const void* fn, dim3 grid, int threads, void** argv, hipStr
 // The head dims and page sizes that there are kernels for.
 bool known_dim(int dim) { return dim == 64 || dim == 128 || dim == 256; }
 
+bool known_page(int page_size) {
+    return page_size == 16 || page_size == 32 || page_size == 64 || page_size == 128 || page_size == 256;
+}
+constexpr int kMostHeads = 65535;
+
 bool make_cache(const gemv_kv_cache_t* in, kvdev::Cache* out) {
     if (in == nullptr || (in->format != GEMV_KV_INT8 && in->format != GEMV_KV_E4M3) ||
-        in->pages < 1 || in->heads < 1 || in->heads > 65535 || !known_dim(in->dim))
+        in->pages < 1 || in->heads < 1 || in->heads > kMostHeads || !known_dim(in->dim) ||
+        !known_page(in->page_size))
         return false;
     int log2 = 0;
-    while (log2 < 4 && (GEMV_KV_BLOCK << log2) != in->page_size) ++log2;
-    if ((GEMV_KV_BLOCK << log2) != in->page_size) return false;
+    while ((GEMV_KV_BLOCK << log2) != in->page_size) ++log2;
     if (in->k == nullptr || in->v == nullptr || in->k_scale == nullptr || in->v_scale == nullptr ||
         !aligned(in->k, 16) || !aligned(in->v, 16) || !aligned(in->k_scale, 4) || !aligned(in->v_scale, 4))
         return false;
@@ -77,7 +82,6 @@ template <class T, class F, int DIM>
 gemv_status_t attend(const Mapping& m, Attend& p, hipStream_t stream) {
     int64_t places = m.places;
     const int64_t grid = places * p.cache.heads * p.splits;
-    if (grid > 0x7fffffff) return GEMV_ERROR_INVALID_VALUE;
     void* argv[] = {&p, &places};
     constexpr int kTwo = DIM <= 128 ? 2 : 1;
     constexpr int kSmall = DIM <= 128 ? DIM : 128;  // (dim 256 has no eight, see map_attend)
@@ -85,8 +89,7 @@ gemv_status_t attend(const Mapping& m, Attend& p, hipStream_t stream) {
                      : m.row_tiles == 2 ? (const void*)&kvdev::kv_attend_kernel<T, F, DIM, kTwo, 4>
                      : m.waves_share == 8 ? (const void*)&kvdev::kv_attend_kernel<T, F, kSmall, 1, 8>
                                           : (const void*)&kvdev::kv_attend_kernel<T, F, DIM, 1, 4>;
-    const gemv_status_t st = launch(fn, dim3((unsigned)grid),
-                                    64 * (m.waves_share == 1 ? kvdev::kOwnWaves : m.waves_share), argv, stream);
+    const gemv_status_t st = launch(fn, dim3((unsigned)grid), 64 * kvplan::waves_of(m), argv, stream);
     if (st != GEMV_SUCCESS || p.splits == 1) return st;
     const void* join = m.waves_share == 1 ? (const void*)&kvdev::kv_join_kernel<T, DIM, 16 * kvdev::kOwnWaves * kTwo, 16 * kTwo>
                        : m.row_tiles == 2 ? (const void*)&kvdev::kv_join_kernel<T, DIM, 16 * kTwo, 16 * kTwo>
@@ -134,6 +137,7 @@ gemv_status_t attend(const gemv_kv_cache_t* cache, const uint16_t* Q, int ldq, u
     const int64_t capacity = capacity_of(batch->table_width, cache->page_size);
     const Mapping m = map_attend(q_heads, p.cache.heads, cache->dim, rows, p.batch.count, batch->starts == nullptr,
                                  capacity, window, sinks);
+    if (!kvplan::launchable(m, p.cache.heads)) return GEMV_ERROR_INVALID_VALUE;
     const size_t need = workspace_of(m, p.cache.heads, cache->dim);
     if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 16)))
         return GEMV_ERROR_INVALID_VALUE;
@@ -160,15 +164,18 @@ gemv_status_t attend(const gemv_kv_cache_t* cache, const uint16_t* Q, int ldq, u
 extern "C" gemv_status_t gemv_kv_attend_workspace_size(int q_heads, int heads, int dim, int rows,
                                                        int sequences, int one_each, int table_width,
                                                        int page_size, int window, int sinks, size_t* bytes) {
-    if (bytes == nullptr || heads < 1 || q_heads < 1 || q_heads % heads != 0 || !known_dim(dim) ||
-        rows < 0 || sequences < 0 || (one_each && rows != sequences) || table_width < 0 ||
-        page_size < GEMV_KV_BLOCK || window < 0 || sinks < 0)
+    if (bytes == nullptr || heads < 1 || heads > kMostHeads || q_heads < 1 || q_heads % heads != 0 ||
+        !known_dim(dim) || rows < 0 || sequences < 0 || (one_each && rows != sequences) || table_width < 0 ||
+        !known_page(page_size) || (int64_t)rows * q_heads > 0x7fffffff || window < 0 || sinks < 0)
         return GEMV_ERROR_INVALID_VALUE;
-    *bytes = rows == 0 || sequences == 0
-                 ? 0
-                 : workspace_of(map_attend(q_heads, heads, dim, rows, sequences, one_each != 0,
-                                           capacity_of(table_width, page_size), window, sinks),
-                                heads, dim);
+    size_t need = 0;
+    if (rows > 0 && sequences > 0) {
+        const Mapping m = map_attend(q_heads, heads, dim, rows, sequences, one_each != 0,
+                                     capacity_of(table_width, page_size), window, sinks);
+        if (!kvplan::launchable(m, heads)) return GEMV_ERROR_INVALID_VALUE;
+        need = workspace_of(m, heads, dim);
+    }
+    *bytes = need;
     return GEMV_SUCCESS;
 }
 

@@ -71,6 +71,7 @@ struct Mapping {
 // 32 heads: 154 us in splits of 12, 126 in one round; 9 x 29 over up to 42563, 5
 // heads: 83 and 54), and not at all once a quarter of that has a workgroup.
 constexpr int64_t kOwnSlots = 1024, kLeastLongSplit = 4;
+constexpr int64_t kMostTiles = 0x7fffffff;
 constexpr int64_t kLeastSplit = 8, kOneRoundSplit = 32, kSplit = 12, kSlots = 512, kMostWorkgroups = 8192;
 
 inline Mapping map_attend(int q_heads, int heads, int dim, int rows, int sequences, bool one_each, int64_t capacity,
@@ -91,6 +92,11 @@ inline Mapping map_attend(int q_heads, int heads, int dim, int rows, int sequenc
         const int64_t in_window = ceil_div((int64_t)window + tokens, kChunk) + 1 +
                                   ceil_div(sinks, kChunk);
         if (in_window < chunks) chunks = in_window;
+    }
+    if (m.places * heads > kMostTiles) {  // (launchable refuses it; the products below would overflow)
+        m.splits = 1;
+        m.split_chunks = (int)chunks;
+        return m;
     }
     const int64_t all = m.places * heads * chunks;
     const bool own = m.waves_share == 1;
@@ -114,6 +120,15 @@ inline Mapping map_attend(int q_heads, int heads, int dim, int rows, int sequenc
         m.places * heads * m.splits <= kSlots / 2)
         m.waves_share = 8;
     return m;
+}
+
+// Wavefronts of a workgroup of the attention, and whether its launch and the
+// join's hold all their workgroups and threads.
+constexpr int waves_of(const Mapping& m) { return m.waves_share == 1 ? kOwnWaves : m.waves_share; }
+constexpr bool launchable(const Mapping& m, int heads) {
+    const int64_t tiles = m.places * heads, most = 0xffffffff;
+    return tiles <= kMostTiles && tiles * m.splits <= kMostTiles && tiles * m.splits * waves_of(m) * 64 <= most &&
+           (m.splits == 1 || tiles * kShareWaves * 64 <= most);
 }
 
 // The workspace holds so many partial rows' maxima and sums, then the rows, which

@@ -121,6 +121,34 @@ def test_workspace_size():
     assert last < 1 << 30
 
 
+def test_workspace_size_refuses_what_a_call_refuses():
+    n = ctypes.c_size_t(7)
+    good = dict(q_heads=8, heads=2, dim=128, rows=1, sequences=1, one_each=0, table_width=100, page_size=64, window=0,
+                sinks=0)
+    def size(**kw):
+        return lg.gemv_kv_attend_workspace_size(*{**good, **kw}.values(), ctypes.byref(n))
+    for page in (16, 32, 64, 128, 256):
+        assert size(page_size=page) == 0
+    for bad in (dict(page_size=48), dict(page_size=512), dict(page_size=24), dict(heads=65536, q_heads=65536),
+                dict(rows=1 << 29), dict(rows=1 << 20, q_heads=1 << 12)):
+        assert size(**bad) == BAD, bad
+    # more workgroups than a launch holds: refused by both, whatever the products of the sizes
+    most = 2 ** 31 - 1
+    for many in (dict(sequences=most), dict(sequences=most, heads=65535, q_heads=65535),
+                 dict(sequences=most, heads=65535, q_heads=65535, table_width=most, page_size=256),
+                 dict(sequences=1 << 24, heads=2), dict(sequences=1 << 24, heads=2, table_width=1)):
+        assert size(**many) == BAD, many
+        a = {**good, **many}
+        ld = a["q_heads"] * 128
+        call = lg.gemv_kv_attend_f16(
+            ctypes.byref(cache(heads=a["heads"], page_size=a["page_size"])), P, ld, P, ld, a["q_heads"], 1,
+            ctypes.byref(batch(sequences=a["sequences"], table_width=a["table_width"], table_pitch=a["table_width"])),
+            0.1, 0, 0, P, 1 << 62, None)
+        assert call == BAD, many
+    for many in (dict(sequences=1 << 20, heads=3, q_heads=3), dict(sequences=1 << 20, rows=1 << 25)):
+        assert size(**many) == 0, many
+
+
 @pytest.fixture(scope="module")
 def kernels(tmp_path_factory):
     """Metadata of every kernel of the 8-bit operators in the library: each

@@ -11,6 +11,7 @@ from pathlib import Path
 
 import pytest
 
+import memory_bound_gemv_f32_amd as lg
 from kv_variants import CASES
 
 TESTS = Path(__file__).resolve().parent
@@ -156,3 +157,22 @@ def test_each_mapping_has_its_case(shim, name):
             assert m["row_tiles"] == 1 and m["waves_share"] == (1 if waves == 1 else 4), m
         else:
             assert (m["waves_share"], m["row_tiles"], m["splits"] > 1) == (waves, tiles, split), m
+
+
+def test_sizes_that_one_launch_always_holds():
+    """sequences x heads up to 2^22 and rows x q_heads up to 2^29, as documented."""
+    rng = random.Random(4)
+    n = ctypes.c_size_t()
+    for _ in range(20000):
+        heads = rng.choice((1, 2, 3, 8, 64, 1000, 65535))
+        sequences = rng.choice((1, 7, (1 << 22) // heads, rng.randint(1, (1 << 22) // heads)))
+        group = rng.choice((1, 2, 4, 8, 16, 17, 32, 33, 64, 128, 1000))
+        most = (1 << 29) // (heads * group)
+        one = rng.random() < 0.3 and sequences <= most
+        if most < 1:
+            continue
+        rows = sequences if one else rng.choice((1, most, rng.randint(1, most), min(most, sequences * rng.choice((1, 16, 17, 32, 33)))))
+        rc = lg.gemv_kv_attend_workspace_size(heads * group, heads, rng.choice((64, 128, 256)), rows, sequences, int(one),
+                                              rng.choice((1, 100, 1 << 20, MOST)), rng.choice((16, 256)),
+                                              rng.choice((0, 0, 1000)), rng.choice((0, 70)), ctypes.byref(n))
+        assert rc == 0, (heads, group, rows, sequences, one)
