@@ -38,8 +38,8 @@ constexpr int kFewTokens = 16, kFewRows = 8192, kFewWaves = 16, kFewBlocks = 2;
 constexpr int kExactTokens = 32;  // up to so many, every result takes the exact steps
 constexpr int64_t kUnits = 256, kEnoughTiles = 192;
 // Of one launch, whose threads a 32-bit number counts: rows of W and tokens of
-// the product, wavefronts of the quantiser.
-constexpr int kMostRows = 1 << 20, kMostTokens = 1 << 16, kMostUnits = 1 << 25;
+// the product, wavefronts of the quantiser, columns of its 128 x 128 blocks.
+constexpr int kMostRows = 1 << 20, kMostTokens = 1 << 16, kMostUnits = 1 << 25, kMostColumns = 1 << 29;
 
 // A kernel and what its launch needs.
 struct Tiled {
@@ -129,11 +129,21 @@ gemv_status_t quantise(const typename D::storage* X, int ldx, uint8_t* Q, int ld
         }
         return GEMV_SUCCESS;
     }
-    const dim3 grid((unsigned)ceil_div(K, GEMV_FP8_BLOCK), (unsigned)ceil_div(rows, GEMV_FP8_BLOCK));
-    if (grid.y > 65535) return GEMV_ERROR_INVALID_VALUE;
-    void* argv[] = {&X, &ldx64, &Q, &ldq64, &scale, &lds64, &rows, &K};
-    return launch((const void*)&fp8dev::fp8_quantise_tile_kernel<D>, grid,
-                  fp8dev::kTileWaves * 64, 0, argv, stream);
+    const int64_t lines = ceil_div(rows, GEMV_FP8_BLOCK);
+    if (lines > 65535) return GEMV_ERROR_INVALID_VALUE;
+    int columns = 0;
+    void* argv[] = {&X, &ldx64, &Q, &ldq64, &scale, &lds64, &rows, &columns};
+    for (int k = 0; k < K; k += columns) {
+        columns = K - k < kMostColumns ? K - k : kMostColumns;
+        const dim3 grid((unsigned)ceil_div(columns, GEMV_FP8_BLOCK), (unsigned)lines);
+        const gemv_status_t st = launch((const void*)&fp8dev::fp8_quantise_tile_kernel<D>, grid,
+                                        fp8dev::kTileWaves * 64, 0, argv, stream);
+        if (st != GEMV_SUCCESS) return st;
+        X += columns;
+        Q += columns;
+        scale += columns / GEMV_FP8_BLOCK;  // (whole blocks but for the last launch)
+    }
+    return GEMV_SUCCESS;
 }
 
 template <class O>
