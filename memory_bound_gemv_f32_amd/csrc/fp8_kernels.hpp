@@ -626,7 +626,6 @@ __global__ __launch_bounds__(C::kWaves * 64, DIRECT ? C::kOccupancy : 2) void fp
             change_over();
         }
     }
-    wait_loads<0>();
     // The results go through LDS, so that a token's BM values are stored as
     // one piece (straight from the registers they would be 32-byte pieces).
     wait_loads<0>();

@@ -378,8 +378,10 @@ __device__ __forceinline__ float sum_of_groups(float v) {
     return gemvdev::half_pair_sum32(gemvdev::row_pair_sum16(v));
 }
 
-// 16 bytes of the cache; ONCE: nothing reads them again in this call, so they
-// go past the caches (nontemporal; 7 % of one long sequence's time).
+// 16 bytes of the cache; ONCE: as a rule nothing reads them again in this call
+// (wavefronts share their rows, and there are seldom more of them to a K/V head than
+// one workgroup takes), so they go past the caches (nontemporal; 7 % of one long
+// sequence's time).
 template <bool ONCE>
 __device__ __forceinline__ quad load_once(const uint8_t* p) {
     if constexpr (ONCE) return __builtin_nontemporal_load(reinterpret_cast<const quad*>(p));
