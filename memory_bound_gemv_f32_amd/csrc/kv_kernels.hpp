@@ -886,7 +886,12 @@ __global__ __launch_bounds__(kShareWaves * 64) void kv_join_kernel(Attend p, int
         if (wave == 0) weight[s] = ls == 0.0f ? -1.0f : w;
     }
     l = gemvdev::segment_sum<64>(l);
+    // (over the sum before they meet the rows: a result is within V's range, its
+    // multiple need not be)
     const float by = l == 0.0f ? 0.0f : 1.0f / l;
+    if (wave == 0)
+        for (int s = lane; s < splits; s += 64)
+            if (weight[s] != -1.0f) weight[s] *= by;
     __syncthreads();
     float o[kPer];
 #pragma unroll
@@ -898,7 +903,7 @@ __global__ __launch_bounds__(kShareWaves * 64) void kv_join_kernel(Attend p, int
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const float x = row[i * 64 + lane];
-            o[i] += w == -1.0f ? 0.0f : x * (w * by);
+            o[i] += w == -1.0f ? 0.0f : x * w;
         }
     }
 #pragma unroll
