@@ -177,8 +177,9 @@ __device__ __forceinline__ uint32_t low_bits(int64_t n) {
 // holds K's pieces lane, lane + 64, ... and V's pieces of DIM / 64 neighbouring
 // dims, so that both read runs of elements.  The values are asked for before
 // the page, which they do not need.  Bound by latency for single tokens (64
-// sequences, 8 heads of 128: 6.0 us, of which the bytes are 0.14) and by memory
-// for prompts (14.4 us against 9.9 at a large copy's rate); one wavefront to a
+// sequences, 8 heads of 128: 5.8 us, of which the bytes are 0.14) and by that and memory
+// for prompts (14.4 us against 9.9 at a large copy's rate, the vector ALUs busy for a
+// third of it); one wavefront to a
 // workgroup, because blocks share nothing.
 template <class D, class F, int DIM>
 __global__ __launch_bounds__(64) void kv_append_kernel(Cache c, Batch q,
@@ -297,13 +298,13 @@ __global__ __launch_bounds__(64) void kv_append_kernel(Cache c, Batch q,
 // Nothing passes through LDS or between lanes but the row maximum (once a
 // chunk) and the row sum (once at the end).
 //
-// Single tokens are bound by memory: one sequence of 131071 tokens 50.5 us with
-// its join (5.3 TB/s), 64 sequences of up to 8192 113 us (4.9 TB/s), 4 with a
-// window of 512 10.9 us, which is latency.  Prompts are bound by the vector ALUs,
-// which widen K and V for every 32 rows and take 7 instructions to each
-// matrix-core one: 2160 tokens over contexts of up to 4096, 32 heads, 161 to 178
-// us, 660 to 590 TFLOP/s.  (Wider row tiles would share the widening, but 32
-// rows of dim 128 fill 235 registers as it is.)
+// Single tokens are bound by memory: one sequence of 131071 tokens 50.7 us with
+// its join (5.3 TB/s), 64 sequences of up to 8192 115 us (4.8 TB/s), 4 with a
+// window of 512 10.6 us, which is latency.  Prompts are bound by the vector ALUs,
+// which widen K and V for every 32 rows and take 7 to 8 instructions to each
+// matrix-core one: 2160 tokens over contexts of up to 4096, 32 heads, 161 to 164
+// us, 655 TFLOP/s.  (Wider row tiles would share the widening, but 32 rows of dim
+// 128 fill 237 registers as it is.)
 //
 // K and V are widened exactly (e4m3 and int8 both fit fp16 and bf16); a
 // block's scales are one number a lane: K's multiplies S in fp32, V's
