@@ -45,3 +45,43 @@ def test_append_to_many_sequences(many, form):
     lg.gemv_kv_append(cache, K, V, *batch.tensors())
     plain.append(f64(K), f64(V), batch)
     assert_same_cache(cache, plain)
+
+
+def test_captured_split_calls_replay():
+    """Two captured calls that take a workspace, of single tokens and of a
+    prompt's chunk behind padding rows, replayed in turn while the lengths in
+    device memory grow and eager calls run between: every replay equals the
+    eager call."""
+    rng = np.random.default_rng(1)
+    calls = []
+    for lens, new, pad, window in (([2000, 700], None, 0, 0), ([3000, 90], [70, 9], 5, 1500)):
+        batch = Batch([n + 400 for n in lens], [1] * 2 if new is None else new, 64, rng)
+        cache = filled(batch.pages, 2, 128, 64, E4M3, 1)
+        table, length, starts = batch.tensors(new is not None)
+        length.copy_(torch.tensor(lens, dtype=torch.int32))
+        Q = values(1, batch.rows + pad, 8, 128, BF16)
+        need = lg.kv_attend_workspace_size(cache, 8, len(Q), 2, table.shape[1], one_each=new is None, window=window, sinks=4)
+        assert need > 0
+        def call(out, args=(Q, cache, table, length, starts), window=window):
+            return lg.gemv_kv_attend(*args, window=window, sinks=4, out=out)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        out = torch.full_like(Q, 3.0)
+        with torch.cuda.stream(side):
+            call(out)
+        torch.cuda.current_stream().wait_stream(side)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call(out)
+        calls.append((graph, call, out, Q, length, lens))
+    for step in range(12):
+        for graph, call, out, Q, length, lens in calls:
+            length.copy_(torch.tensor([n + 33 * step for n in lens], dtype=torch.int32))
+            Q.copy_(torch.roll(Q, 1, 0))
+        for graph, *_ in calls:
+            graph.replay()
+        for graph, call, out, Q, length, lens in calls:
+            want = call(torch.full_like(Q, 3.0))
+            assert torch.equal(out, want) and torch.isfinite(want).all(), step
+        if step % 4 == 0:
+            torch.cuda.synchronize()
