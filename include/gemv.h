@@ -8,7 +8,9 @@
  *   y = A·x for few, long rows        gemv_splitk_* (caller's workspace)
  *   y = scale ⊙ (Q·x), int8 Q         gemv_q8_f32 / gemv_q8_f16 / gemv_q8_bf16
  *   e4m3, a scale per block of 128    gemv_fp8_quantise_*, gemv_fp8_* (any number of vectors)
- *   a paged 8-bit key/value cache     gemv_kv_append_*, gemv_kv_attend_*
+ *   4-bit weights with group scales   gemv_q4_f32 / gemv_q4_f16 / gemv_q4_bf16 (any number of vectors)
+ *   norms and rotary positions        gemv_rotary_* (query and key heads, before the append)
+ *   a paged 8-bit key/value cache     gemv_kv_append_*, gemv_kv_attend_*, gemv_kv_attend_shared_*
  *
  * The operation.  Output m is the dot product of row m of A with x (page
  * "SGEMV CUDA代码学习", section "问题定义: 一行一个点积": A is M×K, x is K×1,
@@ -264,6 +266,49 @@ gemv_status_t gemv_q8_bf16(const int8_t *Q, int ldq, const float *scale,
                            int M, int K, hipStream_t stream);
 
 /* ------------------------------------------------------------------------
+ * 4-bit weights with a scale for each row and group of columns: half the bytes
+ * of gemv_q8_*, with scales that follow the weights along a row.
+ *
+ *   Y[t,m] = Σ_g scale[m,g]·Σ_{k in group g} (q[m,k] - zero[m,g])·X[t,k] + bias[m]
+ *
+ * Q      M rows of ceil(K / 2) bytes, row stride ldq bytes (the bytes between
+ *        are never read): column k's q, 0..15, is the low half of byte k / 2
+ *        for even k and the high half for odd k.
+ * group  columns of a group: 32, 64 or 128; a row's last group may be shorter.
+ * scale  M x ceil(K / group) values of X's type, row stride lds.
+ * zero   M x ceil(K / group) bytes, row stride ldz, any value 0..255; or NULL,
+ *        where every zero is 8 (weights from -8 to 7).
+ * X      nvec rows of K elements of the type in the name, row stride ldx >= K;
+ *        nvec is any number >= 0.
+ * bias   M fp32 values, or NULL.
+ * Y      nvec rows of M values of y_dtype, row stride ldy >= M.
+ * q - zero and X enter the products exactly (an fp32 X as three bf16 parts
+ * that add up to it, but for bits below 2^-126); a group's products are summed in fp32,
+ * its sum is scaled and added in fp32, and the result is rounded to Y's type
+ * once.  Deterministic; a vector's result does not depend on the other vectors'
+ * values, but its last bits may depend on how many vectors and rows there are.
+ * 16-byte aligned Q and X with pitches of whole 16 bytes are fastest; any other
+ * layout works.
+ * Errors as for gemv_*, also for another group or y_dtype and a pitch that is
+ * too small.  M == 0 or nvec == 0 enqueues nothing; K == 0 writes the bias (or
+ * 0). */
+gemv_status_t gemv_q4_f32(const uint8_t *Q, int ldq, const float *scale, int lds,
+                          const uint8_t *zero, int ldz, int group,
+                          const float *X, int ldx, const float *bias, void *Y,
+                          gemv_dtype_t y_dtype, int ldy, int M, int K, int nvec,
+                          hipStream_t stream);
+gemv_status_t gemv_q4_f16(const uint8_t *Q, int ldq, const uint16_t *scale,
+                          int lds, const uint8_t *zero, int ldz, int group,
+                          const uint16_t *X, int ldx, const float *bias, void *Y,
+                          gemv_dtype_t y_dtype, int ldy, int M, int K, int nvec,
+                          hipStream_t stream);
+gemv_status_t gemv_q4_bf16(const uint8_t *Q, int ldq, const uint16_t *scale,
+                           int lds, const uint8_t *zero, int ldz, int group,
+                           const uint16_t *X, int ldx, const float *bias,
+                           void *Y, gemv_dtype_t y_dtype, int ldy, int M, int K,
+                           int nvec, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
  * 8-bit floating point with a scale for each block of 128.  Where gemv_q8_*
  * halves the weight bytes with one scale a row, these hold weights and
  * activations in e4m3 (the OCP format: 4 exponent and 3 mantissa bits, largest
@@ -394,6 +439,60 @@ typedef struct {
     const int *starts;            /* [sequences + 1], ascending from 0, or NULL */
 } gemv_kv_batch_t;
 
+/* Norms and rotary positions of the heads of the batch's new tokens, between
+ * the product that gives them and gemv_kv_append_* and gemv_kv_attend_*:
+ *
+ *   n = x·weight / sqrt(mean(x^2) + eps)     over a head's dim values; n = x without a weight
+ *   (a, b) -> magnitude·(a·cos t - b·sin t, b·cos t + a·sin t),  t = position·frequency[i]
+ *
+ * for the pairs i < `pairs` of a head's first 2·pairs values: (n[i], n[i +
+ * pairs]), or (n[2i], n[2i + 1]) where `interleaved` is 1; the values behind
+ * them stay n.  A row's position is its token's place in its sequence, by
+ * seq_lens and starts as the append has it (the batch's table is not read).
+ * Long contexts are a matter of the frequencies and the magnitude.
+ *
+ * A part is rows x heads x dim of one matrix, at x with ldx elements of the
+ * type in the name from row to row (so queries and keys may be columns of one
+ * wider matrix), whose result goes to y, in y_dtype with ldy elements from row
+ * to row.  y may be x where type and pitch are the same; else it must not
+ * overlap any part's x or y.  weight: dim fp32 values, or NULL: no norm.
+ * dim is even and at most GEMV_ROTARY_MAX_DIM, pairs at most dim / 2;
+ * frequency: `pairs` fp32 values (NULL where pairs is 0), finite.
+ * The angle is worked out in 64 bits and keeps fp32's bits of its place in the
+ * turn at every position; squares, products and sums are fp32, and a value is
+ * rounded to y_dtype once.  Rows from starts[sequences] on are neither read nor
+ * written.
+ * Errors: GEMV_ERROR_INVALID_VALUE for sizes that are not as above, another
+ * y_dtype, a pitch below heads·dim, a NULL or misaligned pointer, rows !=
+ * sequences without starts, an eps that is negative or not finite, a magnitude
+ * that is not finite, and more rows or heads than one launch holds (never with
+ * up to 2^25 rows and 65535 heads). */
+#define GEMV_ROTARY_MAX_PARTS 4
+#define GEMV_ROTARY_MAX_DIM 512
+
+typedef struct {
+    const void *x;
+    int ldx;
+    void *y;
+    int ldy;
+    int heads;            /* >= 0 */
+    int y_dtype;          /* gemv_dtype_t */
+    const float *weight;
+} gemv_rotary_part_t;
+
+gemv_status_t gemv_rotary_f32(const gemv_rotary_part_t *parts, int count, int dim,
+                              int rows, const float *frequency, int pairs,
+                              int interleaved, float magnitude, float eps,
+                              const gemv_kv_batch_t *batch, hipStream_t stream);
+gemv_status_t gemv_rotary_f16(const gemv_rotary_part_t *parts, int count, int dim,
+                              int rows, const float *frequency, int pairs,
+                              int interleaved, float magnitude, float eps,
+                              const gemv_kv_batch_t *batch, hipStream_t stream);
+gemv_status_t gemv_rotary_bf16(const gemv_rotary_part_t *parts, int count, int dim,
+                               int rows, const float *frequency, int pairs,
+                               int interleaved, float magnitude, float eps,
+                               const gemv_kv_batch_t *batch, hipStream_t stream);
+
 /* Write the keys and values of the batch's new tokens into the cache.  K and V
  * are rows x heads x dim of the type in the name, ldk and ldv elements
  * from row to row (so they may be columns of one wider matrix).
@@ -469,6 +568,37 @@ gemv_status_t gemv_kv_attend_bf16(const gemv_kv_cache_t *cache, const uint16_t *
                                 float scale, int window, int sinks,
                                 void *workspace, size_t workspace_bytes,
                                 hipStream_t stream);
+
+/* As gemv_kv_attend_*, for a batch whose sequences begin with the same tokens
+ * (a common instruction or document): the first `shared` tokens of every
+ * sequence that has them have the same keys and values.  Their tokens are read
+ * and multiplied once for the whole batch, from the pages that the first row of
+ * the table names, whatever the first sequence's length; a shared token is there
+ * where that row has its page.  (The other rows name a page for each shared token as well, the
+ * same one or a copy: how many of the tokens are taken together is the
+ * library's choice.)  shared == 0 computes what gemv_kv_attend_* does.  Other
+ * arguments, results and errors are gemv_kv_attend_*'s, also for a negative
+ * `shared`; the workspace has its own size. */
+gemv_status_t gemv_kv_attend_shared_workspace_size(int q_heads, int heads, int dim,
+                                                   int rows, int sequences,
+                                                   int one_each, int table_width,
+                                                   int page_size, int window,
+                                                   int sinks, int shared,
+                                                   size_t *bytes);
+gemv_status_t gemv_kv_attend_shared_f16(const gemv_kv_cache_t *cache,
+                                       const uint16_t *Q, int ldq, uint16_t *O,
+                                       int ldo, int q_heads, int rows,
+                                       const gemv_kv_batch_t *batch, float scale,
+                                       int window, int sinks, int shared,
+                                       void *workspace, size_t workspace_bytes,
+                                       hipStream_t stream);
+gemv_status_t gemv_kv_attend_shared_bf16(const gemv_kv_cache_t *cache,
+                                        const uint16_t *Q, int ldq, uint16_t *O,
+                                        int ldo, int q_heads, int rows,
+                                        const gemv_kv_batch_t *batch, float scale,
+                                        int window, int sinks, int shared,
+                                        void *workspace, size_t workspace_bytes,
+                                        hipStream_t stream);
 
 /* ------------------------------------------------------------------------
  * Introspection and testing.  These do not change what the entry points

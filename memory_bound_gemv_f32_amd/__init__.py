@@ -9,15 +9,18 @@ Two levels:
 
 * the C ABI under the same names (``gemv_f32``, ``gemv_f16``, ``gemv_bf16``,
   ``gemv_batched_*``, ``gemv_multi_*``, ``gemv_gate_up_silu_*``,
-  ``gemv_splitk_*``, ``gemv_q8_*``, ``gemv_fp8_*``, ``gemv_kv_*``, ``gemv_plan``,
+  ``gemv_splitk_*``, ``gemv_q8_*``, ``gemv_q4_*``, ``gemv_fp8_*``, ``gemv_rotary_*``,
+  ``gemv_kv_*``, ``gemv_plan``,
   ``gemv_run_family``, ...), taking integer addresses and returning the
   ``gemv_status_t`` code;
 * tensor helpers ``gemv``, ``gemv_batched``, ``gemv_multi``,
   ``gemv_gate_up_silu``, ``gemv_splitk`` and ``gemv_q8`` that check dtype, shape,
   strides and device, call the matching entry point on
   ``torch.cuda.current_stream()`` and raise ``GemvError`` on a failure code;
-  ``gemv_fp8_quantise`` and ``gemv_fp8`` (e4m3 with a scale per block of 128)
-  and ``gemv_kv_append`` and ``gemv_kv_attend`` (a paged 8-bit key/value cache,
+  ``gemv_q4`` (4-bit weights with group scales), ``gemv_fp8_quantise`` and
+  ``gemv_fp8`` (e4m3 with a scale per block of 128), ``gemv_rotary`` (norms and
+  rotary positions of query and key heads; ``rotary_frequencies`` gives the
+  frequencies) and ``gemv_kv_append`` and ``gemv_kv_attend`` (a paged 8-bit key/value cache,
   ``KVCache``) do so on the current stream of their tensors' device.
 
 Layout of the tensor helpers: ``A`` is (M, K) with unit column stride and row
@@ -163,6 +166,12 @@ class KvBatchStruct(ctypes.Structure):
                 ("seq_lens", ctypes.c_void_p), ("starts", ctypes.c_void_p)]
 
 
+class RotaryPartStruct(ctypes.Structure):
+    """gemv_rotary_part_t."""
+    _fields_ = [("x", ctypes.c_void_p), ("ldx", ctypes.c_int), ("y", ctypes.c_void_p), ("ldy", ctypes.c_int),
+                ("heads", ctypes.c_int), ("y_dtype", ctypes.c_int), ("weight", ctypes.c_void_p)]
+
+
 _cache_p, _batch_p = ctypes.POINTER(KvCacheStruct), ctypes.POINTER(KvBatchStruct)
 _quantise_args = [_vp, _i, _vp, _i, _vp, _i, _i, _i, _i, _st]
 gemv_fp8_quantise_f32 = _bind("gemv_fp8_quantise_f32", _quantise_args)
@@ -181,6 +190,20 @@ gemv_kv_attend_workspace_size = _bind("gemv_kv_attend_workspace_size",
 _attend_args = [_cache_p, _vp, _i, _vp, _i, _i, _i, _batch_p, ctypes.c_float, _i, _i, _vp, _sz, _st]
 gemv_kv_attend_f16 = _bind("gemv_kv_attend_f16", _attend_args)
 gemv_kv_attend_bf16 = _bind("gemv_kv_attend_bf16", _attend_args)
+gemv_kv_attend_shared_workspace_size = _bind("gemv_kv_attend_shared_workspace_size",
+                                             [_i, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i, ctypes.POINTER(_sz)])
+_attend_shared_args = [_cache_p, _vp, _i, _vp, _i, _i, _i, _batch_p, ctypes.c_float, _i, _i, _i, _vp, _sz, _st]
+gemv_kv_attend_shared_f16 = _bind("gemv_kv_attend_shared_f16", _attend_shared_args)
+gemv_kv_attend_shared_bf16 = _bind("gemv_kv_attend_shared_bf16", _attend_shared_args)
+_q4_args = [_vp, _i, _vp, _i, _vp, _i, _i, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _st]
+gemv_q4_f32 = _bind("gemv_q4_f32", _q4_args)
+gemv_q4_f16 = _bind("gemv_q4_f16", _q4_args)
+gemv_q4_bf16 = _bind("gemv_q4_bf16", _q4_args)
+ROTARY_MAX_PARTS, ROTARY_MAX_DIM = 4, 512
+_rotary_args = [ctypes.POINTER(RotaryPartStruct), _i, _i, _i, _vp, _i, _i, ctypes.c_float, ctypes.c_float, _batch_p, _st]
+gemv_rotary_f32 = _bind("gemv_rotary_f32", _rotary_args)
+gemv_rotary_f16 = _bind("gemv_rotary_f16", _rotary_args)
+gemv_rotary_bf16 = _bind("gemv_rotary_bf16", _rotary_args)
 
 EXPORTED = ("gemv_status_string", "gemv_last_hip_error",
             "gemv_last_hip_error_string", "gemv_f32", "gemv_f16", "gemv_bf16",
@@ -195,7 +218,9 @@ EXPORTED = ("gemv_status_string", "gemv_last_hip_error",
             "gemv_fp8_quantise_f32", "gemv_fp8_quantise_f16", "gemv_fp8_quantise_bf16",
             "gemv_fp8_f32", "gemv_fp8_f16", "gemv_fp8_bf16", "gemv_kv_append_f32",
             "gemv_kv_append_f16", "gemv_kv_append_bf16", "gemv_kv_attend_workspace_size",
-            "gemv_kv_attend_f16", "gemv_kv_attend_bf16")
+            "gemv_kv_attend_f16", "gemv_kv_attend_bf16", "gemv_kv_attend_shared_workspace_size",
+            "gemv_kv_attend_shared_f16", "gemv_kv_attend_shared_bf16", "gemv_q4_f32", "gemv_q4_f16",
+            "gemv_q4_bf16", "gemv_rotary_f32", "gemv_rotary_f16", "gemv_rotary_bf16")
 
 
 class GemvError(RuntimeError):
@@ -504,6 +529,11 @@ if _torch_runtime is not None:
     _APPEND = _by_dtype(gemv_kv_append_f32, gemv_kv_append_f16, gemv_kv_append_bf16)
     _KV_FORMATS = {_torch_runtime.int8: KV_INT8, _torch_runtime.float8_e4m3fn: KV_E4M3}
     _ATTEND = {_torch_runtime.float16: gemv_kv_attend_f16, _torch_runtime.bfloat16: gemv_kv_attend_bf16}
+    _ATTEND_SHARED = {_torch_runtime.float16: gemv_kv_attend_shared_f16,
+                      _torch_runtime.bfloat16: gemv_kv_attend_shared_bf16}
+    _Q4 = _by_dtype(gemv_q4_f32, gemv_q4_f16, gemv_q4_bf16)
+    _ROTARY = _by_dtype(gemv_rotary_f32, gemv_rotary_f16, gemv_rotary_bf16)
+    _CODES = _by_dtype(DTYPE_F32, DTYPE_F16, DTYPE_BF16)
 
 
 def _entry(table, dtype):
@@ -632,6 +662,183 @@ def gemv_fp8(W, w_scale, X, x_scale, bias=None, out=None, *, out_dtype=None, str
 
 
 # ---------------------------------------------------------------------------
+# 4-bit weights with group scales
+# ---------------------------------------------------------------------------
+
+def gemv_q4(Q, scale, X, bias=None, out=None, *, zero=None, group: int = 128, out_dtype=None, stream=None):
+    """X @ W.T (+ bias) for 4-bit weights W[m, k] = scale[m, k // group] · (q[m, k] - zero[m, k // group]).
+
+    Q (M, ceil(K / 2)) uint8 holds q, column 2·i in the low half of byte i and
+    2·i + 1 in the high half; scale (M, ceil(K / group)) is of X's dtype, zero
+    uint8 of the same shape (None: 8); group is 32, 64 or 128.  X is (nvec, K)
+    with unit column stride, any nvec, or (K,), in float32, float16 or bfloat16.
+    Returns (nvec, M) or (M,) float32, or in ``out_dtype`` / out's dtype; out may
+    be a column slice of a wider matrix."""
+    fn = _entry(_Q4, X.dtype)
+    dev = X.get_device()
+    single = X.dim() == 1
+    if single:
+        X = X.unsqueeze(0)
+    nvec, K, ldx = _rows(X, "X", dev)
+    if Q.dtype is not _torch_runtime.uint8:
+        raise TypeError("Q must be uint8")
+    M, across, ldq = _rows(Q, "Q", dev)
+    if across != (K + 1) // 2:
+        raise ValueError("Q must have a byte for each two columns of X")
+    if group != 32 and group != 64 and group != 128:
+        raise ValueError("group must be 32, 64 or 128")
+    groups = -(-K // group)
+    have, across, lds = _rows(scale, "scale", dev)
+    if have != M or across != groups or scale.dtype is not X.dtype:
+        raise ValueError(f"scale must be of X's dtype and shape {(M, groups)}")
+    zptr, ldz = None, 0
+    if zero is not None:
+        have, across, ldz = _rows(zero, "zero", dev)
+        if have != M or across != groups or zero.dtype is not _torch_runtime.uint8:
+            raise ValueError(f"zero must be a uint8 tensor of shape {(M, groups)}")
+        zptr = zero.data_ptr()
+    if bias is not None:
+        bias = _check_bias(bias, M, Q.device).data_ptr()
+    if out is None:
+        if out_dtype is None:
+            out_dtype = _F32
+        code = _entry(_CODES, out_dtype)
+        out = _empty(Q, (M,) if single else (nvec, M), out_dtype, stream)
+        ldy = M
+    else:
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError("out is not of out_dtype")
+        code = _entry(_CODES, out.dtype)
+        rows, cols, ldy = _rows(out.unsqueeze(0) if single else out, "out", dev)
+        if (rows, cols) != (nvec, M) or out.dim() != (1 if single else 2):
+            raise ValueError(f"out must be of shape {(M,) if single else (nvec, M)}")
+    _call(dev, stream, fn, Q.data_ptr(), ldq, scale.data_ptr(), lds, zptr, ldz, group, X.data_ptr(), ldx, bias,
+          out.data_ptr(), code, ldy, M, K, nvec)
+    return out
+
+
+# ---------------------------------------------------------------------------
+# norms and rotary positions of query and key heads
+# ---------------------------------------------------------------------------
+
+def rotary_frequencies(dim: int, base: float = 10000.0, *, factor: float = 1.0, original: int = 0,
+                       fast: float = 32.0, slow: float = 1.0, device="cuda"):
+    """(frequency, magnitude) for ``gemv_rotary``: dim rotated values of a head
+    (even), frequency[i] = base^(-2·i / dim), float32 (dim / 2,).
+
+    factor > 1 stretches the positions for contexts ``factor`` times longer:
+    without ``original`` every frequency is divided by it.  With the original
+    context's length, a pair that turns more than ``fast`` times within it keeps its
+    frequency, one that turns less than ``slow`` times is divided, those between
+    are mixed linearly in i, and the magnitude is 1 + 0.1·ln(factor)."""
+    import math
+    torch = _torch()
+    if dim < 0 or dim % 2 or base <= 0 or not factor >= 1 or original < 0 or not 0 < slow < fast:
+        raise ValueError("dim must be even, base positive, factor at least 1 and 0 < slow < fast")
+    i = torch.arange(dim // 2, dtype=torch.float64)
+    frequency = base ** (-2.0 * i / max(dim, 1))
+    magnitude = 1.0
+    if original and factor > 1:
+        # the i at which a pair turns so many times
+        def place(turns):
+            return dim / 2 * math.log(original / (2 * math.pi * turns)) / math.log(base)
+        low, high = max(math.floor(place(fast)), 0), min(math.ceil(place(slow)), dim // 2 - 1)
+        divided = torch.clamp((i - low) / max(high - low, 1e-3), 0.0, 1.0)
+        frequency = frequency * (1 - divided) + frequency / factor * divided
+        magnitude = 1.0 + 0.1 * math.log(factor)
+    elif factor > 1:
+        frequency = frequency / factor
+    return frequency.float().to(device), magnitude
+
+
+def _head_rows(t, name, dim, dev):
+    """(rows, heads, row stride) of a (rows, heads, dim) tensor whose rows may
+    be columns of a wider matrix."""
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != dim or t.get_device() != dev:
+        raise ValueError(f"{name} must be a device tensor (rows, heads, {dim}), all on one device")
+    rows, heads, _ = shape
+    if rows > _MOST or heads * dim > _MOST:
+        raise ValueError(f"{name} has more rows or columns than an int counts")
+    if t.is_contiguous():
+        return rows, heads, heads * dim
+    if (dim > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != dim):
+        raise ValueError(f"{name}'s heads must lie one behind the other in a row")
+    pitch = t.stride(0) if rows > 1 else heads * dim
+    if not heads * dim <= pitch <= _MOST:
+        raise ValueError(f"{name}'s row stride is smaller than its rows, or more than an int counts")
+    return rows, heads, pitch
+
+
+def gemv_rotary(Q, K, frequency, seq_lens, starts=None, *, q_weight=None, k_weight=None, eps: float = 1e-6,
+                magnitude: float = 1.0, interleaved: bool = False, q_out=None, k_out=None, q_dtype=None,
+                k_dtype=None, stream=None):
+    """(Q, K) with each head normed (where it has a weight) and rotated by its
+    token's position: Q (rows, q_heads, dim) and K (rows, heads, dim) or None,
+    both in float32, float16 or bfloat16, as the product gave them (their rows may
+    be columns of a wider matrix).
+
+    A head's first 2·len(frequency) values are rotated: value i with value i +
+    len(frequency), or value 2·i with 2·i + 1 if ``interleaved``, by
+    position·frequency[i], and multiplied by ``magnitude``.  seq_lens and starts
+    give the positions as for ``gemv_kv_append``.  q_weight, k_weight: float32
+    (dim,), for heads divided by the root of their mean square (+ eps) and
+    weighted first.  The results are new tensors of the inputs' dtype or of
+    q_dtype and k_dtype, or q_out and k_out, which may be Q and K themselves.
+    Rows behind the last start are left as they were."""
+    fn = _entry(_ROTARY, Q.dtype)
+    dev = Q.get_device()
+    if Q.dim() != 3:
+        raise ValueError("Q must be (rows, heads, dim)")
+    dim, total = Q.shape[2], Q.shape[0]
+    if dev < 0:
+        raise ValueError("Q must be a device tensor")
+    parts, results = (RotaryPartStruct * 2)(), []
+    for n, (x, name, weight, out, dtype) in enumerate((
+            (Q, "Q", q_weight, q_out, q_dtype), (K, "K", k_weight, k_out, k_dtype))):
+        if x is None:
+            if weight is not None or out is not None:
+                raise ValueError("K's weight and output need a K")
+            results.append(None)
+            continue
+        if x.dtype is not Q.dtype:
+            raise ValueError("Q and K must have the same dtype")
+        rows, heads, ldx = _head_rows(x, name, dim, dev)
+        if rows != total:
+            raise ValueError("Q and K must have the same rows")
+        if weight is not None:
+            if weight.dtype is not _F32 or weight.shape != (dim,) or not weight.is_contiguous() \
+                    or weight.get_device() != dev:
+                raise ValueError(f"{name}'s weight must be a contiguous float32 tensor of shape {(dim,)} on its device")
+            weight = weight.data_ptr()
+        if out is None:
+            out = _empty(x, (rows, heads, dim), x.dtype if dtype is None else dtype, stream)
+            ldy = heads * dim
+        else:
+            if out.shape != x.shape or (dtype is not None and out.dtype is not dtype):
+                raise ValueError(f"{name}'s output must have its shape, and the dtype asked for")
+            ldy = _head_rows(out, name + "'s output", dim, dev)[2]
+        parts[n] = RotaryPartStruct(x.data_ptr(), ldx, out.data_ptr(), ldy, heads, _entry(_CODES, out.dtype), weight)
+        results.append(out)
+    if frequency.dtype is not _F32 or frequency.dim() != 1 or not frequency.is_contiguous() \
+            or frequency.get_device() != dev:
+        raise ValueError("frequency must be a contiguous float32 tensor (pairs,) on Q's device")
+    if seq_lens.dtype is not _I32 or seq_lens.dim() != 1 or not seq_lens.is_contiguous() or seq_lens.get_device() != dev:
+        raise ValueError("seq_lens must be a contiguous int32 (sequences,) tensor on Q's device")
+    sequences = seq_lens.shape[0]
+    if starts is None:
+        if total != sequences:
+            raise ValueError("without starts every sequence has one row")
+    elif starts.dtype is not _I32 or starts.shape != (sequences + 1,) or not starts.is_contiguous() \
+            or starts.get_device() != dev:
+        raise ValueError("starts must be a contiguous int32 (sequences + 1,) tensor on Q's device")
+    batch = KvBatchStruct(sequences, None, 0, 0, seq_lens.data_ptr(), None if starts is None else starts.data_ptr())
+    _call(dev, stream, fn, parts, 1 if K is None else 2, dim, total, frequency.data_ptr(), frequency.shape[0],
+          1 if interleaved else 0, magnitude, eps, ctypes.byref(batch))
+    return results[0], results[1]
+
+
+# ---------------------------------------------------------------------------
 # a paged key/value cache in 8 bits
 # ---------------------------------------------------------------------------
 
@@ -748,38 +955,40 @@ def gemv_kv_append(cache, K, V, table, seq_lens, starts=None, *, stream=None):
 
 
 @functools.lru_cache(maxsize=256)
-def _attend_workspace(q_heads, heads, dim, rows, sequences, one_each, table_width, page_size, window, sinks):
+def _attend_workspace(q_heads, heads, dim, rows, sequences, one_each, table_width, page_size, window, sinks, shared=0):
     n = ctypes.c_size_t(0)
-    rc = gemv_kv_attend_workspace_size(q_heads, heads, dim, rows, sequences, one_each, table_width, page_size, window,
-                                       sinks, ctypes.byref(n))
+    rc = gemv_kv_attend_shared_workspace_size(q_heads, heads, dim, rows, sequences, one_each, table_width, page_size,
+                                              window, sinks, shared, ctypes.byref(n))
     if rc != GEMV_SUCCESS:
         raise GemvError(rc, "gemv_kv_attend_workspace_size")
     return n.value
 
 
 def kv_attend_workspace_size(cache, q_heads: int, rows: int, sequences: int, table_width: int, *,
-                             one_each: bool = True, window: int = 0, sinks: int = 0) -> int:
+                             one_each: bool = True, window: int = 0, sinks: int = 0, shared: int = 0) -> int:
     """Workspace bytes that ``gemv_kv_attend`` needs (0: none); one_each: the
     call has no ``starts``.  It depends on these sizes only."""
     return _attend_workspace(q_heads, cache.heads, cache.dim, rows, sequences, int(one_each), table_width,
-                             cache.page_size, window, sinks)
+                             cache.page_size, window, sinks, shared)
 
 
 def gemv_kv_attend(Q, cache, table, seq_lens, starts=None, *, scale=None, window: int = 0, sinks: int = 0,
-                   out=None, workspace=None, stream=None):
+                   shared: int = 0, out=None, workspace=None, stream=None):
     """Causal attention of the batch's new tokens, Q (rows, q_heads, dim) in
     float16 or bfloat16, over the cache, which holds their own keys and values
     already; returns (rows, q_heads, dim) of Q's dtype.
 
     table, seq_lens and starts as for ``gemv_kv_append``.  scale: 1 / sqrt(dim)
     by default.  window > 0: a token sees the last ``window`` tokens (itself
-    among them) and the first ``sinks``.  Rows of out behind the last start are
+    among them) and the first ``sinks``.  shared > 0: the first ``shared`` tokens
+    are the same in every sequence, and are read once for the whole batch, from
+    the pages in the table's first row.  Rows of out behind the last start are
     left as they were.  workspace: a device tensor of at least
     ``kv_attend_workspace_size(...)`` bytes, allocated here through torch when
     not given."""
-    fn = _entry(_ATTEND, Q.dtype)
-    if not (-_MOST <= window <= _MOST and -_MOST <= sinks <= _MOST):
-        raise ValueError("window and sinks must be what an int holds")
+    fn = _entry(_ATTEND_SHARED if shared else _ATTEND, Q.dtype)
+    if not (-_MOST <= window <= _MOST and -_MOST <= sinks <= _MOST and -_MOST <= shared <= _MOST):
+        raise ValueError("window, sinks and shared must be what an int holds")
     rows, q_heads, ldq = _heads(Q, "Q", cache)
     if out is None:
         out = _empty(Q, (rows, q_heads, cache.dim), Q.dtype, stream)
@@ -790,7 +999,7 @@ def gemv_kv_attend(Q, cache, table, seq_lens, starts=None, *, scale=None, window
         ldo = _heads(out, "out", cache)[2]
     batch = _kv_batch(cache, table, seq_lens, starts, rows)
     need = _attend_workspace(q_heads, cache.heads, cache.dim, rows, batch.sequences, starts is None,
-                             batch.table_width, cache.page_size, window, sinks)
+                             batch.table_width, cache.page_size, window, sinks, shared)
     if workspace is not None:
         if workspace.get_device() != cache._device or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on the cache's device")
@@ -799,5 +1008,5 @@ def gemv_kv_attend(Q, cache, table, seq_lens, starts=None, *, scale=None, window
         workspace = _empty(Q, need // 4, _F32, stream)
     _call(cache._device, stream, fn, cache._ref, Q.data_ptr(), ldq, out.data_ptr(), ldo, q_heads, rows,
           ctypes.byref(batch), cache.dim ** -0.5 if scale is None else scale, window, sinks,
-          workspace.data_ptr() if workspace is not None else None, need)
+          *((shared,) if shared else ()), workspace.data_ptr() if workspace is not None else None, need)
     return out

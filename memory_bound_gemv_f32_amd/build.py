@@ -18,11 +18,13 @@ from pathlib import Path
 PACKAGE = Path(__file__).resolve().parent
 ROOT = PACKAGE.parent
 CSRC = PACKAGE / "csrc"
-SOURCES = [CSRC / "gemv_api.hip", CSRC / "fp8_api.hip", CSRC / "kv_api.hip"]
+SOURCES = [CSRC / "gemv_api.hip", CSRC / "fp8_api.hip", CSRC / "kv_api.hip", CSRC / "q4_api.hip",
+           CSRC / "rotary_api.hip"]
 HEADERS = [CSRC / "gemv_plan.hpp", CSRC / "gemv_device.hpp",
            CSRC / "gemv_kernels.hpp", CSRC / "gemv_launch.hpp",
            CSRC / "fp8_device.hpp", CSRC / "fp8_kernels.hpp",
-           CSRC / "kv_kernels.hpp", CSRC / "kv_plan.hpp", ROOT / "include" / "gemv.h"]
+           CSRC / "kv_kernels.hpp", CSRC / "kv_plan.hpp", CSRC / "q4_kernels.hpp",
+           CSRC / "rotary_kernels.hpp", ROOT / "include" / "gemv.h"]
 LIBRARY = PACKAGE / "libgemv.so"
 ARCH = "gfx950"
 

@@ -17,7 +17,9 @@ using kvdev::TF16;
 using kvdev::TF32;
 using kvplan::capacity_of;
 using kvplan::map_attend;
+using kvplan::map_both;
 using kvplan::Mapping;
+using kvplan::SharedMapping;
 using kvplan::workspace_of;
 
 static_assert(GEMV_KV_BLOCK == kvdev::kBlock, "the header states the block");
@@ -78,28 +80,61 @@ gemv_status_t append(int dim, const kvdev::Cache& c, const kvdev::Batch& q, cons
     return launch(fn, dim3((unsigned)places, (unsigned)c.heads, 2), 64, argv, stream);
 }
 
-template <class T, class F, int DIM>
-gemv_status_t attend(const Mapping& m, Attend& p, hipStream_t stream) {
+// Joins p's splits; with s, also those over the shared tokens.
+template <class T, int DIM, bool SHARED>
+gemv_status_t join(const Mapping& m, Attend& p, Attend& s, int64_t shared_places, hipStream_t stream) {
+    int64_t places = m.places;
+    void* argv[] = {&p, &places, &s, &shared_places};
+    constexpr int kTwo = DIM <= 128 ? 2 : 1;
+    const void* fn = m.waves_share == 1
+                         ? (const void*)&kvdev::kv_join_kernel<T, DIM, 16 * kvdev::kOwnWaves * kTwo, 16 * kTwo, SHARED>
+                     : m.row_tiles == 2 ? (const void*)&kvdev::kv_join_kernel<T, DIM, 16 * kTwo, 16 * kTwo, SHARED>
+                                        : (const void*)&kvdev::kv_join_kernel<T, DIM, 16, 16, SHARED>;
+    return launch(fn, dim3((unsigned)(places * p.cache.heads), (unsigned)m.place_rows),
+                  kvdev::kShareWaves * 64, argv, stream);
+}
+
+template <class T, class F, int DIM, bool SHARED>
+gemv_status_t walk(const Mapping& m, Attend& p, hipStream_t stream) {
     int64_t places = m.places;
     const int64_t grid = places * p.cache.heads * p.splits;
     void* argv[] = {&p, &places};
     constexpr int kTwo = DIM <= 128 ? 2 : 1;
-    constexpr int kSmall = DIM <= 128 ? DIM : 128;  // (dim 256 has no eight, see map_attend)
-    const void* fn = m.waves_share == 1 ? (const void*)&kvdev::kv_attend_kernel<T, F, DIM, kTwo, 1>
-                     : m.row_tiles == 2 ? (const void*)&kvdev::kv_attend_kernel<T, F, DIM, kTwo, 4>
-                     : m.waves_share == 8 ? (const void*)&kvdev::kv_attend_kernel<T, F, kSmall, 1, 8>
-                                          : (const void*)&kvdev::kv_attend_kernel<T, F, DIM, 1, 4>;
-    const gemv_status_t st = launch(fn, dim3((unsigned)grid), 64 * kvplan::waves_of(m), argv, stream);
-    if (st != GEMV_SUCCESS || p.splits == 1) return st;
-    const void* join = m.waves_share == 1 ? (const void*)&kvdev::kv_join_kernel<T, DIM, 16 * kvdev::kOwnWaves * kTwo, 16 * kTwo>
-                       : m.row_tiles == 2 ? (const void*)&kvdev::kv_join_kernel<T, DIM, 16 * kTwo, 16 * kTwo>
-                                          : (const void*)&kvdev::kv_join_kernel<T, DIM, 16, 16>;
-    return launch(join, dim3((unsigned)(places * p.cache.heads), (unsigned)m.place_rows),
-                  kvdev::kShareWaves * 64, argv, stream);
+    constexpr int kSmall = DIM <= 128 ? DIM : 128;  // (dim 256 has no eight, see cut)
+    const void* fn = nullptr;
+    if constexpr (!SHARED)
+        if (m.waves_share == 1) fn = (const void*)&kvdev::kv_attend_kernel<T, F, DIM, kTwo, 1>;
+    if (fn == nullptr)
+        fn = m.row_tiles == 2     ? (const void*)&kvdev::kv_attend_kernel<T, F, DIM, kTwo, 4, SHARED>
+             : m.waves_share == 8 ? (const void*)&kvdev::kv_attend_kernel<T, F, kSmall, 1, 8, SHARED>
+                                  : (const void*)&kvdev::kv_attend_kernel<T, F, DIM, 1, 4, SHARED>;
+    return launch(fn, dim3((unsigned)grid), 64 * kvplan::waves_of(m), argv, stream);
+}
+
+template <class T, class F, int DIM>
+gemv_status_t attend(const SharedMapping& m, Attend& p, hipStream_t stream) {
+    Attend s = p;
+    if constexpr (DIM <= 128) {
+        if (m.chunks > 0) {
+            s.splits = m.shared.splits;
+            s.split_chunks = m.shared.split_chunks;
+            s.rows = m.shared.place_rows;
+            s.capacity = m.chunks * kvplan::kChunk;
+            s.shared = 0;
+            s.partial = p.partial + kvplan::partials_of(m.own, p.cache.heads, DIM) / sizeof(float);
+            const gemv_status_t st = walk<T, F, DIM, true>(m.shared, s, stream);
+            if (st != GEMV_SUCCESS) return st;
+        }
+    }
+    const gemv_status_t st = walk<T, F, DIM, false>(m.own, p, stream);
+    if (st != GEMV_SUCCESS) return st;
+    if constexpr (DIM <= 128)
+        if (m.chunks > 0) return join<T, DIM, true>(m.own, p, s, m.shared.places, stream);
+    return p.splits == 1 ? st : join<T, DIM, false>(m.own, p, s, 0, stream);
 }
 
 template <class T, class F>
-gemv_status_t attend_dim(int dim, const Mapping& m, Attend& p, hipStream_t stream) {
+gemv_status_t attend_dim(int dim, const SharedMapping& m, Attend& p, hipStream_t stream) {
     switch (dim) {
     case 64: return attend<T, F, 64>(m, p, stream);
     case 128: return attend<T, F, 128>(m, p, stream);
@@ -125,18 +160,18 @@ gemv_status_t append(const gemv_kv_cache_t* cache, const void* K, int ldk, const
 template <class T>
 gemv_status_t attend(const gemv_kv_cache_t* cache, const uint16_t* Q, int ldq, uint16_t* O, int ldo,
                      int q_heads, int rows, const gemv_kv_batch_t* batch, float scale, int window,
-                     int sinks, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+                     int sinks, int shared, void* workspace, size_t workspace_bytes, hipStream_t stream) {
     Attend p;
     if (!make_cache(cache, &p.cache) ||
         !make_batch(batch, rows, &p.batch) || q_heads < 1 || q_heads % p.cache.heads != 0 ||
         (int64_t)ldq < (int64_t)q_heads * cache->dim || (int64_t)ldo < (int64_t)q_heads * cache->dim ||
-        (int64_t)rows * q_heads > 0x7fffffff || window < 0 || sinks < 0 || !(scale - scale == 0.0f))
+        (int64_t)rows * q_heads > 0x7fffffff || window < 0 || sinks < 0 || shared < 0 || !(scale - scale == 0.0f))
         return GEMV_ERROR_INVALID_VALUE;
     if (rows == 0 || p.batch.count == 0) return GEMV_SUCCESS;
     if (Q == nullptr || O == nullptr || !aligned(Q, 2) || !aligned(O, 2)) return GEMV_ERROR_INVALID_VALUE;
     const int64_t capacity = capacity_of(batch->table_width, cache->page_size);
-    const Mapping m = map_attend(q_heads, p.cache.heads, cache->dim, rows, p.batch.count, batch->starts == nullptr,
-                                 capacity, window, sinks);
+    const SharedMapping m = map_both(q_heads, p.cache.heads, cache->dim, rows, p.batch.count,
+                                     batch->starts == nullptr, capacity, window, sinks, shared);
     if (!kvplan::launchable(m, p.cache.heads)) return GEMV_ERROR_INVALID_VALUE;
     const size_t need = workspace_of(m, p.cache.heads, cache->dim);
     if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 16)))
@@ -151,9 +186,10 @@ gemv_status_t attend(const gemv_kv_cache_t* cache, const uint16_t* Q, int ldq, u
     p.window = window;
     p.sinks = sinks;
     p.capacity = (int)capacity;
-    p.splits = m.splits;
-    p.split_chunks = m.split_chunks;
-    p.rows = m.place_rows;
+    p.splits = m.own.splits;
+    p.split_chunks = m.own.split_chunks;
+    p.rows = m.own.place_rows;
+    p.shared = m.chunks;
     p.partial = static_cast<float*>(workspace);
     return cache->format == GEMV_KV_E4M3 ? attend_dim<T, E4m3>(cache->dim, m, p, stream)
                                          : attend_dim<T, Int8>(cache->dim, m, p, stream);
@@ -161,22 +197,30 @@ gemv_status_t attend(const gemv_kv_cache_t* cache, const uint16_t* Q, int ldq, u
 
 }  // namespace
 
-extern "C" gemv_status_t gemv_kv_attend_workspace_size(int q_heads, int heads, int dim, int rows,
-                                                       int sequences, int one_each, int table_width,
-                                                       int page_size, int window, int sinks, size_t* bytes) {
+extern "C" gemv_status_t gemv_kv_attend_shared_workspace_size(int q_heads, int heads, int dim, int rows,
+                                                              int sequences, int one_each, int table_width,
+                                                              int page_size, int window, int sinks, int shared,
+                                                              size_t* bytes) {
     if (bytes == nullptr || heads < 1 || heads > kMostHeads || q_heads < 1 || q_heads % heads != 0 ||
         !known_dim(dim) || rows < 0 || sequences < 0 || (one_each && rows != sequences) || table_width < 0 ||
-        !known_page(page_size) || (int64_t)rows * q_heads > 0x7fffffff || window < 0 || sinks < 0)
+        !known_page(page_size) || (int64_t)rows * q_heads > 0x7fffffff || window < 0 || sinks < 0 || shared < 0)
         return GEMV_ERROR_INVALID_VALUE;
     size_t need = 0;
     if (rows > 0 && sequences > 0) {
-        const Mapping m = map_attend(q_heads, heads, dim, rows, sequences, one_each != 0,
-                                     capacity_of(table_width, page_size), window, sinks);
+        const SharedMapping m = map_both(q_heads, heads, dim, rows, sequences, one_each != 0,
+                                         capacity_of(table_width, page_size), window, sinks, shared);
         if (!kvplan::launchable(m, heads)) return GEMV_ERROR_INVALID_VALUE;
         need = workspace_of(m, heads, dim);
     }
     *bytes = need;
     return GEMV_SUCCESS;
+}
+
+extern "C" gemv_status_t gemv_kv_attend_workspace_size(int q_heads, int heads, int dim, int rows,
+                                                       int sequences, int one_each, int table_width,
+                                                       int page_size, int window, int sinks, size_t* bytes) {
+    return gemv_kv_attend_shared_workspace_size(q_heads, heads, dim, rows, sequences, one_each, table_width,
+                                                page_size, window, sinks, 0, bytes);
 }
 
 #define GEMV_KV_APPEND(NAME, D, T)                                                             \
@@ -195,8 +239,15 @@ GEMV_KV_APPEND(bf16, TBF16, uint16_t)
         const gemv_kv_cache_t* cache, const uint16_t* Q, int ldq, uint16_t* O, int ldo,          \
         int q_heads, int rows, const gemv_kv_batch_t* batch, float scale, int window, int sinks, \
         void* workspace, size_t workspace_bytes, hipStream_t stream) {                           \
-        return attend<T>(cache, Q, ldq, O, ldo, q_heads, rows, batch, scale, window, sinks,      \
+        return attend<T>(cache, Q, ldq, O, ldo, q_heads, rows, batch, scale, window, sinks, 0,   \
                          workspace, workspace_bytes, stream);                                    \
+    }                                                                                            \
+    extern "C" gemv_status_t gemv_kv_attend_shared_##NAME(                                       \
+        const gemv_kv_cache_t* cache, const uint16_t* Q, int ldq, uint16_t* O, int ldo,          \
+        int q_heads, int rows, const gemv_kv_batch_t* batch, float scale, int window, int sinks, \
+        int shared, void* workspace, size_t workspace_bytes, hipStream_t stream) {               \
+        return attend<T>(cache, Q, ldq, O, ldo, q_heads, rows, batch, scale, window, sinks,      \
+                         shared, workspace, workspace_bytes, stream);                            \
     }
 GEMV_KV_ATTEND(f16, TF16)
 GEMV_KV_ATTEND(bf16, TBF16)

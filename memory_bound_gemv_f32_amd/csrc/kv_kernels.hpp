@@ -442,11 +442,13 @@ struct Attend {
     int split_chunks;   // ... each so many chunks of them; splits > 1:
     int rows;           // rows of a place that can be there
     float* partial;     // see partial_at
+    int shared;         // chunks that the batch shares and another launch takes (0: none):
+                        // then the results are partial ones, whatever the splits
 };
 
 // What a row tile sees of the sequence's tokens.
 __device__ __forceinline__ Span span_of(const Attend& p, int min_pos, int max_pos, int len) {
-    return kvplan::span_of(p.window, p.sinks, p.capacity, min_pos, max_pos, len);
+    return kvplan::span_of(p.window, p.sinks, p.capacity, min_pos, max_pos, len, p.shared);
 }
 
 // Rows of a sequence that a workgroup takes: from row r0 on.
@@ -486,6 +488,43 @@ __device__ __forceinline__ bool tile_of(const Attend& p, int64_t place, Tile& t)
     return r0 >= 0 && r0 < t.rows;
 }
 
+// Where all sequences share their first tokens: the rows of the whole batch, over
+// the first sequence's pages.
+template <int R>
+__device__ __forceinline__ bool shared_tile_of(const Attend& p, int64_t place, Tile& t) {
+    const Batch& q = p.batch;
+    int rows = start_of(q, q.count);
+    rows = rows < q.total ? rows : q.total;
+    t.b = t.start = t.first = 0;
+    t.len = p.capacity;
+    t.rows = rows * p.group;
+    const int64_t r0 = place * R;
+    t.r0 = (int)r0;
+    return r0 < t.rows;
+}
+// The position of a row of the call in its sequence, or -1 where it has none.
+__device__ __forceinline__ int position_of(const Batch& q, int row) {
+    int lo = row, hi = row + 1;
+    if (q.starts != nullptr) {
+        lo = 0;
+        hi = q.count;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (q.starts[mid] <= row)
+                lo = mid;
+            else
+                hi = mid;
+        }
+    }
+    const int start = start_of(q, lo), stop = start_of(q, lo + 1);
+    if (row < start || row >= stop || stop > q.total) return -1;
+    const int64_t pos = (int64_t)q.lens[lo] - (stop - row);
+    return pos < 0 ? -1 : (int)pos;
+}
+__device__ __forceinline__ int wave_max_int(int v) {  // of numbers from -1 on
+    return (int)fp8dev::wave_max((uint32_t)(v + 1)) - 1;
+}
+
 // splits > 1: each split of a place and head leaves p.rows rows, each as the result
 // over its own tokens, and their m and l: first all (m, l), then all rows.
 struct Partial {
@@ -499,8 +538,10 @@ __device__ __forceinline__ Partial partial_at(const Attend& p, int64_t places, i
 }
 
 // WS > 1: the workgroup's wavefronts take the chunks of one row tile in turn
-// and join in LDS.  WS = 1: each wavefront has a row tile of its own.
-template <class T, class F, int DIM, int RT, int WS>
+// and join in LDS.  WS = 1: each wavefront has a row tile of its own.  SHARED: the
+// rows of all sequences over the p.capacity tokens that they share; the results
+// are partial ones.
+template <class T, class F, int DIM, int RT, int WS, bool SHARED = false>
 __global__ __launch_bounds__(kWavesOf<WS> * 64, DIM <= 128 ? 2 : 1) void kv_attend_kernel(Attend p, int64_t places) {
     constexpr int kRows = 16 * RT;                              // rows of a wavefront
     constexpr int kGroupRows = WS == 1 ? kOwnWaves * kRows : kRows;
@@ -517,22 +558,36 @@ __global__ __launch_bounds__(kWavesOf<WS> * 64, DIM <= 128 ? 2 : 1) void kv_atte
     const int split = (int)(at % p.splits);
     const int64_t place = at / p.splits;
     Tile t;
-    if (!tile_of<kGroupRows>(p, place, t)) return;
+    if (!(SHARED ? shared_tile_of<kGroupRows>(p, place, t) : tile_of<kGroupRows>(p, place, t))) return;
     const int r0 = t.r0 + (WS == 1 ? wave * kRows : 0);
     if (WS == 1 && r0 >= t.rows) return;
     const int last = (r0 + kRows < t.rows ? r0 + kRows : t.rows) - 1;
-    const int min_pos = t.first + r0 / p.group, max_pos = t.first + last / p.group;
+    int min_pos = t.first + r0 / p.group, max_pos = t.first + last / p.group;
+    int pos[RT];  // the lane's row of each 16: its position (-1: none)
+    if constexpr (SHARED) {
+        int most = -1, most_left = -1;  // 0x7fffffff less the position
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            const int r = r0 + 16 * i + n;
+            pos[i] = r <= last ? position_of(p.batch, r / p.group) : -1;
+            most = pos[i] > most ? pos[i] : most;
+            const int left = pos[i] < 0 ? -1 : 0x7ffffffe - pos[i];
+            most_left = left > most_left ? left : most_left;
+        }
+        max_pos = __builtin_amdgcn_readfirstlane(wave_max_int(most));
+        min_pos = 0x7ffffffe - __builtin_amdgcn_readfirstlane(wave_max_int(most_left));
+        min_pos = max_pos < 0 ? -1 : min_pos;
+    }
     const Span span = span_of(p, min_pos, max_pos, t.len);
     const int begin = p.splits == 1 ? 0 : split * p.split_chunks;
     int end = p.splits == 1 ? span.count() : begin + p.split_chunks;
     end = end < span.count() ? end : span.count();
-    if (split > 0 && begin >= end) return;  // (the whole workgroup: the splits are cut for all its rows alike)
+    if (!SHARED && split > 0 && begin >= end) return;  // (the whole workgroup: the splits are cut for all its rows alike)
 
-    // the lane's row of each 16: its position (-1: none) and its Q
+    // ... and its Q
     // (two tiles' Q does not fit the registers beside the rest: it stays in LDS)
     constexpr bool kQInLds = RT > 1;
     __shared__ quad q_lds[kQInLds ? kWavesOf<WS> : 1][kQInLds ? RT : 1][kQInLds ? kSteps : 1][64];
-    int pos[RT];
     int64_t row[RT];     // row of the call
     int qhead[RT];
     quad q[RT][kSteps];
@@ -541,7 +596,7 @@ __global__ __launch_bounds__(kWavesOf<WS> * 64, DIM <= 128 ? 2 : 1) void kv_atte
         const int r = r0 + 16 * i + n;
         const int rr = r <= last ? r : last;
         const int token = rr / p.group;
-        pos[i] = r <= last ? t.first + token : -1;
+        if (!SHARED) pos[i] = r <= last ? t.first + token : -1;
         row[i] = (int64_t)t.start + token;
         qhead[i] = head * p.group + (rr - token * p.group);
         const uint16_t* src = p.Q + row[i] * p.ldq + (int64_t)qhead[i] * DIM + 16 * g;
@@ -828,7 +883,7 @@ __global__ __launch_bounds__(kWavesOf<WS> * 64, DIM <= 128 ? 2 : 1) void kv_atte
     float result[RT];
 #pragma unroll
     for (int i = 0; i < RT; ++i) result[i] = l[i] == 0.0f ? 0.0f : unit[i] * (1.0f / l[i]);
-    if (p.splits == 1) {
+    if (!SHARED && p.splits == 1 && p.shared == 0) {
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
             if (r0 + 16 * i + n > last) continue;
@@ -862,11 +917,13 @@ __global__ __launch_bounds__(kWavesOf<WS> * 64, DIM <= 128 ? 2 : 1) void kv_atte
 // Joins the splits of a row, a workgroup a row (R: rows of a place, RW: of one
 // of its wavefronts): the splits' maxima and sums give each its weight, then the
 // wavefronts add the weighted rows in turn and join in LDS, in a fixed order.
+// SHARED: behind its own splits come those of the shared tokens, `s`.
 // Bound by latency: 4.5 us for 32 rows of 64 splits, 7.0 for 2048 rows of up to 11.
-template <class T, int DIM, int R, int RW>
-__global__ __launch_bounds__(kShareWaves * 64) void kv_join_kernel(Attend p, int64_t places) {
+template <class T, int DIM, int R, int RW, bool SHARED = false>
+__global__ __launch_bounds__(kShareWaves * 64) void kv_join_kernel(Attend p, int64_t places, Attend s,
+                                                                   int64_t shared_places) {
     constexpr int kPer = DIM / 64;
-    __shared__ float weight[kMaxSplits];
+    __shared__ float weight[kMaxSplits * (SHARED ? 2 : 1)];
     __shared__ float part[kShareWaves][DIM];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const Cache& c = p.cache;
@@ -875,51 +932,69 @@ __global__ __launch_bounds__(kShareWaves * 64) void kv_join_kernel(Attend p, int
     Tile t;
     const int r = blockIdx.y;
     if (!tile_of<R>(p, place, t) || t.r0 + r >= t.rows) return;
+    const int token = (t.r0 + r) / p.group;
+    const int in_group = t.r0 + r - token * p.group;
     // the splits that its wavefront's rows have (split 0 always leaves its rows)
     const int r0 = t.r0 + r / RW * RW, last = (r0 + RW < t.rows ? r0 + RW : t.rows) - 1;
     const int chunks = span_of(p, t.first + r0 / p.group, t.first + last / p.group, t.len).count();
     int splits = chunks > p.split_chunks ? (chunks + p.split_chunks - 1) / p.split_chunks : 1;
     splits = splits < p.splits ? splits : p.splits;  // (the partial results end there)
     const Partial in = partial_at<DIM>(p, places, (place * c.heads + head) * p.splits);
+    // the row's place among the rows over the shared tokens
+    Partial also{};
+    int shared_r = 0, all = splits;
+    if constexpr (SHARED) {
+        const int row = (t.start + token) * p.group + in_group;
+        shared_r = row % s.rows;
+        also = partial_at<DIM>(s, shared_places, ((int64_t)(row / s.rows) * c.heads + head) * s.splits);
+        all += s.splits;
+    }
+    const auto ml_of = [&](int i) {
+        if (!SHARED || i < splits) return in.ml + (i * p.rows + r) * 2;
+        return also.ml + ((i - splits) * s.rows + shared_r) * 2;
+    };
     // every wavefront reduces the maxima and sums for itself
     float top = -__builtin_inff();
-    for (int s = lane; s < splits; s += 64) top = fmaxf(top, in.ml[(s * p.rows + r) * 2]);
+    for (int i = lane; i < all; i += 64) top = fmaxf(top, ml_of(i)[0]);
     const float base = finite_base(wave_max(top));
     float l = 0.0f;
-    for (int s = lane; s < splits; s += 64) {
-        const float ls = in.ml[(s * p.rows + r) * 2 + 1];
+    for (int i = lane; i < all; i += 64) {
+        const float ls = ml_of(i)[1];
         // a split in which the row sees nothing adds nothing, whatever its row holds
-        const float w = ls == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(in.ml[(s * p.rows + r) * 2] - base) * ls;
+        const float w = ls == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(ml_of(i)[0] - base) * ls;
         l += w;
-        if (wave == 0) weight[s] = ls == 0.0f ? -1.0f : w;
+        if (wave == 0) weight[i] = ls == 0.0f ? -1.0f : w;
     }
     l = gemvdev::segment_sum<64>(l);
     // (over the sum before they meet the rows: a result is within V's range, its
     // multiple need not be)
     const float by = l == 0.0f ? 0.0f : 1.0f / l;
     if (wave == 0)
-        for (int s = lane; s < splits; s += 64)
-            if (weight[s] != -1.0f) weight[s] *= by;
+        for (int i = lane; i < all; i += 64)
+            if (weight[i] != -1.0f) weight[i] *= by;
     __syncthreads();
     float o[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) o[i] = 0.0f;
-#pragma unroll 8
-    for (int s = wave; s < splits; s += kShareWaves) {
-        const float w = weight[s];
-        const float* row = in.rows + ((int64_t)s * p.rows + r) * DIM;
+    const auto add = [&](int i, const float* row) {
+        const float w = weight[i];
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const float x = row[i * 64 + lane];
-            o[i] += w == -1.0f ? 0.0f : x * w;
+        for (int d = 0; d < kPer; ++d) {
+            const float x = row[d * 64 + lane];
+            o[d] += w == -1.0f ? 0.0f : x * w;
         }
+    };
+#pragma unroll 8
+    for (int i = wave; i < splits; i += kShareWaves) add(i, in.rows + ((int64_t)i * p.rows + r) * DIM);
+    if constexpr (SHARED) {
+#pragma unroll 8
+        for (int i = wave; i < s.splits; i += kShareWaves)
+            add(splits + i, also.rows + ((int64_t)i * s.rows + shared_r) * DIM);
     }
 #pragma unroll
     for (int i = 0; i < kPer; ++i) part[wave][i * 64 + lane] = o[i];
     __syncthreads();
-    const int token = (t.r0 + r) / p.group;
-    uint16_t* dst = p.O + ((int64_t)t.start + token) * p.ldo +
-                    (int64_t)(head * p.group + (t.r0 + r - token * p.group)) * DIM;
+    uint16_t* dst = p.O + ((int64_t)t.start + token) * p.ldo + (int64_t)(head * p.group + in_group) * DIM;
     for (int d = threadIdx.x; d < DIM; d += kShareWaves * 64) {
         float v = part[0][d];
 #pragma unroll

@@ -24,14 +24,15 @@ constexpr int kShareWaves = 4, kOwnWaves = 2;
 // visible, [low, high) the window (or everything up to the last row).
 struct Span {
     int first, low, high;
-    constexpr int count() const { return first + high - low; }
-    constexpr int chunk(int i) const { return i < first ? i : i - first + low; }
+    int skip = 0;  // so many of these are left out: those that the batch shares
+    constexpr int count() const { return first + high - low - skip; }
+    constexpr int chunk(int i) const { return i + skip < first ? i + skip : i + skip - first + low; }
 };
 // Of rows at positions min_pos to max_pos of a sequence of len tokens, whose row
 // of the table can hold `capacity` of them: tokens past that are not there, so
 // no chunk lies past it, whatever the length says, and there are no more chunks
-// than map_attend counts.
-constexpr Span span_of(int window, int sinks, int capacity, int min_pos, int max_pos, int len) {
+// than map_attend counts.  Chunks before `from` are left out.
+constexpr Span span_of(int window, int sinks, int capacity, int min_pos, int max_pos, int len, int from = 0) {
     int end = max_pos + 1 < len ? max_pos + 1 : len;
     end = end < capacity ? end : capacity;
     Span s{0, 0, 0};
@@ -42,6 +43,8 @@ constexpr Span span_of(int window, int sinks, int capacity, int min_pos, int max
         const int in_sinks = sinks / kChunk + (sinks % kChunk != 0);
         s.first = in_sinks < s.low ? in_sinks : s.low;
     }
+    const int in_window = from < s.low ? 0 : from < s.high ? from - s.low : s.high - s.low;
+    s.skip = from < s.first ? from : s.first + in_window;
     return s;
 }
 
@@ -74,29 +77,13 @@ constexpr int64_t kOwnSlots = 1024, kLeastLongSplit = 4;
 constexpr int64_t kMostTiles = 0x7fffffff;
 constexpr int64_t kLeastSplit = 8, kOneRoundSplit = 32, kSplit = 12, kSlots = 512, kMostWorkgroups = 8192;
 
-inline Mapping map_attend(int q_heads, int heads, int dim, int rows, int sequences, bool one_each, int64_t capacity,
-                   int window, int sinks) {
-    Mapping m;
-    const int group = q_heads / heads;
-    const int64_t per_sequence = one_each ? group : ceil_div((int64_t)rows * group, sequences);
-    m.waves_share = per_sequence <= 32 ? 4 : 1;
-    m.row_tiles = per_sequence <= 16 || dim > 128 ? 1 : 2;  // (two of dim 256 would not fit the registers)
-    m.group_rows = 16 * m.row_tiles * (m.waves_share == 1 ? kOwnWaves : 1);
-    m.places = one_each ? sequences * ceil_div(group, m.group_rows)
-                        : (int64_t)rows * group / m.group_rows + sequences;
-    m.place_rows = one_each && group < m.group_rows ? group : m.group_rows;
-    // chunks that a row tile can see
-    int64_t chunks = ceil_div(capacity, kChunk);
-    if (window > 0) {
-        const int64_t tokens = ceil_div(m.group_rows, group) + 1;
-        const int64_t in_window = ceil_div((int64_t)window + tokens, kChunk) + 1 +
-                                  ceil_div(sinks, kChunk);
-        if (in_window < chunks) chunks = in_window;
-    }
+
+// Cuts a mapping's chunks into splits.
+inline void cut(Mapping& m, int heads, int dim, int64_t chunks) {
     if (m.places * heads > kMostTiles) {  // (launchable refuses it; the products below would overflow)
         m.splits = 1;
         m.split_chunks = (int)chunks;
-        return m;
+        return;
     }
     const int64_t all = m.places * heads * chunks;
     const bool own = m.waves_share == 1;
@@ -119,6 +106,42 @@ inline Mapping map_attend(int q_heads, int heads, int dim, int rows, int sequenc
     if (dim <= 128 && m.waves_share == 4 && m.row_tiles == 1 && each > 4 &&
         m.places * heads * m.splits <= kSlots / 2)
         m.waves_share = 8;
+}
+
+// (skip: chunks at the start of the sequences that are left out)
+inline Mapping map_attend(int q_heads, int heads, int dim, int rows, int sequences, bool one_each, int64_t capacity,
+                          int window, int sinks, int skip = 0) {
+    Mapping m;
+    const int group = q_heads / heads;
+    const int64_t per_sequence = one_each ? group : ceil_div((int64_t)rows * group, sequences);
+    m.waves_share = per_sequence <= 32 ? 4 : 1;
+    m.row_tiles = per_sequence <= 16 || dim > 128 ? 1 : 2;  // (two of dim 256 would not fit the registers)
+    m.group_rows = 16 * m.row_tiles * (m.waves_share == 1 ? kOwnWaves : 1);
+    m.places = one_each ? sequences * ceil_div(group, m.group_rows)
+                        : (int64_t)rows * group / m.group_rows + sequences;
+    m.place_rows = one_each && group < m.group_rows ? group : m.group_rows;
+    // chunks that a row tile can see
+    int64_t chunks = ceil_div(capacity, kChunk) - skip;
+    if (window > 0) {
+        const int64_t tokens = ceil_div(m.group_rows, group) + 1;
+        const int64_t in_window = ceil_div((int64_t)window + tokens, kChunk) + 1 +
+                                  ceil_div(sinks, kChunk);
+        if (in_window < chunks) chunks = in_window;
+    }
+    cut(m, heads, dim, chunks);
+    return m;
+}
+
+// The rows of the whole batch over `chunks` chunks that all its sequences share.
+inline Mapping map_shared(int q_heads, int heads, int dim, int rows, int64_t chunks) {
+    Mapping m;
+    const int64_t all_rows = (int64_t)rows * (q_heads / heads);
+    m.waves_share = 4;
+    m.row_tiles = all_rows <= 16 || dim > 128 ? 1 : 2;
+    m.group_rows = 16 * m.row_tiles;
+    m.places = ceil_div(all_rows, m.group_rows);
+    m.place_rows = all_rows < m.group_rows ? (int)all_rows : m.group_rows;
+    cut(m, heads, dim, chunks);
     return m;
 }
 
@@ -135,15 +158,41 @@ constexpr bool launchable(const Mapping& m, int heads) {
 // are stored in 16-byte pieces: the first part in floats.
 constexpr int64_t stats_floats(int64_t rows) { return (rows * 2 + 3) / 4 * 4; }
 
-inline size_t workspace_of(const Mapping& m, int heads, int dim) {
-    if (m.splits == 1) return 0;
+inline size_t partials_of(const Mapping& m, int heads, int dim) {
     const int64_t rows = m.places * heads * m.splits * m.place_rows;
     return (size_t)(stats_floats(rows) + rows * dim) * sizeof(float);
+}
+inline size_t workspace_of(const Mapping& m, int heads, int dim) {
+    return m.splits == 1 ? 0 : partials_of(m, heads, dim);
 }
 
 inline int64_t capacity_of(int64_t table_width, int page_size) {
     const int64_t n = table_width * page_size;
     return n < 0x7fffffff ? n : 0x7fffffff;
+}
+
+// A call whose sequences share their first tokens: `chunks` chunks of them are
+// taken for all rows together and the rest for each sequence as ever; 0: that
+// would gain nothing, and `own` takes all.
+struct SharedMapping {
+    int chunks;
+    Mapping shared, own;
+};
+inline SharedMapping map_both(int q_heads, int heads, int dim, int rows, int sequences, bool one_each,
+                              int64_t capacity, int window, int sinks, int shared) {
+    SharedMapping s{};
+    const int64_t there = shared < capacity ? shared : capacity;
+    if (sequences > 1 && dim <= 128) s.chunks = (int)(there / kChunk);
+    if (s.chunks > 0) s.shared = map_shared(q_heads, heads, dim, rows, s.chunks);
+    s.own = map_attend(q_heads, heads, dim, rows, sequences, one_each, capacity, window, sinks, s.chunks);
+    return s;
+}
+constexpr bool launchable(const SharedMapping& s, int heads) {
+    return launchable(s.own, heads) && (s.chunks == 0 || launchable(s.shared, heads));
+}
+inline size_t workspace_of(const SharedMapping& s, int heads, int dim) {
+    return s.chunks == 0 ? workspace_of(s.own, heads, dim)
+                         : partials_of(s.own, heads, dim) + partials_of(s.shared, heads, dim);
 }
 
 }  // namespace kvplan
