@@ -26,13 +26,84 @@ gemv_status_t launch(const void* fn, dim3 grid, int threads, int lds_bytes, void
 }
 
 // Of one launch: rows and vectors.
-constexpr int kMostRows = 1 << 20, kMostTokens = 1 << 16;
+constexpr int kMostRows = 1 << 20, kMostTokens = 1 << 15;
 
-template <class T, int RT, int NT, int W>
-gemv_status_t few(Product& p, hipStream_t stream) {
+// LDS that the vectors (or their parts) of a call take.
+template <class T>
+int64_t staged_bytes(const Product& p) {
+    return q4dev::Operand<T>::parts * (int64_t)p.T * (ceil_div(p.K, q4dev::kChunk) * q4dev::kChunk * 2 + 16);
+}
+
+template <class T, int RT, int NT, int W, int U, bool STAGED>
+gemv_status_t few(Product& p, int group, hipStream_t stream) {
     void* argv[] = {&p};
     const dim3 grid((unsigned)ceil_div(p.M, 16 * RT), (unsigned)ceil_div(p.T, 16 * NT));
-    return launch((const void*)&q4dev::q4_few_kernel<T, RT, NT, W>, grid, W * 64, 0, argv, stream);
+    const int64_t staged = STAGED ? staged_bytes<T>(p) : 0, sums = RT * NT * W * 64 * 16;
+    const void* fn = nullptr;
+    if constexpr (RT * U <= 8)  // (groups of 32 with more than that would not fit the registers)
+        if (group == 32) fn = (const void*)&q4dev::q4_few_kernel<T, 0, RT, NT, W, U, STAGED>;
+    if (fn == nullptr)
+        fn = group == 64 ? (const void*)&q4dev::q4_few_kernel<T, 1, RT, NT, W, U, STAGED>
+                         : (const void*)&q4dev::q4_few_kernel<T, 2, RT, NT, W, U, STAGED>;
+    return launch(fn, grid, W * 64, (int)(staged > sums ? staged : sums), argv, stream);
+}
+
+template <class T, int RT, int NT, int W>
+gemv_status_t tile(Product& p, int group, hipStream_t stream) {
+    int row_tiles = (int)ceil_div(p.M, 16 * RT * W);
+    void* argv[] = {&p, &row_tiles};
+    const dim3 grid((unsigned)(row_tiles * ceil_div(p.T, 16 * NT)));
+    const int lds = 2 * 16 * NT * 256 * q4dev::Operand<T>::parts;
+    const void* fn = group == 32   ? (const void*)&q4dev::q4_tile_kernel<T, 0, RT, NT, W>
+                     : group == 64 ? (const void*)&q4dev::q4_tile_kernel<T, 1, RT, NT, W>
+                                   : (const void*)&q4dev::q4_tile_kernel<T, 2, RT, NT, W>;
+    return launch(fn, grid, W * 64, lds, argv, stream);
+}
+
+// Which kernel.  Few vectors read W straight into registers, in as many rows to a
+// workgroup as leave two of them to a compute unit at most (X, which each
+// of them reads whole, is what wider row tiles save); past that the tiles, whose X goes
+// through LDS, the larger once it fills three quarters of the places for it.  Measured,
+// us at vectors x rows x K, bf16, groups of 128 (16 rows | 32 rows | 64 rows | tile of
+// 64 x 64 | 128 x 128):
+//   1 x 4096 x 4096        5.3 |  7.3 | 11.8
+//   1 x 14336 x 4096      13.0 | 11.3 | 13.0
+//   16 x 4096 x 4096       7.8 |  8.9 | 12.5
+//   16 x 14336 x 4096     21.7 | 15.2 | 13.5
+//   32 x 14336 x 4096          | 27.6 | 24.8 | 31.5
+//   64 x 4096 x 4096           | 15.9 | 13.3 | 32.2
+//   64 x 14336 x 4096          | 44.8 | 45.7 | 33.2
+//   256 x 4096 x 4096                         | 32.9 |  72.9
+//   512 x 14336 x 4096                        | 121.7 | 110.4
+//   1024 x 14336 x 4096                       | 236.5 | 213.3
+constexpr int64_t kUnits = 256, kEnoughTiles = 384;
+constexpr int64_t kMostStaged = 150 * 1024;  // bytes of LDS for vectors
+constexpr int kMostOffset = 1 << 22;         // pitch with which a tile's rows are 32-bit offsets apart
+
+template <class T>
+gemv_status_t mapped(Product& p, int group, hipStream_t stream) {
+    constexpr bool kParts = q4dev::Operand<T>::parts > 1;
+    if (p.K < q4dev::kLeastColumns) {
+        void* argv[] = {&p};
+        const dim3 grid((unsigned)ceil_div(p.M, 256), (unsigned)p.T);
+        return launch((const void*)&q4dev::q4_short_kernel<T>, grid, 256, 0, argv, stream);
+    }
+    if constexpr (kParts)
+        // (1 x 4096 x 11008: 11.1 us; with the parts cut by every wavefront for itself 17)
+        if (3 * p.T <= 16 && staged_bytes<T>(p) <= kMostStaged) return few<T, 1, 1, 16, 2, true>(p, group, stream);
+    const int64_t tokens = ceil_div(p.T, 16);
+    const bool far = p.ldq >= kMostOffset || p.lds >= kMostOffset || p.ldz >= kMostOffset || p.ldx >= kMostOffset;
+    if (ceil_div(p.M, 16) * tokens <= kUnits) return few<T, 1, 1, 8, kParts ? 1 : 4, false>(p, group, stream);
+    if (ceil_div(p.M, 32) * tokens < 2 * kUnits) return few<T, 2, 1, 8, kParts ? 1 : 4, false>(p, group, stream);
+    if (far || ceil_div(p.M, 64) * tokens < 2 * kUnits) {
+        if (group == 32 || kParts) return few<T, 4, 1, 8, 1, false>(p, group, stream);  // (more would not fit the registers)
+        return few<T, 4, 1, 8, 4, false>(p, group, stream);
+    }
+    if (ceil_div(p.M, 128) * ceil_div(p.T, 128) < kEnoughTiles) return tile<T, 1, 4, 4>(p, group, stream);
+    if constexpr (kParts)
+        return tile<T, 3, 4, 4>(p, group, stream);
+    else
+        return tile<T, 2, 8, 4>(p, group, stream);
 }
 
 template <class T>
@@ -59,14 +130,17 @@ gemv_status_t product(const uint8_t* Q, int ldq, const typename T::storage* scal
             p.ldq = ldq;
             p.scale = scale;
             p.lds = lds;
-            p.zero = K > 0 ? zero : nullptr;
-            p.ldz = ldz;
+            // (without zeros the kernels load bytes of the scales, and use none)
+            p.zero = zero != nullptr ? zero : reinterpret_cast<const uint8_t*>(scale);
+            p.ldz = zero != nullptr ? ldz : lds * (int64_t)T::bytes;
+            p.zero_mask = zero != nullptr ? 0xffffffffu : 0u;
+            p.no_zero = zero != nullptr ? 0u : q4dev::kNoZero * 0x01010101u;
             p.X = X;
             p.ldx = ldx;
             if (K > 0) {
                 p.Q += m * p.ldq;
                 p.scale = scale + m * p.lds;
-                if (zero != nullptr) p.zero += m * p.ldz;
+                p.zero += m * p.ldz;
                 p.X = X + t * p.ldx;
             }
             p.bias = bias != nullptr ? bias + m : nullptr;
@@ -76,8 +150,7 @@ gemv_status_t product(const uint8_t* Q, int ldq, const typename T::storage* scal
             p.M = rows;
             p.K = K;
             p.T = tokens;
-            p.group_log2 = group == 32 ? 0 : group == 64 ? 1 : 2;
-            const gemv_status_t st = few<T, 1, 1, 16>(p, stream);
+            const gemv_status_t st = mapped<T>(p, group, stream);
             if (st != GEMV_SUCCESS) return st;
         }
     }

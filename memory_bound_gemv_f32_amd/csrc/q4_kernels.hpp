@@ -32,8 +32,9 @@ struct Product {
     int64_t ldq;
     const void* scale;
     int64_t lds;
-    const uint8_t* zero;         // NULL: kNoZero everywhere
+    const uint8_t* zero;         // without zeros: bytes that may be read in their place, ...
     int64_t ldz;
+    uint32_t zero_mask, no_zero;  // ... of which this mask leaves nothing, and kNoZero in each byte
     const void* X;
     int64_t ldx;
     const float* bias;           // or NULL
@@ -41,7 +42,6 @@ struct Product {
     int64_t ldy;
     int y_type;                  // gemv_dtype_t
     int M, K, T;
-    int group_log2;              // columns of a group over kBlock, as a power of two: 0, 1 or 2
 };
 
 // The type that X meets the weights in, and in how many parts.
@@ -66,27 +66,46 @@ struct Operand<TF32> {
 // 1024 + q, from which 1024 + zero is taken exactly.
 // ---------------------------------------------------------------------------
 
-// 1024 + zero, twice.
-__device__ __forceinline__ uint32_t offset_of(uint32_t zero) { return zero * 0x10001u | 0x64006400u; }
+// 1024 + zero: for fp16 twice in a word, for bf16 as an fp32 number.
+__device__ __forceinline__ uint32_t offset_of(TF16, uint32_t zero) { return zero * 0x10001u + 0x64006400u; }
+__device__ __forceinline__ float offset_of(TBF16, uint32_t zero) { return (float)zero + 1024.0f; }
 
-__device__ __forceinline__ uint32_t pair_of(uint32_t w, int i) {
-    return ((w >> (4 * i)) & 0x000f000fu) | 0x64006400u;
+// The four bits' place in both halves and 1024's exponent; the latter stays in a
+// vector register, so that one instruction masks and sets (an instruction of three
+// operands takes no constant of 32 bits and one scalar register).
+__device__ __forceinline__ uint32_t pair_of(uint32_t w, int i, uint32_t exponent) {
+    return ((w >> (4 * i)) & 0x000f000fu) | exponent;
 }
-__device__ __forceinline__ quad values8(TF16, uint32_t w, uint32_t offset) {
+__device__ __forceinline__ uint32_t exponent_of_1024() {
+    uint32_t e = 0x64006400u;
+    asm("" : "+v"(e));
+    return e;
+}
+// A half of a pair of fp16 values minus an fp32 number.
+template <int HALF>
+__device__ __forceinline__ float half_minus(uint32_t pair, float b) {
+    float d;
+    if constexpr (HALF == 0)
+        asm("v_fma_mix_f32 %0, %1, 1.0, -%2 op_sel_hi:[1,0,0]" : "=v"(d) : "v"(pair), "v"(b));
+    else
+        asm("v_fma_mix_f32 %0, %1, 1.0, -%2 op_sel:[1,0,0] op_sel_hi:[1,0,0]" : "=v"(d) : "v"(pair), "v"(b));
+    return d;
+}
+__device__ __forceinline__ quad values8(TF16, uint32_t w, uint32_t offset, uint32_t exponent) {
     quad v;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        v[i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, pair_of(w, i)) - __builtin_bit_cast(f16x2, offset));
+        v[i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, pair_of(w, i, exponent)) -
+                                                __builtin_bit_cast(f16x2, offset));
     return v;
 }
-__device__ __forceinline__ quad values8(TBF16, uint32_t w, uint32_t offset) {
-    const float zero = gemvdev::lo_f16(offset);
+__device__ __forceinline__ quad values8(TBF16, uint32_t w, float offset, uint32_t exponent) {
     quad v;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t p = pair_of(w, i);
-        const uint32_t a = __builtin_bit_cast(uint32_t, gemvdev::lo_f16(p) - zero);
-        const uint32_t b = __builtin_bit_cast(uint32_t, gemvdev::hi_f16(p) - zero);
+        const uint32_t p = pair_of(w, i, exponent);
+        const uint32_t a = __builtin_bit_cast(uint32_t, half_minus<0>(p, offset));
+        const uint32_t b = __builtin_bit_cast(uint32_t, half_minus<1>(p, offset));
         v[i] = __builtin_amdgcn_perm(b, a, 0x07060302u);  // their upper halves: whole numbers of 8 bits
     }
     return v;
@@ -147,8 +166,35 @@ __device__ __forceinline__ Vec8<TF32> operand_of(TF32, quad lo, quad hi) {
     return v;
 }
 
+// A uniform address that the compiler keeps in scalar registers: loads add the lanes'
+// 32-bit offsets to it, where it would else keep a 64-bit address for each of them.
+__device__ __forceinline__ const uint8_t* scalar_here(const uint8_t* p) {
+    asm volatile("" : "+s"(p));
+    return p;
+}
+__device__ __forceinline__ uint32_t offset_here(uint32_t v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
+// 16 bytes at byte `at` of a row of `bytes` (at least 16), in one load: near the
+// row's end the last 16, moved down; what lies behind reads as zero.
+__device__ __forceinline__ quad load_end(const uint8_t* row, int64_t at, int64_t bytes) {
+    const int64_t from = at < bytes - 16 ? at : bytes - 16;
+    const int64_t by = at - from;
+    const int down = by < 16 ? (int)by : 16;
+    quad v = *reinterpret_cast<const quad_any*>(row + from);
+    if (down & 4) v = quad{v[1], v[2], v[3], 0u};
+    if (down & 8) v = quad{v[2], v[3], 0u, 0u};
+    if (down & 16) v = quad{0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __builtin_amdgcn_alignbyte(i < 3 ? v[i + 1] : 0u, v[i], down & 3);
+    return v;
+}
+
 // What a lane loads of a vector for one matrix-core step: columns k .. k+7;
-// those from K on read as zero and are not touched.
+// those from K on read as zero and are not touched.  Rows are of 32 columns at least.
+constexpr int kLeastColumns = 32;
 template <class T>
 struct Raw8 {
     quad v[T::bytes / 2];
@@ -160,20 +206,10 @@ __device__ __forceinline__ Raw8<T> load_vec(const typename T::storage* x, int64_
 #pragma unroll
         for (int i = 0; i < T::bytes / 2; ++i)
             r.v[i] = *reinterpret_cast<const quad_any*>(x + k + i * (16 / T::bytes));
-        return r;
-    }
+    } else {
 #pragma unroll
-    for (int i = 0; i < T::bytes / 2; ++i) {
-        r.v[i] = quad{0u, 0u, 0u, 0u};
-#pragma unroll
-        for (int e = 0; e < 16 / T::bytes; ++e) {
-            const int64_t at = k + i * (16 / T::bytes) + e;
-            if (at >= K) continue;
-            if constexpr (T::bytes == 4)
-                r.v[i][e] = __builtin_bit_cast(uint32_t, x[at]);
-            else
-                r.v[i][e >> 1] |= (uint32_t)x[at] << (16 * (e & 1));
-        }
+        for (int i = 0; i < T::bytes / 2; ++i)
+            r.v[i] = load_end(reinterpret_cast<const uint8_t*>(x), k * T::bytes + 16 * i, (int64_t)K * T::bytes);
     }
     return r;
 }
@@ -185,26 +221,84 @@ __device__ __forceinline__ Vec8<T> operand_of(const Raw8<T>& r) {
         return operand_of(T{}, r.v[0]);
 }
 
-// Scale and zero of the four steps of a chunk (their group's, so two or four
-// of them may be alike); of steps behind the row's last column, 0.
-struct Scales {
-    float scale[4];
-    uint32_t offset[4];
+// Scales and zeros of U neighbouring chunks of a row as they lie in memory (G:
+// columns of a group over kBlock, as a power of two); those of groups behind the row's last
+// are 0.
+// N bytes from p on as they are: a number of the narrow type where N is 2 (widened
+// right behind the load, it would be waited for there), else words.
+template <int N>
+struct Narrow {
+    using type = uint32_t;
 };
-template <class T>
-__device__ __forceinline__ Scales load_scales(const Product& p, int m, int chunk) {
-    const typename T::storage* s = static_cast<const typename T::storage*>(p.scale) + m * p.lds;
-    const uint8_t* z = p.zero ? p.zero + m * p.ldz : nullptr;
-    Scales out;
-    const int blocks = (p.K + kBlock - 1) / kBlock;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int block = 4 * chunk + j, g = block >> p.group_log2;
-        const bool there = block < blocks;
-        out.scale[j] = there ? widen(T{}, s[g]) : 0.0f;
-        out.offset[j] = offset_of(z && there ? z[g] : kNoZero);
+template <>
+struct Narrow<2> {
+    using type = uint16_t;
+};
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t* p, typename Narrow<N>::type (&v)[(N + 3) / 4]) {
+    if constexpr (N == 1) {
+        v[0] = *p;
+        return;
     }
-    return out;
+    struct __attribute__((packed, aligned(1))) Words {
+        typename Narrow<N>::type v[(N + 3) / 4];
+    };
+    const Words w = *reinterpret_cast<const Words*>(p);
+#pragma unroll
+    for (int i = 0; i < (N + 3) / 4; ++i) v[i] = w.v[i];
+}
+template <class T, int G, int U>
+struct RawScales {
+    static constexpr int N = 4 * U >> G, kWords = (N * T::bytes + 3) / 4, kZeros = (N + 3) / 4;
+    typename Narrow<N * T::bytes>::type s[kWords];
+    typename Narrow<N>::type z[kZeros];
+
+    // of step j (0 .. 4·U-1)
+    __device__ __forceinline__ float scale(int j) const {
+        const int i = j >> G;
+        if constexpr (T::bytes == 4) return gemvdev::f32_of(s[i]);
+        return widen(T{}, (uint16_t)(s[i >> 1] >> (16 * (i & 1))));
+    }
+    __device__ __forceinline__ uint32_t zero(const Product& p, int j) const {
+        const int i = j >> G;
+        return (((uint32_t)z[i >> 2] & p.zero_mask) | p.no_zero) >> (8 * (i & 3)) & 0xffu;
+    }
+    template <class MT>
+    __device__ __forceinline__ auto offset(const Product& p, int j) const {
+        return offset_of(MT{}, zero(p, j));
+    }
+};
+template <class T, int G, int U>
+__device__ __forceinline__ RawScales<T, G, U> load_scales(const Product& p, int64_t m, int chunk, bool whole) {
+    using R = RawScales<T, G, U>;
+    using S = typename T::storage;
+    const int g0 = 4 * chunk >> G;
+    const S* s = static_cast<const S*>(p.scale) + m * p.lds + g0;
+    const uint8_t* z = p.zero + m * p.ldz + g0;
+    R r;
+    if (whole) {
+        load_words<R::N * T::bytes>(reinterpret_cast<const uint8_t*>(s), r.s);
+        load_words<R::N>(z, r.z);
+        return r;
+    }
+#pragma unroll
+    for (int i = 0; i < R::kWords; ++i) r.s[i] = 0;
+#pragma unroll
+    for (int i = 0; i < R::kZeros; ++i) r.z[i] = 0;
+    const int left = (((p.K + kBlock - 1) / kBlock + (1 << G) - 1) >> G) - g0;  // groups from g0 on
+#pragma unroll
+    for (int i = 0; i < R::N; ++i) {
+        const int at = i < left ? i : left - 1;  // (those behind repeat the last, and become 0)
+        if constexpr (T::bytes == 4) {
+            const uint32_t v = __builtin_bit_cast(uint32_t, s[at]);
+            r.s[i] = i < left ? v : 0u;
+        } else {
+            const uint32_t v = s[at];
+            r.s[i >> 1] = (typename Narrow<R::N * 2>::type)(r.s[i >> 1] | (i < left ? v : 0u) << (16 * (i & 1)));
+        }
+        r.z[i >> 2] = (typename Narrow<R::N>::type)(r.z[i >> 2] | (uint32_t)z[at] << (8 * (i & 3)));
+    }
+    return r;
 }
 
 template <class O>
@@ -221,23 +315,90 @@ __device__ __forceinline__ void store(const Product& p, int t, int m, float v) {
         put<TBF16>(p, at, v);
 }
 
+// Rows of fewer columns than one matrix-core step (and the empty sum): a thread a
+// result.
+template <class T>
+__global__ __launch_bounds__(256) void q4_short_kernel(Product p) {
+    const int64_t t = blockIdx.y;
+    const int m = (int)(blockIdx.x * 256 + threadIdx.x);
+    if (m >= p.M) return;
+    float v = 0.0f;
+    if (p.K > 0) {
+        const uint8_t* q = p.Q + m * p.ldq;
+        const typename T::storage* x = static_cast<const typename T::storage*>(p.X) + t * p.ldx;
+        const float zero = (float)(((p.zero[m * p.ldz] & p.zero_mask) | p.no_zero) & 0xffu);
+        for (int k = 0; k < p.K; ++k) v = __builtin_fmaf((float)(q[k >> 1] >> (4 * (k & 1)) & 15) - zero, widen(T{}, x[k]), v);
+        v *= widen(T{}, static_cast<const typename T::storage*>(p.scale)[m * p.lds]);
+    }
+    if (p.bias) v += p.bias[m];
+    store(p, (int)t, m, v);
+}
+
+// The products of one chunk: acc += scale·(w·x) for each group, which takes one,
+// two or four steps.
+template <class MT, int G, int RT, int NT, int PARTS, class S, class X>
+__device__ __forceinline__ void multiply(const Product& p, f32x4 (&acc)[RT][NT], const quad (&w)[RT], const S (&scales)[RT], int first,
+                                         X&& x_of) {
+    constexpr int kSteps = 1 << G;
+    const uint32_t exponent = exponent_of_1024();
+#pragma unroll
+    for (int j0 = 0; j0 < 4; j0 += kSteps) {
+        f32x4 d[RT][NT];
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+            const int j = j0 + s;
+            quad b[RT];
+#pragma unroll
+            for (int i = 0; i < RT; ++i) b[i] = values8(MT{}, w[i][j], scales[i].template offset<MT>(p, first + j), exponent);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const auto v = x_of(n, j);
+#pragma unroll
+                for (int i = 0; i < RT; ++i) {
+                    if (s == 0) d[i][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int e = 0; e < PARTS; ++e) d[i][n] = gemvdev::mma_16x16x32(MT{}, v.part[e], b[i], d[i][n]);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            const float by = scales[i].scale(first + j0);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[i][n][e] = __builtin_fmaf(d[i][n][e], by, acc[i][n][e]);
+        }
+    }
+}
+
 // Few vectors: a workgroup takes 16·RT rows by 16·NT vectors; its W wavefronts
-// take the chunks of 128 columns in turn and add their sums in LDS, in a fixed
-// order.  A lane has row (and vector) lane % 16.
-template <class T, int RT, int NT, int W>
+// take U neighbouring chunks of 128 columns in turn, the next ones' weights and
+// scales in flight while those at hand are multiplied, and add their sums in LDS,
+// in a fixed order.  A lane has row (and vector) lane % 16.
+//
+// STAGED (where the vectors fit): they are brought to LDS once for the workgroup, in
+// the order that the weights come out in; an fp32 vector as three, of its parts,
+// whose sums are added at the end.
+template <class T, int G, int RT, int NT, int W, int U, bool STAGED>
 __global__ __launch_bounds__(W * 64) void q4_few_kernel(Product p) {
     using MT = typename Operand<T>::type;
-    __shared__ f32x4 part[W][64];
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    constexpr int PER = STAGED ? Operand<T>::parts : 1, PARTS = STAGED ? 1 : Operand<T>::parts;
+    static_assert(!STAGED || NT == 1, "one tile of vectors or parts");
+    extern __shared__ __align__(16) uint8_t lds[];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int r = lane & 15, g = lane >> 4;
     const int row0 = (int)blockIdx.x * 16 * RT, t0 = (int)blockIdx.y * 16 * NT;
-    const int chunks = p.K / kChunk + (p.K % kChunk != 0);
-    const int row_bytes = p.K / 2 + (p.K & 1);
+    const int chunks = p.K / kChunk + (p.K % kChunk != 0), whole = p.K / kChunk;
     // rows and vectors past the end repeat the last one; their results are not stored
-    int m[RT];
-    const typename T::storage* x[NT];
+    int64_t m[RT];
+    const uint8_t* q[RT];
 #pragma unroll
-    for (int i = 0; i < RT; ++i) m[i] = row0 + 16 * i + r < p.M ? row0 + 16 * i + r : p.M - 1;
+    for (int i = 0; i < RT; ++i) {
+        m[i] = row0 + 16 * i + r < p.M ? row0 + 16 * i + r : p.M - 1;
+        q[i] = p.Q + m[i] * p.ldq + 16 * g;
+    }
+    const typename T::storage* x[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         const int t = t0 + 16 * n + r;
@@ -248,63 +409,330 @@ __global__ __launch_bounds__(W * 64) void q4_few_kernel(Product p) {
     for (int i = 0; i < RT; ++i)
 #pragma unroll
         for (int n = 0; n < NT; ++n) acc[i][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int c = wave; c < chunks; c += W) {
-        const int64_t k = (int64_t)c * kChunk;
-        const bool whole = p.K - k >= kChunk;
-        quad w[RT];
-        Scales s[RT];
-#pragma unroll
-        for (int i = 0; i < RT; ++i) {
-            const uint8_t* at = p.Q + m[i] * p.ldq;
-            w[i] = whole ? *reinterpret_cast<const quad_any*>(at + k / 2 + 16 * g)
-                         : fp8dev::load_end(at, k / 2 + 16 * g, row_bytes);
-            s[i] = load_scales<T>(p, m[i], c);
-        }
-        Raw8<T> raw[NT][4];
+
+    struct Batch {
+        quad w[U][RT];
+        RawScales<T, G, U> s[RT];
+        Raw8<T> x[STAGED ? 1 : U][NT][4];
+    };
+    const auto load_x = [&](Raw8<T> (&to)[NT][4], int c, bool all) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) raw[n][j] = load_vec<T>(x[n], k + 32 * j + 8 * g, whole, p.K);
+            for (int j = 0; j < 4; ++j) to[n][j] = load_vec<T>(x[n], (int64_t)c * kChunk + 32 * j + 8 * g, all, p.K);
+    };
+    const auto load = [&](Batch& to, int c) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < RT; ++i)
+                to.w[u][i] = *reinterpret_cast<const quad_any*>(q[i] + (int64_t)(c + u) * (kChunk / 2));
+#pragma unroll
+        for (int i = 0; i < RT; ++i) to.s[i] = load_scales<T, G, U>(p, m[i], c, true);
+        if constexpr (!STAGED)
+#pragma unroll
+            for (int u = 0; u < U; ++u) load_x(to.x[u], c + u, true);
+    };
+    // a vector's (or part's) line in LDS: whole chunks and 16 bytes, so that lines
+    // start in other banks
+    const int pitch = chunks * kChunk * 2 + 16;
+    const uint8_t* line = lds + (r < PER * p.T ? r : PER * p.T - 1) * pitch + 16 * g;
+    struct Parts {
+        quad part[PARTS];
+    };
+    // the products of chunk c of the U that start at its batch's first
+    const auto chunk = [&](quad (&w)[RT], const auto (&scales)[RT], const Raw8<T> (&raw)[NT][4], int u, int c) {
 #pragma unroll
         for (int i = 0; i < RT; ++i) w[i] = transposed(w[i]);
+        multiply<MT, G, RT, NT, PARTS>(p, acc, w, scales, 4 * u, [&](int n, int j) {
+            Parts v;
+            if constexpr (STAGED) {
+                v.part[0] = *reinterpret_cast<const quad*>(line + c * 256 + 64 * j);
+            } else {
+                const Vec8<T> full = operand_of<T>(raw[n][j]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            Vec8<T> v[NT];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) v[n] = operand_of(raw[n][j]);
-#pragma unroll
-            for (int i = 0; i < RT; ++i) {
-                const quad b = values8(MT{}, w[i][j], s[i].offset[j]);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    f32x4 d{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                    for (int e = 0; e < Operand<T>::parts; ++e) d = gemvdev::mma_16x16x32(MT{}, v[n].part[e], b, d);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[i][n][e] = __builtin_fmaf(d[e], s[i].scale[j], acc[i][n][e]);
-                }
+                for (int e = 0; e < PARTS; ++e) v.part[e] = full.part[e];
             }
+            return v;
+        });
+    };
+    const auto work = [&](Batch& b, int c) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) chunk(b.w[u], b.s, b.x[STAGED ? 0 : u], u, c + u);
+    };
+    int c = wave * U;
+    Batch batch;
+    const bool any = c + U <= whole;
+    if (any) load(batch, c);
+    if constexpr (STAGED) {
+        const int pieces = chunks * 16;
+        for (int at = threadIdx.x; at < p.T * pieces; at += W * 64) {
+            const int t = at / pieces, piece = at - t * pieces;
+            const Vec8<T> v = operand_of<T>(load_vec<T>(static_cast<const typename T::storage*>(p.X) + t * p.ldx,
+                                                        piece * 8, p.K % kChunk == 0, p.K));
+#pragma unroll
+            for (int e = 0; e < PER; ++e)
+                *reinterpret_cast<quad*>(lds + (t * PER + e) * pitch + piece * 16) = v.part[e];
+        }
+        __syncthreads();
+    }
+    if (any) {
+        while (true) {
+            work(batch, c);
+            c += W * U;
+            if (c + U > whole) break;
+            load(batch, c);
         }
     }
+    // the last columns: fewer chunks than U, the last of fewer columns
+    for (int u = 0; u < U && c + u < chunks; ++u) {
+        const int64_t row_bytes = p.K / 2 + (p.K & 1);
+        quad w[RT];
+        RawScales<T, G, 1> s[RT];
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            w[i] = load_end(p.Q + m[i] * p.ldq, (int64_t)(c + u) * (kChunk / 2) + 16 * g, row_bytes);
+            s[i] = load_scales<T, G, 1>(p, m[i], c + u, false);
+        }
+        Raw8<T> raw[NT][4];
+        if constexpr (!STAGED) load_x(raw, c + u, false);
+        chunk(w, s, raw, 0, c + u);
+    }
+    // join: of the tile's 256 sums a thread takes one, vector e / 16, row e % 16
+    if constexpr (STAGED) __syncthreads();  // (the sums lie where the vectors did)
+    f32x4(*part)[64] = reinterpret_cast<f32x4(*)[64]>(lds);
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            if (i + n > 0) __syncthreads();
-            part[wave][lane] = acc[i][n];
-            __syncthreads();
-            // of the tile's 256 sums a thread takes one: vector e / 16, row e % 16
-            for (int e = threadIdx.x; e < 256; e += W * 64) {
-                const int tt = e >> 4, rr = e & 15;
-                const int t = t0 + 16 * n + tt, row = row0 + 16 * i + rr;
-                if (t >= p.T || row >= p.M) continue;
-                float v = part[0][(tt >> 2) * 16 + rr][tt & 3];
+        for (int n = 0; n < NT; ++n) part[(i * NT + n) * W + wave][lane] = acc[i][n];
+    __syncthreads();
+    for (int at = threadIdx.x; at < RT * NT * 256; at += W * 64) {
+        const int tile = at >> 8, i = tile / NT, n = tile - i * NT;
+        const int tt = at >> 4 & 15, rr = at & 15;
+        const int t = t0 + 16 * n + tt, row = row0 + 16 * i + rr;
+        if (PER * tt > 16 - PER || t >= p.T || row >= p.M) continue;
+        float v = 0.0f;
 #pragma unroll
-                for (int q = 1; q < W; ++q) v += part[q][(tt >> 2) * 16 + rr][tt & 3];
-                if (p.bias) v += p.bias[row];
-                store(p, t, row, v);
+        for (int a = 0; a < PER; ++a) {
+            const int from = PER * tt + a;
+#pragma unroll
+            for (int k = 0; k < W; ++k) v += part[tile * W + k][(from >> 2) * 16 + rr][from & 3];
+        }
+        if (p.bias) v += p.bias[row];
+        store(p, t, row, v);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// many vectors: X through LDS
+//
+// A workgroup takes 16·RT·W rows by 16·NT vectors, a wavefront 16·RT rows of its
+// own by all the vectors, so no weight is widened twice.  A chunk of 128 columns
+// of X lies in LDS in the order that the weights' values come out in, its parts one
+// behind the other; the next chunk's X and weights are loaded into registers
+// meanwhile.
+//
+// LDS.  A vector's 256 bytes of a chunk are 16 slots; slot s holds piece
+// s ^ (vector % 16), so that 16 lanes that want the same piece of 16 neighbouring
+// vectors find it in 16 different slots.
+// ---------------------------------------------------------------------------
+template <class T, int G, int RT, int NT, int W>
+__global__ __launch_bounds__(W * 64, 2) void q4_tile_kernel(Product p, int row_tiles) {
+    using MT = typename Operand<T>::type;
+    using R = RawScales<T, G, 1>;
+    constexpr int PARTS = Operand<T>::parts, BN = 16 * NT, BM = 16 * RT * W;
+    constexpr int kPieces = BN * 16 / (W * 64);       // of X, for each thread and chunk
+    constexpr int kPart = BN * 256, kStage = PARTS * kPart;
+    static_assert(BN * 16 % (W * 64) == 0 && W * 4 % 16 == 0,
+                  "whole pieces, which lie in the same slot of their vectors for each thread");
+    extern __shared__ __align__(16) uint8_t lds[];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int r = lane & 15, g = lane >> 4;
+    // the workgroups that share a chiplet's cache (every eighth) take
+    // neighbouring tiles: all the vectors of a row tile, then the next
+    const int tiles = gridDim.x, per = tiles / 8, id = blockIdx.x;
+    const int tile = id < per * 8 ? id % 8 * per + id / 8 : id;
+    const int token_tiles = tiles / row_tiles;
+    const int row0 = tile / token_tiles * BM, t0 = tile % token_tiles * BN;
+    const int chunks = p.K / kChunk + (p.K % kChunk != 0);
+    const int row_bytes = p.K / 2 + (p.K & 1);
+    // rows and vectors past the end repeat the last one; their results are not stored.
+    // Places are 32-bit offsets from the tile's first row or vector.
+    const int64_t first_row = row0 + wave * RT * 16 < p.M ? row0 + wave * RT * 16 : p.M - 1;
+    uint32_t q_at[RT], s_at[RT], z_at[RT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+        const int left = p.M - 1 - (int)first_row;
+        const uint32_t n = 16 * i + r < left ? 16 * i + r : left;
+        q_at[i] = n * (uint32_t)p.ldq + 16 * g;
+        s_at[i] = n * (uint32_t)p.lds * T::bytes;
+        z_at[i] = n * (uint32_t)p.ldz;
+    }
+    const uint8_t* q0 = p.Q + first_row * p.ldq;
+    const uint8_t* s0 = static_cast<const uint8_t*>(p.scale) + first_row * p.lds * T::bytes;
+    const uint8_t* z0 = p.zero + first_row * p.ldz;
+    const uint8_t* x0 = static_cast<const uint8_t*>(p.X) + t0 * p.ldx * T::bytes;
+    const int piece = threadIdx.x & 15, first = threadIdx.x >> 4;
+    const int to = first * 256 + 16 * (piece ^ (first & 15));
+
+    Raw8<T> ahead[kPieces];
+    quad next[RT];
+    R then[RT];
+    const auto fetch = [&](int c) {
+        const uint8_t* xc = scalar_here(x0 + (int64_t)c * (kChunk * T::bytes));
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            const int t = first + i * (W * 4), last = p.T - 1 - t0;
+            const uint32_t at = (uint32_t)(t < last ? t : last) * ((uint32_t)p.ldx * T::bytes) + piece * 8 * T::bytes;
+#pragma unroll
+            for (int h = 0; h < T::bytes / 2; ++h) ahead[i].v[h] = *reinterpret_cast<const quad_any*>(xc + offset_here(at + 16 * h));
+        }
+        const int g0 = 4 * c >> G;
+        const uint8_t* qc = scalar_here(q0 + (int64_t)c * (kChunk / 2));
+        const uint8_t* sc = scalar_here(s0 + (int64_t)g0 * T::bytes);
+        const uint8_t* zc = scalar_here(z0 + g0);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            next[i] = *reinterpret_cast<const quad_any*>(qc + offset_here(q_at[i]));
+            load_words<R::N * T::bytes>(sc + offset_here(s_at[i]), then[i].s);
+            load_words<R::N>(zc + offset_here(z_at[i]), then[i].z);
+        }
+    };
+    // the last chunk, where it has fewer columns
+    const auto fetch_end = [&](int c) {
+        const int id = fp8dev::worked_out_here(threadIdx.x);
+        const int64_t k = (int64_t)c * (kChunk * T::bytes);
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            const int t = t0 + (id >> 4) + i * (W * 4);
+            const uint8_t* row = static_cast<const uint8_t*>(p.X) + (t < p.T ? t : p.T - 1) * p.ldx * T::bytes;
+#pragma unroll
+            for (int h = 0; h < T::bytes / 2; ++h)
+                ahead[i].v[h] = load_end(row, k + (id & 15) * 8 * T::bytes + 16 * h, (int64_t)p.K * T::bytes);
+        }
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            const int row = row0 + ((id >> 6) * RT + i) * 16 + (id & 15);
+            const int64_t m = row < p.M ? row : p.M - 1;
+            next[i] = load_end(p.Q + m * p.ldq, (int64_t)c * (kChunk / 2) + 16 * ((id & 63) >> 4), row_bytes);
+            then[i] = load_scales<T, G, 1>(p, m, c, false);
+        }
+    };
+    const auto put_x = [&](int c) {
+        uint8_t* stage = lds + (c & 1) * kStage;
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            const Vec8<T> v = operand_of<T>(ahead[i]);
+#pragma unroll
+            for (int e = 0; e < PARTS; ++e)
+                *reinterpret_cast<quad*>(stage + e * kPart + to + i * (W * 4 * 256)) = v.part[e];
+        }
+    };
+    f32x4 acc[RT][NT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) acc[i][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    const int whole = p.K / kChunk;
+    if (whole > 0)
+        fetch(0);
+    else
+        fetch_end(0);
+    put_x(0);
+    __syncthreads();
+    const uint32_t exponent = exponent_of_1024();
+    for (int c = 0; c < chunks; ++c) {
+        quad w[RT];
+        R s[RT];
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            w[i] = transposed(next[i]);
+            s[i] = then[i];
+        }
+        if (c + 1 < whole) fetch(c + 1);
+        const uint8_t* stage = lds + (c & 1) * kStage + r * 256;
+        // a group's steps, two at most (of 128 columns in two halves, whose scales are alike)
+        constexpr int kSteps = G == 0 ? 1 : 2;
+#pragma unroll
+        for (int j0 = 0; j0 < 4; j0 += kSteps) {
+            __builtin_amdgcn_sched_barrier(0);
+            quad b[RT][kSteps];
+            float by[RT];
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+                by[i] = s[i].scale(j0);
+#pragma unroll
+                for (int e = 0; e < kSteps; ++e) b[i][e] = values8(MT{}, w[i][j0 + e], s[i].template offset<MT>(p, j0 + e), exponent);
+            }
+            // a vector tile's operands are read while the one before is multiplied, whose
+            // sums are scaled while the next one is
+            struct Tile {
+                quad v[kSteps][PARTS];
+            } v[2];
+            f32x4 d[2][RT];
+            const auto read = [&](int n, Tile& to) {
+#pragma unroll
+                for (int e = 0; e < kSteps; ++e)
+#pragma unroll
+                    for (int a = 0; a < PARTS; ++a)
+                        to.v[e][a] = *reinterpret_cast<const quad*>(stage + a * kPart + n * 4096 +
+                                                                    16 * ((4 * (j0 + e) + g) ^ r));
+            };
+            read(0, v[0]);
+#pragma unroll
+            for (int n = 0; n <= NT; ++n) {
+                __builtin_amdgcn_sched_barrier(0);
+                if (n + 1 < NT) read(n + 1, v[(n + 1) & 1]);
+                if (n < NT) {
+#pragma unroll
+                    for (int e = 0; e < kSteps; ++e)
+#pragma unroll
+                        for (int a = 0; a < PARTS; ++a)
+#pragma unroll
+                            for (int i = 0; i < RT; ++i) {
+                                if (e + a == 0) d[n & 1][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                                d[n & 1][i] = gemvdev::mma_16x16x32(MT{}, v[n & 1].v[e][a], b[i][e], d[n & 1][i]);
+                            }
+                }
+                if (n > 0)
+#pragma unroll
+                    for (int i = 0; i < RT; ++i) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            acc[i][n - 1][e] = __builtin_fmaf(d[(n - 1) & 1][i][e], by[i], acc[i][n - 1][e]);
+                        // (here, and not where the chunk ends: the sums would all wait in registers)
+                        asm volatile("" : "+v"(acc[i][n - 1]));
+                    }
+                if (n > 0 && n < NT) {
+                    constexpr int kProducts = RT * kSteps * PARTS, kEach = (4 * RT + kProducts - 1) / kProducts;
+#pragma unroll
+                    for (int i = 0; i < kProducts; ++i) {
+                        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                        __builtin_amdgcn_sched_group_barrier(0x002, kEach, 0);
+                    }
+                }
             }
         }
+        __builtin_amdgcn_sched_barrier(0);
+        if (c + 1 < chunks) {
+            if (c + 1 >= whole) fetch_end(c + 1);
+            put_x(c + 1);
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+        const int row = row0 + (wave * RT + i) * 16 + r;
+        if (row >= p.M) continue;
+        const float add = p.bias ? p.bias[row] : 0.0f;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int t = t0 + 16 * n + 4 * g + e;
+                if (t < p.T) store(p, t, row, acc[i][n][e] + add);
+            }
+    }
 }
 
 }  // namespace q4dev

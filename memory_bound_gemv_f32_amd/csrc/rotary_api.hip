@@ -19,6 +19,8 @@ static_assert(GEMV_ROTARY_MAX_PARTS == rotarydev::kMostParts && GEMV_ROTARY_MAX_
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+constexpr int kMostRows = 1 << 25;  // of one launch
+
 bool aligned(const void* p, int n) { return (uintptr_t)p % n == 0; }
 
 // A kernel and the heads of one of its steps.
@@ -29,8 +31,16 @@ struct Kernel {
 
 template <class D>
 Kernel kernel_of(int dim, int pairs) {
-    // four pairs to a lane where no run of four straddles the rotated ones' end,
-    // else one
+    // as many pairs to a lane as one 16-byte load of each half holds, or four, where no
+    // run of them straddles the rotated ones' end; else one
+    if constexpr (D::bytes == 2)
+        if (dim % 16 == 0 && pairs % 8 == 0) {
+            const int lanes = dim / 16;
+            if (lanes <= 4) return {(const void*)&rotarydev::rotary_kernel<D, 8, 4, 1>, 16};
+            if (lanes <= 8) return {(const void*)&rotarydev::rotary_kernel<D, 8, 8, 1>, 8};
+            if (lanes <= 16) return {(const void*)&rotarydev::rotary_kernel<D, 8, 16, 1>, 4};
+            return {(const void*)&rotarydev::rotary_kernel<D, 8, 32, 1>, 2};
+        }
     if (dim % 8 == 0 && pairs % 4 == 0) {
         const int lanes = dim / 8;
         if (lanes <= 8) return {(const void*)&rotarydev::rotary_kernel<D, 4, 8, 1>, 8};
@@ -40,6 +50,10 @@ Kernel kernel_of(int dim, int pairs) {
     }
     return {(const void*)&rotarydev::rotary_kernel<D, 1, 64, rotarydev::kMostDim / 128>, 1};
 }
+
+// Wavefronts that fill the GPU several times over: a row's heads go to as many
+// wavefronts as there are fewer rows than that.
+constexpr int64_t kEnoughWaves = 8192;
 
 bool known(int dtype) { return dtype == GEMV_DTYPE_F32 || dtype == GEMV_DTYPE_F16 || dtype == GEMV_DTYPE_BF16; }
 
@@ -57,7 +71,6 @@ gemv_status_t rotary(const gemv_rotary_part_t* parts, int count, int dim, int ro
                 !aligned(batch->seq_lens, 4) || !aligned(batch->starts, 4)))
         return GEMV_ERROR_INVALID_VALUE;
     Rotary p{};
-    int64_t heads = 0;
     for (int i = 0; i < count; ++i) {
         const gemv_rotary_part_t& a = parts[i];
         if (a.heads < 0 || !known(a.y_dtype) || a.ldx < (int64_t)a.heads * dim || a.ldy < (int64_t)a.heads * dim)
@@ -67,15 +80,16 @@ gemv_status_t rotary(const gemv_rotary_part_t* parts, int count, int dim, int ro
                     !aligned(a.y, a.y_dtype == GEMV_DTYPE_F32 ? 4 : 2) || !aligned(a.weight, 4)))
             return GEMV_ERROR_INVALID_VALUE;
         p.part[p.parts++] = rotarydev::Part{a.x, a.ldx, a.y, a.ldy, a.weight, a.heads, a.y_dtype};
-        heads += a.heads;
     }
-    if (!any || heads == 0) return GEMV_SUCCESS;
+    if (!any || p.parts == 0) return GEMV_SUCCESS;
     const Kernel k = kernel_of<D>(dim, pairs);
-    const int64_t groups = ceil_div(heads, k.heads);
-    p.steps = 1;
-    const int64_t across = ceil_div(groups, p.steps);
-    if (heads > 0x7fffffff || across > 65535 || (int64_t)rows * 64 > 0xffffffffll) return GEMV_ERROR_INVALID_VALUE;
-    p.heads = (int)heads;
+    int64_t steps = 0;
+    for (int i = 0; i < p.parts; ++i) steps += ceil_div(p.part[i].heads, k.heads);
+    if (steps > 0x7fffffff || rows > kMostRows) return GEMV_ERROR_INVALID_VALUE;
+    int64_t across = ceil_div(kEnoughWaves, rows);
+    across = across < steps ? across : steps;
+    p.steps = (int)steps;
+    p.each = (int)ceil_div(steps, across);
     p.dim = dim;
     p.pairs = pairs;
     p.interleaved = interleaved != 0;
@@ -84,7 +98,8 @@ gemv_status_t rotary(const gemv_rotary_part_t* parts, int count, int dim, int ro
     p.eps = eps;
     p.batch = kvdev::Batch{nullptr, 0, 0, batch->seq_lens, batch->starts, batch->sequences, rows};
     void* argv[] = {&p};
-    return finish(hipLaunchKernel(k.fn, dim3((unsigned)rows, (unsigned)across), dim3(64), argv, 0, stream));
+    const dim3 grid((unsigned)ceil_div(rows, rotarydev::kWaves), (unsigned)ceil_div(steps, p.each));
+    return finish(hipLaunchKernel(k.fn, grid, dim3(rotarydev::kWaves * 64), argv, 0, stream));
 }
 
 }  // namespace

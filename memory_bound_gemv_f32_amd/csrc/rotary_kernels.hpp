@@ -19,6 +19,7 @@ using fp8dev::TF32;
 using fp8dev::widen;
 
 constexpr int kMostParts = 4, kMostDim = 512;
+constexpr int kWaves = 4;  // rows of a workgroup
 
 struct Part {
     const void* x;
@@ -31,13 +32,13 @@ struct Part {
 };
 struct Rotary {
     Part part[kMostParts];
-    int parts, heads;     // heads of all parts
+    int parts, steps;     // steps: of all parts, each of one part's heads
     int dim, pairs;       // pairs: F
     bool interleaved;
     const float* frequency;
     float magnitude, eps;
     kvdev::Batch batch;
-    int steps;            // head groups that a wavefront takes
+    int each;             // steps of a wavefront
 };
 
 // The angle of a position in half turns, in [-1, 1].  frequency/π and its
@@ -52,39 +53,103 @@ __device__ __forceinline__ float half_turns(int position, float frequency) {
     return (float)(a - 2.0 * __builtin_rint(0.5 * a) + a_rest);
 }
 
+// N values of a type: as loaded, widened, and stored.
 template <class D, int N>
-__device__ __forceinline__ void load_run(const void* base, int64_t at, float (&v)[N]) {
-    kvdev::load_run<D, N>(static_cast<const typename D::storage*>(base) + at, v);
+struct __attribute__((packed, aligned(D::bytes))) Run {
+    typename D::storage v[N];
+};
+template <class D, int N>
+__device__ __forceinline__ Run<D, N> load_run(const void* base, int64_t at) {
+    return *reinterpret_cast<const Run<D, N>*>(static_cast<const typename D::storage*>(base) + at);
 }
 template <class D, int N>
-__device__ __forceinline__ void store_run(void* base, int64_t at, const float (&v)[N]) {
-    using S = typename D::storage;
-    struct __attribute__((packed, aligned(D::bytes))) Run {
-        S v[N];
-    } r;
+__device__ __forceinline__ void store_as(void* base, int64_t at, const float (&v)[N]) {
+    Run<D, N> r;
 #pragma unroll
     for (int i = 0; i < N; ++i) r.v[i] = fp8dev::narrow(D{}, v[i]);
-    *reinterpret_cast<Run*>(static_cast<S*>(base) + at) = r;
+    *reinterpret_cast<Run<D, N>*>(static_cast<typename D::storage*>(base) + at) = r;
 }
 template <int N>
 __device__ __forceinline__ void store_run(int type, void* base, int64_t at, const float (&v)[N]) {
     if (type == 0)
-        store_run<TF32>(base, at, v);
+        store_as<TF32>(base, at, v);
     else if (type == 1)
-        store_run<TF16>(base, at, v);
+        store_as<TF16>(base, at, v);
     else
-        store_run<TBF16>(base, at, v);
+        store_as<TBF16>(base, at, v);
 }
 
-// A wavefront takes one row; L lanes share a head, each V of its pairs at N
-// places, so 64 / L heads at a time.  A pair is also taken where nothing is
-// rotated: pairs from F on are the values 2s and 2s + 1.  The sines and cosines
-// are worked out once and serve all of a wavefront's heads.
+// The first and second values of V pairs that lie in two runs: as they are, or one pair
+// behind the other.
+template <class D, int V>
+__device__ __forceinline__ void pairs_of(const Run<D, V>& lo, const Run<D, V>& hi, bool together, float (&u)[V],
+                                         float (&v)[V]) {
+    float x[2 * V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        x[i] = widen(D{}, lo.v[i]);
+        x[V + i] = widen(D{}, hi.v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        u[i] = together ? x[2 * i] : x[i];
+        v[i] = together ? x[2 * i + 1] : x[V + i];
+    }
+}
+
+// A wavefront takes a row, 64 / L heads of one part at a time; L lanes share a
+// head, each V of its pairs at N places.  A pair is also taken where nothing is
+// rotated: pairs from F on are the values 2s and 2s + 1.  A lane works out the
+// angles of every 64th pair, and LDS hands their sines and cosines to the lanes
+// that want them, for all of the row's heads; the next heads' values are loaded
+// meanwhile.
 template <class D, int V, int L, int N>
-__global__ __launch_bounds__(64) void rotary_kernel(Rotary p) {
+__global__ __launch_bounds__(kWaves * 64) void rotary_kernel(Rotary p) {
     constexpr int kHeads = 64 / L;
-    const int lane = threadIdx.x, in = lane % L;
-    const int row = (int)blockIdx.x;
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    __shared__ f32x2 turns[kWaves][kMostDim / 2];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, in = lane % L;
+    const int row = (int)blockIdx.x * kWaves + wave;
+    if (row >= p.batch.total) return;
+    const int half = p.dim / 2;
+    int slot[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) slot[n] = (in + L * n) * V;
+    // a lane's values at its places: pairs' first values, then their second ones, or
+    // the pairs one behind the other
+    struct Raw {
+        Run<D, V> lo[N], hi[N];
+    };
+    const int from = (int)blockIdx.y * p.each;
+    const int until = from + p.each < p.steps ? from + p.each : p.steps;
+    // the part and the first head of a step
+    const auto place = [&](int step, int& at, int& head) {
+        at = 0;
+        head = step;
+        while (at + 1 < p.parts) {
+            const int steps = (p.part[at].heads + kHeads - 1) / kHeads;
+            if (head < steps) break;
+            head -= steps;
+            ++at;
+        }
+        head = head * kHeads + lane / L;
+    };
+    const auto load = [&](int step, Raw& to) {
+        int at, head;
+        place(step, at, head);
+        const Part& part = p.part[at];
+        head = head < part.heads ? head : part.heads - 1;  // (spare lanes repeat the last, and store nothing)
+        const int64_t base = row * part.ldx + (int64_t)head * p.dim;
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const int at_slot = slot[n] < half ? slot[n] : half - V;  // (likewise)
+            const bool together = p.interleaved || at_slot >= p.pairs;
+            to.lo[n] = load_run<D, V>(part.x, base + (together ? 2 * at_slot : at_slot));
+            to.hi[n] = load_run<D, V>(part.x, base + (together ? 2 * at_slot + V : at_slot + p.pairs));
+        }
+    };
+    Raw raw;
+    load(from, raw);
     int b;
     if (p.batch.starts == nullptr)
         b = row;
@@ -93,83 +158,86 @@ __global__ __launch_bounds__(64) void rotary_kernel(Rotary p) {
     const int start = kvdev::start_of(p.batch, b), stop = kvdev::start_of(p.batch, b + 1);
     if (row < start || row >= stop) return;  // padding
     const int position = p.batch.lens[b] - (stop - row);
-    const int half = p.dim / 2;
-    int slot[N];
+    for (int i = lane; i < p.pairs; i += 64) {
+        float s, c;
+        sincospif(half_turns(position, p.frequency[i]), &s, &c);
+        turns[wave][i] = f32x2{c * p.magnitude, s * p.magnitude};
+    }
+    // (a wavefront's own: its LDS accesses are in order)
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     float c[N][V], s[N][V];
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-        slot[n] = (in + L * n) * V;
+    for (int n = 0; n < N; ++n)
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            c[n][i] = 1.0f;
-            s[n][i] = 0.0f;
-            if (slot[n] + i < p.pairs) {
-                sincospif(half_turns(position, p.frequency[slot[n] + i]), &s[n][i], &c[n][i]);
-                c[n][i] *= p.magnitude;
-                s[n][i] *= p.magnitude;
+            const bool turned = slot[n] + i < p.pairs;
+            const f32x2 t = turns[wave][turned ? slot[n] + i : 0];
+            c[n][i] = turned ? t[0] : 1.0f;
+            s[n][i] = turned ? t[1] : 0.0f;
+        }
+    // a part's weights stay in registers while its heads last
+    float wu[N][V], wv[N][V];
+    int weighted = -1;
+    for (int step = from; step < until; ++step) {
+        int at, head;
+        place(step, at, head);
+        const Part& part = p.part[at];
+        if (part.weight && weighted != at) {
+            weighted = at;
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                const int at_slot = slot[n] < half ? slot[n] : half - V;
+                const bool together = p.interleaved || at_slot >= p.pairs;
+                const Run<TF32, V> lo = load_run<TF32, V>(part.weight, together ? 2 * at_slot : at_slot);
+                const Run<TF32, V> hi = load_run<TF32, V>(part.weight, together ? 2 * at_slot + V : at_slot + p.pairs);
+                pairs_of<TF32>(lo, hi, together, wu[n], wv[n]);
             }
         }
-    }
-    for (int step = 0; step < p.steps; ++step) {
-        const int head = ((int)blockIdx.y * p.steps + step) * kHeads + lane / L;
-        const bool there = head < p.heads;
-        // the part that the head is of (a lane without one takes the first, and stores nothing)
-        int at = 0, h = there ? head : 0;
-        while (at + 1 < p.parts && h >= p.part[at].heads) h -= p.part[at++].heads;
-        const Part& part = p.part[at];
-        const int64_t from = row * part.ldx + (int64_t)h * p.dim, to = row * part.ldy + (int64_t)h * p.dim;
-        float x[N][2 * V];
+        float u[N][V], v[N][V];
         float squares = 0.0f;
 #pragma unroll
         for (int n = 0; n < N; ++n) {
+            const bool together = p.interleaved || slot[n] >= p.pairs;
+            pairs_of<D>(raw.lo[n], raw.hi[n], together, u[n], v[n]);
+            if (slot[n] < half)
 #pragma unroll
-            for (int i = 0; i < 2 * V; ++i) x[n][i] = 0.0f;
-            if (slot[n] >= half) continue;
-            if (p.interleaved || slot[n] >= p.pairs) {
-                load_run<D, 2 * V>(part.x, from + 2 * slot[n], x[n]);
-            } else {
-                float lo[V], hi[V];
-                load_run<D, V>(part.x, from + slot[n], lo);
-                load_run<D, V>(part.x, from + slot[n] + p.pairs, hi);
+                for (int i = 0; i < V; ++i)
+                    squares = __builtin_fmaf(u[n][i], u[n][i], __builtin_fmaf(v[n][i], v[n][i], squares));
+        }
+        if (step + 1 < until) load(step + 1, raw);
+        if (part.weight) {
+            squares = gemvdev::segment_sum<L>(squares);
+            const float by = 1.0f / sqrtf(squares / (float)p.dim + p.eps);
+#pragma unroll
+            for (int n = 0; n < N; ++n)
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    x[n][2 * i] = lo[i];
-                    x[n][2 * i + 1] = hi[i];
+                    u[n][i] *= by * wu[n][i];
+                    v[n][i] *= by * wv[n][i];
                 }
-            }
-#pragma unroll
-            for (int i = 0; i < 2 * V; ++i) squares = __builtin_fmaf(x[n][i], x[n][i], squares);
         }
-        squares = gemvdev::segment_sum<L>(squares);
-        if (!there) continue;
-        const float by = part.weight ? 1.0f / sqrtf(squares / (float)p.dim + p.eps) : 1.0f;
+        if (head >= part.heads) continue;
+        const int64_t base = row * part.ldy + (int64_t)head * p.dim;
 #pragma unroll
         for (int n = 0; n < N; ++n) {
             if (slot[n] >= half) continue;
-            const bool together = p.interleaved || slot[n] >= p.pairs;
-            float y[2 * V];
+            float lo[V], hi[V];
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                float u = x[n][2 * i], v = x[n][2 * i + 1];
-                if (part.weight) {
-                    const int j = slot[n] + i;
-                    u *= by * part.weight[together ? 2 * j : j];
-                    v *= by * part.weight[together ? 2 * j + 1 : j + p.pairs];
-                }
-                y[2 * i] = __builtin_fmaf(u, c[n][i], -(v * s[n][i]));
-                y[2 * i + 1] = __builtin_fmaf(v, c[n][i], u * s[n][i]);
+                lo[i] = __builtin_fmaf(u[n][i], c[n][i], -(v[n][i] * s[n][i]));
+                hi[i] = __builtin_fmaf(v[n][i], c[n][i], u[n][i] * s[n][i]);
             }
-            if (together) {
-                store_run<2 * V>(part.y_type, part.y, to + 2 * slot[n], y);
-            } else {
-                float lo[V], hi[V];
+            if (p.interleaved || slot[n] >= p.pairs) {
+                float y[2 * V];
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    lo[i] = y[2 * i];
-                    hi[i] = y[2 * i + 1];
+                    y[2 * i] = lo[i];
+                    y[2 * i + 1] = hi[i];
                 }
-                store_run<V>(part.y_type, part.y, to + slot[n], lo);
-                store_run<V>(part.y_type, part.y, to + slot[n] + p.pairs, hi);
+                store_run(part.y_type, part.y, base + 2 * slot[n], y);
+            } else {
+                store_run(part.y_type, part.y, base + slot[n], lo);
+                store_run(part.y_type, part.y, base + slot[n] + p.pairs, hi);
             }
         }
     }
