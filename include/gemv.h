@@ -465,8 +465,7 @@ typedef struct {
  * Errors: GEMV_ERROR_INVALID_VALUE for sizes that are not as above, another
  * y_dtype, a pitch below heads·dim, a NULL or misaligned pointer, rows !=
  * sequences without starts, an eps that is negative or not finite, a magnitude
- * that is not finite, and more rows or heads than one launch holds (never with
- * up to 2^25 rows and 65535 heads). */
+ * that is not finite, and more than 2^25 rows. */
 #define GEMV_ROTARY_MAX_PARTS 4
 #define GEMV_ROTARY_MAX_DIM 512
 

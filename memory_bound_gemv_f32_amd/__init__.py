@@ -35,6 +35,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import struct
 from pathlib import Path
 
 # torch ships its own HIP runtime under the same soname (libamdhip64.so.7) as
@@ -200,7 +201,10 @@ gemv_q4_f32 = _bind("gemv_q4_f32", _q4_args)
 gemv_q4_f16 = _bind("gemv_q4_f16", _q4_args)
 gemv_q4_bf16 = _bind("gemv_q4_bf16", _q4_args)
 ROTARY_MAX_PARTS, ROTARY_MAX_DIM = 4, 512
-_rotary_args = [ctypes.POINTER(RotaryPartStruct), _i, _i, _i, _vp, _i, _i, ctypes.c_float, ctypes.c_float, _batch_p, _st]
+# (parts and batch: structures, or bytes laid out like them)
+_rotary_args = [_vp, _i, _i, _i, _vp, _i, _i, ctypes.c_float, ctypes.c_float, _vp, _st]
+_ROTARY_PART, _KV_BATCH = struct.Struct("@PiPiiiP0P"), struct.Struct("@iPiiPP0P")
+assert _ROTARY_PART.size == ctypes.sizeof(RotaryPartStruct) and _KV_BATCH.size == ctypes.sizeof(KvBatchStruct)
 gemv_rotary_f32 = _bind("gemv_rotary_f32", _rotary_args)
 gemv_rotary_f16 = _bind("gemv_rotary_f16", _rotary_args)
 gemv_rotary_bf16 = _bind("gemv_rotary_bf16", _rotary_args)
@@ -518,7 +522,7 @@ def gemv_gate_up_silu(A_gate, A_up, x, out=None, *, stream=None):
 # ordered so that the usual call (contiguous tensors on the current device)
 # passes through few of them.
 if _torch_runtime is not None:
-    _F32, _I32 = _torch_runtime.float32, _torch_runtime.int32
+    _F32, _I32, _U8 = _torch_runtime.float32, _torch_runtime.int32, _torch_runtime.uint8
     _E4M3_BYTES = (_torch_runtime.float8_e4m3fn, _torch_runtime.uint8)
 
     def _by_dtype(f32, f16, bf16):
@@ -587,6 +591,16 @@ def _rows(t, name, dev):
     if not cols <= pitch <= _MOST:
         raise ValueError(f"{name}'s row stride is smaller than its rows, or more than an int counts")
     return rows, cols, pitch
+
+
+def _like(t, name, rows, cols, dtype, dev):
+    """The row stride of a (rows, cols) matrix of ``dtype`` with unit column
+    stride on device ``dev``."""
+    if t.shape != (rows, cols) or t.dtype is not dtype:
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {(rows, cols)}")
+    if t.get_device() == dev and t.is_contiguous():
+        return cols
+    return _rows(t, name, dev)[2]
 
 
 def _scales(t, name, rows, cols, dev):
@@ -674,28 +688,23 @@ def gemv_q4(Q, scale, X, bias=None, out=None, *, zero=None, group: int = 128, ou
     with unit column stride, any nvec, or (K,), in float32, float16 or bfloat16.
     Returns (nvec, M) or (M,) float32, or in ``out_dtype`` / out's dtype; out may
     be a column slice of a wider matrix."""
-    fn = _entry(_Q4, X.dtype)
+    dtype = X.dtype
+    fn = _entry(_Q4, dtype)
     dev = X.get_device()
     single = X.dim() == 1
-    if single:
-        X = X.unsqueeze(0)
-    nvec, K, ldx = _rows(X, "X", dev)
-    if Q.dtype is not _torch_runtime.uint8:
+    nvec, K, ldx = _rows(X.unsqueeze(0) if single else X, "X", dev)
+    if Q.dtype is not _U8:
         raise TypeError("Q must be uint8")
     M, across, ldq = _rows(Q, "Q", dev)
     if across != (K + 1) // 2:
         raise ValueError("Q must have a byte for each two columns of X")
-    if group != 32 and group != 64 and group != 128:
+    if group != 128 and group != 64 and group != 32:
         raise ValueError("group must be 32, 64 or 128")
     groups = -(-K // group)
-    have, across, lds = _rows(scale, "scale", dev)
-    if have != M or across != groups or scale.dtype is not X.dtype:
-        raise ValueError(f"scale must be of X's dtype and shape {(M, groups)}")
+    lds = _like(scale, "scale", M, groups, dtype, dev)
     zptr, ldz = None, 0
     if zero is not None:
-        have, across, ldz = _rows(zero, "zero", dev)
-        if have != M or across != groups or zero.dtype is not _torch_runtime.uint8:
-            raise ValueError(f"zero must be a uint8 tensor of shape {(M, groups)}")
+        ldz = _like(zero, "zero", M, groups, _U8, dev)
         zptr = zero.data_ptr()
     if bias is not None:
         bias = _check_bias(bias, M, Q.device).data_ptr()
@@ -709,9 +718,9 @@ def gemv_q4(Q, scale, X, bias=None, out=None, *, zero=None, group: int = 128, ou
         if out_dtype is not None and out.dtype != out_dtype:
             raise ValueError("out is not of out_dtype")
         code = _entry(_CODES, out.dtype)
-        rows, cols, ldy = _rows(out.unsqueeze(0) if single else out, "out", dev)
-        if (rows, cols) != (nvec, M) or out.dim() != (1 if single else 2):
+        if out.dim() != (1 if single else 2):
             raise ValueError(f"out must be of shape {(M,) if single else (nvec, M)}")
+        ldy = _like(out.unsqueeze(0) if single else out, "out", nvec, M, out.dtype, dev)
     _call(dev, stream, fn, Q.data_ptr(), ldq, scale.data_ptr(), lds, zptr, ldz, group, X.data_ptr(), ldx, bias,
           out.data_ptr(), code, ldy, M, K, nvec)
     return out
@@ -755,19 +764,46 @@ def _head_rows(t, name, dim, dev):
     """(rows, heads, row stride) of a (rows, heads, dim) tensor whose rows may
     be columns of a wider matrix."""
     shape = t.shape
-    if len(shape) != 3 or shape[2] != dim or t.get_device() != dev:
+    if len(shape) != 3 or shape[2] != dim or dev < 0 or t.get_device() != dev:
         raise ValueError(f"{name} must be a device tensor (rows, heads, {dim}), all on one device")
     rows, heads, _ = shape
     if rows > _MOST or heads * dim > _MOST:
         raise ValueError(f"{name} has more rows or columns than an int counts")
     if t.is_contiguous():
         return rows, heads, heads * dim
-    if (dim > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != dim):
+    pitch, of_heads, of_values = t.stride()
+    if (of_values != 1 and dim > 1) or (of_heads != dim and heads > 1):
         raise ValueError(f"{name}'s heads must lie one behind the other in a row")
-    pitch = t.stride(0) if rows > 1 else heads * dim
+    if rows <= 1:
+        pitch = heads * dim
     if not heads * dim <= pitch <= _MOST:
         raise ValueError(f"{name}'s row stride is smaller than its rows, or more than an int counts")
     return rows, heads, pitch
+
+
+def _rotary_part(x, name, total, dim, dev, weight, out, dtype, stream):
+    """(the part's bytes, its result)"""
+    rows, heads, ldx = _head_rows(x, name, dim, dev)
+    if rows != total:
+        raise ValueError("Q and K must have the same rows")
+    wptr = 0
+    if weight is not None:
+        if weight.dtype is not _F32 or weight.shape != (dim,) or not weight.is_contiguous() \
+                or weight.get_device() != dev:
+            raise ValueError(f"{name}'s weight must be a contiguous float32 tensor of shape {(dim,)} on its device")
+        wptr = weight.data_ptr()
+    if out is None:
+        if dtype is None:
+            dtype = x.dtype
+        code = _entry(_CODES, dtype)
+        out = _empty(x, (rows, heads, dim), dtype, stream)
+        ldy = heads * dim
+    else:
+        if out.shape != x.shape or (dtype is not None and out.dtype is not dtype):
+            raise ValueError(f"{name}'s output must have its shape, and the dtype asked for")
+        code = _entry(_CODES, out.dtype)
+        ldy = _head_rows(out, f"{name}'s output", dim, dev)[2]
+    return _ROTARY_PART.pack(x.data_ptr(), ldx, out.data_ptr(), ldy, heads, code, wptr), out
 
 
 def gemv_rotary(Q, K, frequency, seq_lens, starts=None, *, q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -790,52 +826,34 @@ def gemv_rotary(Q, K, frequency, seq_lens, starts=None, *, q_weight=None, k_weig
     dev = Q.get_device()
     if Q.dim() != 3:
         raise ValueError("Q must be (rows, heads, dim)")
-    dim, total = Q.shape[2], Q.shape[0]
-    if dev < 0:
-        raise ValueError("Q must be a device tensor")
-    parts, results = (RotaryPartStruct * 2)(), []
-    for n, (x, name, weight, out, dtype) in enumerate((
-            (Q, "Q", q_weight, q_out, q_dtype), (K, "K", k_weight, k_out, k_dtype))):
-        if x is None:
-            if weight is not None or out is not None:
-                raise ValueError("K's weight and output need a K")
-            results.append(None)
-            continue
-        if x.dtype is not Q.dtype:
-            raise ValueError("Q and K must have the same dtype")
-        rows, heads, ldx = _head_rows(x, name, dim, dev)
-        if rows != total:
-            raise ValueError("Q and K must have the same rows")
-        if weight is not None:
-            if weight.dtype is not _F32 or weight.shape != (dim,) or not weight.is_contiguous() \
-                    or weight.get_device() != dev:
-                raise ValueError(f"{name}'s weight must be a contiguous float32 tensor of shape {(dim,)} on its device")
-            weight = weight.data_ptr()
-        if out is None:
-            out = _empty(x, (rows, heads, dim), x.dtype if dtype is None else dtype, stream)
-            ldy = heads * dim
-        else:
-            if out.shape != x.shape or (dtype is not None and out.dtype is not dtype):
-                raise ValueError(f"{name}'s output must have its shape, and the dtype asked for")
-            ldy = _head_rows(out, name + "'s output", dim, dev)[2]
-        parts[n] = RotaryPartStruct(x.data_ptr(), ldx, out.data_ptr(), ldy, heads, _entry(_CODES, out.dtype), weight)
-        results.append(out)
+    total, _, dim = Q.shape
+    if K is not None and K.dtype is not Q.dtype:
+        raise ValueError("Q and K must have the same dtype")
+    parts, Q = _rotary_part(Q, "Q", total, dim, dev, q_weight, q_out, q_dtype, stream)
+    count = 1
+    if K is not None:
+        part, K = _rotary_part(K, "K", total, dim, dev, k_weight, k_out, k_dtype, stream)
+        parts += part
+        count = 2
+    elif k_weight is not None or k_out is not None:
+        raise ValueError("K's weight and output need a K")
     if frequency.dtype is not _F32 or frequency.dim() != 1 or not frequency.is_contiguous() \
             or frequency.get_device() != dev:
         raise ValueError("frequency must be a contiguous float32 tensor (pairs,) on Q's device")
     if seq_lens.dtype is not _I32 or seq_lens.dim() != 1 or not seq_lens.is_contiguous() or seq_lens.get_device() != dev:
         raise ValueError("seq_lens must be a contiguous int32 (sequences,) tensor on Q's device")
-    sequences = seq_lens.shape[0]
+    sequences, sptr = seq_lens.shape[0], 0
     if starts is None:
         if total != sequences:
             raise ValueError("without starts every sequence has one row")
-    elif starts.dtype is not _I32 or starts.shape != (sequences + 1,) or not starts.is_contiguous() \
-            or starts.get_device() != dev:
-        raise ValueError("starts must be a contiguous int32 (sequences + 1,) tensor on Q's device")
-    batch = KvBatchStruct(sequences, None, 0, 0, seq_lens.data_ptr(), None if starts is None else starts.data_ptr())
-    _call(dev, stream, fn, parts, 1 if K is None else 2, dim, total, frequency.data_ptr(), frequency.shape[0],
-          1 if interleaved else 0, magnitude, eps, ctypes.byref(batch))
-    return results[0], results[1]
+    else:
+        if starts.dtype is not _I32 or starts.shape != (sequences + 1,) or not starts.is_contiguous() \
+                or starts.get_device() != dev:
+            raise ValueError("starts must be a contiguous int32 (sequences + 1,) tensor on Q's device")
+        sptr = starts.data_ptr()
+    _call(dev, stream, fn, parts, count, dim, total, frequency.data_ptr(), frequency.shape[0], 1 if interleaved else 0,
+          magnitude, eps, _KV_BATCH.pack(sequences, 0, 0, 0, seq_lens.data_ptr(), sptr))
+    return Q, K
 
 
 # ---------------------------------------------------------------------------

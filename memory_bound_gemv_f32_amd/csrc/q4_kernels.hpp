@@ -594,8 +594,10 @@ __global__ __launch_bounds__(W * 64, 2) void q4_tile_kernel(Product p, int row_t
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
             next[i] = *reinterpret_cast<const quad_any*>(qc + offset_here(q_at[i]));
-            load_words<R::N * T::bytes>(sc + offset_here(s_at[i]), then[i].s);
-            load_words<R::N>(zc + offset_here(z_at[i]), then[i].z);
+            R raw;
+            load_words<R::N * T::bytes>(sc + offset_here(s_at[i]), raw.s);
+            load_words<R::N>(zc + offset_here(z_at[i]), raw.z);
+            then[i] = raw;
         }
     };
     // the last chunk, where it has fewer columns
