@@ -86,51 +86,70 @@ gemv_status_t join(const Mapping& m, Attend& p, Attend& s, int64_t shared_places
     int64_t places = m.places;
     void* argv[] = {&p, &places, &s, &shared_places};
     constexpr int kTwo = DIM <= 128 ? 2 : 1;
-    const void* fn = m.waves_share == 1
-                         ? (const void*)&kvdev::kv_join_kernel<T, DIM, 16 * kvdev::kOwnWaves * kTwo, 16 * kTwo, SHARED>
-                     : m.row_tiles == 2 ? (const void*)&kvdev::kv_join_kernel<T, DIM, 16 * kTwo, 16 * kTwo, SHARED>
-                                        : (const void*)&kvdev::kv_join_kernel<T, DIM, 16, 16, SHARED>;
-    return launch(fn, dim3((unsigned)(places * p.cache.heads), (unsigned)m.place_rows),
-                  kvdev::kShareWaves * 64, argv, stream);
+    const void* fn;
+    int rows = m.place_rows;
+    if constexpr (SHARED) {
+        if (p.splits + s.splits <= kvdev::kFewSplits) {
+            fn = m.waves_share == 1
+                     ? (const void*)&kvdev::kv_join_rows_kernel<T, DIM, 16 * kvdev::kOwnWaves * kTwo, 16 * kTwo>
+                 : m.row_tiles == 2 ? (const void*)&kvdev::kv_join_rows_kernel<T, DIM, 16 * kTwo, 16 * kTwo>
+                                    : (const void*)&kvdev::kv_join_rows_kernel<T, DIM, 16, 16>;
+            rows = (rows + kvdev::kShareWaves - 1) / kvdev::kShareWaves;
+            return launch(fn, dim3((unsigned)(places * p.cache.heads), (unsigned)rows), kvdev::kShareWaves * 64, argv,
+                          stream);
+        }
+    }
+    fn = m.waves_share == 1
+             ? (const void*)&kvdev::kv_join_kernel<T, DIM, 16 * kvdev::kOwnWaves * kTwo, 16 * kTwo, SHARED>
+         : m.row_tiles == 2 ? (const void*)&kvdev::kv_join_kernel<T, DIM, 16 * kTwo, 16 * kTwo, SHARED>
+                            : (const void*)&kvdev::kv_join_kernel<T, DIM, 16, 16, SHARED>;
+    return launch(fn, dim3((unsigned)(places * p.cache.heads), (unsigned)rows), kvdev::kShareWaves * 64, argv, stream);
 }
 
-template <class T, class F, int DIM, bool SHARED>
+template <class T, class F, int DIM>
 gemv_status_t walk(const Mapping& m, Attend& p, hipStream_t stream) {
     int64_t places = m.places;
     const int64_t grid = places * p.cache.heads * p.splits;
     void* argv[] = {&p, &places};
     constexpr int kTwo = DIM <= 128 ? 2 : 1;
     constexpr int kSmall = DIM <= 128 ? DIM : 128;  // (dim 256 has no eight, see cut)
-    const void* fn = nullptr;
-    if constexpr (!SHARED)
-        if (m.waves_share == 1) fn = (const void*)&kvdev::kv_attend_kernel<T, F, DIM, kTwo, 1>;
-    if (fn == nullptr)
-        fn = m.row_tiles == 2     ? (const void*)&kvdev::kv_attend_kernel<T, F, DIM, kTwo, 4, SHARED>
-             : m.waves_share == 8 ? (const void*)&kvdev::kv_attend_kernel<T, F, kSmall, 1, 8, SHARED>
-                                  : (const void*)&kvdev::kv_attend_kernel<T, F, DIM, 1, 4, SHARED>;
+    const void* fn = m.waves_share == 1 ? (const void*)&kvdev::kv_attend_kernel<T, F, DIM, kTwo, 1>
+                     : m.row_tiles == 2 ? (const void*)&kvdev::kv_attend_kernel<T, F, DIM, kTwo, 4>
+                     : m.waves_share == 8 ? (const void*)&kvdev::kv_attend_kernel<T, F, kSmall, 1, 8>
+                                          : (const void*)&kvdev::kv_attend_kernel<T, F, DIM, 1, 4>;
     return launch(fn, dim3((unsigned)grid), 64 * kvplan::waves_of(m), argv, stream);
+}
+
+// The shared tokens, and each sequence's own in the same launch where their row
+// tiles are of 16 (with two of 32 the workgroup would take a compute unit's LDS alone).
+template <class T, class F, int DIM>
+gemv_status_t walk_shared(const SharedMapping& m, Attend& s, Attend& p, hipStream_t stream) {
+    constexpr int kTwo = DIM <= 128 ? 2 : 1;
+    const bool together = kvplan::together(m);
+    int64_t shared_places = m.shared.places, own_places = together ? m.own.places : 0;
+    const int64_t grid = shared_places * s.cache.heads * s.splits + own_places * p.cache.heads * p.splits;
+    void* argv[] = {&s, &shared_places, &p, &own_places};
+    const void* fn = m.shared.row_tiles == 2 ? (const void*)&kvdev::kv_attend_shared_kernel<T, F, DIM, kTwo>
+                                             : (const void*)&kvdev::kv_attend_shared_kernel<T, F, DIM, 1>;
+    const gemv_status_t st = launch(fn, dim3((unsigned)grid), 64 * kvdev::kShareWaves, argv, stream);
+    return st != GEMV_SUCCESS || together ? st : walk<T, F, DIM>(m.own, p, stream);
 }
 
 template <class T, class F, int DIM>
 gemv_status_t attend(const SharedMapping& m, Attend& p, hipStream_t stream) {
     Attend s = p;
-    if constexpr (DIM <= 128) {
-        if (m.chunks > 0) {
-            s.splits = m.shared.splits;
-            s.split_chunks = m.shared.split_chunks;
-            s.rows = m.shared.place_rows;
-            s.capacity = m.chunks * kvplan::kChunk;
-            s.shared = 0;
-            s.partial = p.partial + kvplan::partials_of(m.own, p.cache.heads, DIM) / sizeof(float);
-            const gemv_status_t st = walk<T, F, DIM, true>(m.shared, s, stream);
-            if (st != GEMV_SUCCESS) return st;
-        }
+    if (m.chunks > 0) {
+        s.splits = m.shared.splits;
+        s.split_chunks = m.shared.split_chunks;
+        s.rows = m.shared.place_rows;
+        s.capacity = m.chunks * kvplan::kChunk;
+        s.shared = 0;
+        s.partial = p.partial + kvplan::partials_of(m.own, p.cache.heads, DIM) / sizeof(float);
+        const gemv_status_t st = walk_shared<T, F, DIM>(m, s, p, stream);
+        return st != GEMV_SUCCESS ? st : join<T, DIM, true>(m.own, p, s, m.shared.places, stream);
     }
-    const gemv_status_t st = walk<T, F, DIM, false>(m.own, p, stream);
-    if (st != GEMV_SUCCESS) return st;
-    if constexpr (DIM <= 128)
-        if (m.chunks > 0) return join<T, DIM, true>(m.own, p, s, m.shared.places, stream);
-    return p.splits == 1 ? st : join<T, DIM, false>(m.own, p, s, 0, stream);
+    const gemv_status_t st = walk<T, F, DIM>(m.own, p, stream);
+    return st != GEMV_SUCCESS || p.splits == 1 ? st : join<T, DIM, false>(m.own, p, s, 0, stream);
 }
 
 template <class T, class F>

@@ -541,8 +541,8 @@ __device__ __forceinline__ Partial partial_at(const Attend& p, int64_t places, i
 // and join in LDS.  WS = 1: each wavefront has a row tile of its own.  SHARED: the
 // rows of all sequences over the p.capacity tokens that they share; the results
 // are partial ones.
-template <class T, class F, int DIM, int RT, int WS, bool SHARED = false>
-__global__ __launch_bounds__(kWavesOf<WS> * 64, DIM <= 128 ? 2 : 1) void kv_attend_kernel(Attend p, int64_t places) {
+template <class T, class F, int DIM, int RT, int WS, bool SHARED>
+__device__ __forceinline__ void attend_part(const Attend& p, int64_t places, int64_t workgroup) {
     constexpr int kRows = 16 * RT;                              // rows of a wavefront
     constexpr int kGroupRows = WS == 1 ? kOwnWaves * kRows : kRows;
     constexpr int kSteps = DIM / 32;                            // K·Q^T steps
@@ -552,11 +552,13 @@ __global__ __launch_bounds__(kWavesOf<WS> * 64, DIM <= 128 ? 2 : 1) void kv_atte
     const Cache& c = p.cache;
     // heads fastest: neighbouring workgroups, which go to different chiplets,
     // share no K or V; then the splits
-    int64_t at = blockIdx.x;
+    int64_t at = workgroup;
     const int head = (int)(at % c.heads);
     at /= c.heads;
-    const int split = (int)(at % p.splits);
-    const int64_t place = at / p.splits;
+    // (the places of shared tokens before their splits: they read the same bytes)
+    const int64_t outer = SHARED ? places : p.splits;
+    const int split = (int)(SHARED ? at / outer : at % outer);
+    const int64_t place = SHARED ? at % outer : at / outer;
     Tile t;
     if (!(SHARED ? shared_tile_of<kGroupRows>(p, place, t) : tile_of<kGroupRows>(p, place, t))) return;
     const int r0 = t.r0 + (WS == 1 ? wave * kRows : 0);
@@ -587,7 +589,10 @@ __global__ __launch_bounds__(kWavesOf<WS> * 64, DIM <= 128 ? 2 : 1) void kv_atte
     // ... and its Q
     // (two tiles' Q does not fit the registers beside the rest: it stays in LDS)
     constexpr bool kQInLds = RT > 1;
-    __shared__ quad q_lds[kQInLds ? kWavesOf<WS> : 1][kQInLds ? RT : 1][kQInLds ? kSteps : 1][64];
+    // (wavefronts that share their rows write the same)
+    constexpr int kCopies = kQInLds && !SHARED ? kWavesOf<WS> : 1;
+    __shared__ quad q_lds[kCopies][kQInLds ? RT : 1][kQInLds ? kSteps : 1][64];
+    const int copy = kCopies > 1 ? wave : 0;
     int64_t row[RT];     // row of the call
     int qhead[RT];
     quad q[RT][kSteps];
@@ -605,10 +610,10 @@ __global__ __launch_bounds__(kWavesOf<WS> * 64, DIM <= 128 ? 2 : 1) void kv_atte
             q[i][s] = *reinterpret_cast<const quad_any*>(src + 64 * (s >> 1) + 8 * (s & 1)) ^ p.q_sign;
         if constexpr (kQInLds)  // read back by the lane that wrote it
 #pragma unroll
-            for (int s = 0; s < kSteps; ++s) q_lds[wave][i][s][lane] = q[i][s];
+            for (int s = 0; s < kSteps; ++s) q_lds[copy][i][s][lane] = q[i][s];
     }
     const auto q_of = [&](int i, int s) {
-        if constexpr (kQInLds) return q_lds[wave][i][s][lane];
+        if constexpr (kQInLds) return q_lds[copy][i][s][lane];
         return q[i][s];
     };
 
@@ -668,7 +673,7 @@ __global__ __launch_bounds__(kWavesOf<WS> * 64, DIM <= 128 ? 2 : 1) void kv_atte
         for (int tt = 0; tt < 4; ++tt)
 #pragma unroll
             for (int h = 0; h < DIM / 64; ++h)
-                to.k[tt][h] = load_once<(WS > 1)>(kp + 4 * tt * DIM + 64 * h);
+                to.k[tt][h] = load_once<(WS > 1 && !SHARED)>(kp + 4 * tt * DIM + 64 * h);
     };
     auto load_v = [&](int it, const Where& w, Bytes& to) {
         const int vb = 4 * span.chunk(it) + g;
@@ -678,7 +683,7 @@ __global__ __launch_bounds__(kWavesOf<WS> * 64, DIM <= 128 ? 2 : 1) void kv_atte
         to.vscale = c.v_scale[vi];
         const uint8_t* vp = c.v + vi * (kBlock * DIM) + n * kBlock;
 #pragma unroll
-        for (int u = 0; u < kTiles; ++u) to.v[u] = load_once<(WS > 1)>(vp + 16 * u * kBlock);
+        for (int u = 0; u < kTiles; ++u) to.v[u] = load_once<(WS > 1 && !SHARED)>(vp + 16 * u * kBlock);
     };
 
     int it = begin + (WS == 1 ? 0 : wave);
@@ -912,6 +917,84 @@ __global__ __launch_bounds__(kWavesOf<WS> * 64, DIM <= 128 ? 2 : 1) void kv_atte
         for (int u = 0; u < kTiles; ++u)
             *reinterpret_cast<f32x4*>(out.rows + (int64_t)r * DIM + 16 * u + 4 * g) = o[i][u] * result[i];
     }
+}
+
+template <class T, class F, int DIM, int RT, int WS>
+__global__ __launch_bounds__(kWavesOf<WS> * 64, DIM <= 128 ? 2 : 1) void kv_attend_kernel(Attend p, int64_t places) {
+    attend_part<T, F, DIM, RT, WS, false>(p, places, blockIdx.x);
+}
+
+// The rows of all sequences over their shared tokens in the first workgroups, then
+// each sequence's rows over its own (own_places: 0 where another launch has these):
+// one launch, whose second part starts as the first runs out (4 sequences of up to
+// 100 tokens behind 2000: 19.3 us in two, 13.0 in one; 64 of up to 1000 behind 8192: 49
+// and 48.  In turns, the longer workgroups of the first part end late: 16 behind 65536
+// take 68 us instead of 55).
+template <class T, class F, int DIM, int RT>
+__global__ __launch_bounds__(kShareWaves * 64, DIM <= 128 ? 2 : 1) void kv_attend_shared_kernel(
+    Attend s, int64_t shared_places, Attend p, int64_t own_places) {
+    const int64_t shared_groups = shared_places * s.cache.heads * s.splits;
+    if (blockIdx.x < shared_groups)
+        attend_part<T, F, DIM, RT, kShareWaves, true>(s, shared_places, blockIdx.x);
+    else
+        attend_part<T, F, DIM, 1, kShareWaves, false>(p, own_places, blockIdx.x - shared_groups);
+}
+
+// Joins a row's few splits, its own and those of the shared tokens `s`, a
+// wavefront a row: a lane has a split's maximum and sum, then DIM / 64 values of the
+// row.  (With a workgroup to each row, prompts' many rows take three times as long.)
+constexpr int kFewSplits = 16;
+template <class T, int DIM, int R, int RW>
+__global__ __launch_bounds__(kShareWaves * 64) void kv_join_rows_kernel(Attend p, int64_t places, Attend s,
+                                                                        int64_t shared_places) {
+    constexpr int kPer = DIM / 64;
+    typedef float piece __attribute__((ext_vector_type(kPer)));
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const Cache& c = p.cache;
+    const int64_t place = blockIdx.x / c.heads;
+    const int head = (int)(blockIdx.x - place * c.heads);
+    Tile t;
+    const int r = (int)blockIdx.y * kShareWaves + wave;
+    if (!tile_of<R>(p, place, t) || r >= p.rows || t.r0 + r >= t.rows) return;
+    const int token = (t.r0 + r) / p.group;
+    const int in_group = t.r0 + r - token * p.group;
+    const int r0 = t.r0 + r / RW * RW, last = (r0 + RW < t.rows ? r0 + RW : t.rows) - 1;
+    const int chunks = span_of(p, t.first + r0 / p.group, t.first + last / p.group, t.len).count();
+    int splits = chunks > p.split_chunks ? (chunks + p.split_chunks - 1) / p.split_chunks : 1;
+    splits = splits < p.splits ? splits : p.splits;
+    const Partial in = partial_at<DIM>(p, places, (place * c.heads + head) * p.splits);
+    const int row = (t.start + token) * p.group + in_group, shared_r = row % s.rows;
+    const Partial also = partial_at<DIM>(s, shared_places, ((int64_t)(row / s.rows) * c.heads + head) * s.splits);
+    const int all = splits + s.splits;
+    const bool own = lane < splits;
+    const float* ml = own ? in.ml + (lane * p.rows + r) * 2 : also.ml + ((lane - splits) * s.rows + shared_r) * 2;
+    const float m = lane < all ? ml[0] : -__builtin_inff(), ls = lane < all ? ml[1] : 0.0f;
+    const float base = finite_base(wave_max(m));
+    const float l = ls == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(m - base) * ls;
+    const float sum = gemvdev::segment_sum<64>(l);
+    // (over the sum before they meet the rows: a result is within V's range, its
+    // multiple need not be; a split in which the row sees nothing adds nothing,
+    // whatever its row holds)
+    const float weight = ls == 0.0f ? -1.0f : l * (sum == 0.0f ? 0.0f : 1.0f / sum);
+    piece o = 0.0f;
+    for (int i = 0; i < all; i += 4) {  // four rows' loads in flight; those behind the last repeat it
+        piece x[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int n = i + k < all ? i + k : all - 1;
+            const float* from = n < splits ? in.rows + ((int64_t)n * p.rows + r) * DIM
+                                           : also.rows + ((int64_t)(n - splits) * s.rows + shared_r) * DIM;
+            x[k] = reinterpret_cast<const piece*>(from)[lane];
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float w = gemvdev::f32_of(__builtin_amdgcn_readlane(__builtin_bit_cast(uint32_t, weight), i + k));
+            if (i + k < all && w != -1.0f) o += x[k] * w;
+        }
+    }
+    uint16_t* dst = p.O + ((int64_t)t.start + token) * p.ldo + (int64_t)(head * p.group + in_group) * DIM + lane * kPer;
+#pragma unroll
+    for (int d = 0; d < kPer; ++d) dst[d] = fp8dev::narrow(T{}, o[d]);
 }
 
 // Joins the splits of a row, a workgroup a row (R: rows of a place, RW: of one

@@ -142,6 +142,14 @@ inline Mapping map_shared(int q_heads, int heads, int dim, int rows, int64_t chu
     m.places = ceil_div(all_rows, m.group_rows);
     m.place_rows = all_rows < m.group_rows ? (int)all_rows : m.group_rows;
     cut(m, heads, dim, chunks);
+    m.waves_share = 4;  // (one kernel takes them and the sequences' own tokens)
+    // Many rows fill the GPU by themselves, and every split costs a start and an end of
+    // its own, and a write and a read of all rows (3768 rows, 8 heads, over 4000 tokens:
+    // 158 us, and in two splits 177).
+    if (m.places * heads >= kSlots) {
+        m.splits = 1;
+        m.split_chunks = (int)chunks;
+    }
     return m;
 }
 
@@ -182,13 +190,19 @@ inline SharedMapping map_both(int q_heads, int heads, int dim, int rows, int seq
                               int64_t capacity, int window, int sinks, int shared) {
     SharedMapping s{};
     const int64_t there = shared < capacity ? shared : capacity;
-    if (sequences > 1 && dim <= 128) s.chunks = (int)(there / kChunk);
+    if (sequences > 1) s.chunks = (int)(there / kChunk);
     if (s.chunks > 0) s.shared = map_shared(q_heads, heads, dim, rows, s.chunks);
     s.own = map_attend(q_heads, heads, dim, rows, sequences, one_each, capacity, window, sinks, s.chunks);
+    if (s.chunks > 0 && s.own.waves_share == 8) s.own.waves_share = 4;  // (as the shared tokens' wavefronts)
     return s;
 }
+// Whether one launch takes both parts.
+constexpr bool together(const SharedMapping& s) { return s.own.waves_share == 4 && s.own.row_tiles == 1; }
 constexpr bool launchable(const SharedMapping& s, int heads) {
-    return launchable(s.own, heads) && (s.chunks == 0 || launchable(s.shared, heads));
+    return launchable(s.own, heads) &&
+           (s.chunks == 0 || (launchable(s.shared, heads) &&
+                              (s.own.places * s.own.splits + s.shared.places * s.shared.splits) * heads *
+                                      kShareWaves * 64 <= 0xffffffff));
 }
 inline size_t workspace_of(const SharedMapping& s, int heads, int dim) {
     return s.chunks == 0 ? workspace_of(s.own, heads, dim)
