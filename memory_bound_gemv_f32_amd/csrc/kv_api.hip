@@ -94,7 +94,8 @@ gemv_status_t join(const Mapping& m, Attend& p, Attend& s, int64_t shared_places
                      ? (const void*)&kvdev::kv_join_rows_kernel<T, DIM, 16 * kvdev::kOwnWaves * kTwo, 16 * kTwo>
                  : m.row_tiles == 2 ? (const void*)&kvdev::kv_join_rows_kernel<T, DIM, 16 * kTwo, 16 * kTwo>
                                     : (const void*)&kvdev::kv_join_rows_kernel<T, DIM, 16, 16>;
-            rows = (rows + kvdev::kShareWaves - 1) / kvdev::kShareWaves;
+            constexpr int kEach = kvdev::kShareWaves * kvdev::kJoinRows;  // rows of a workgroup
+            rows = (rows + kEach - 1) / kEach;
             return launch(fn, dim3((unsigned)(places * p.cache.heads), (unsigned)rows), kvdev::kShareWaves * 64, argv,
                           stream);
         }

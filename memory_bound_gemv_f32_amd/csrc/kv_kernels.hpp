@@ -940,10 +940,12 @@ __global__ __launch_bounds__(kShareWaves * 64, DIM <= 128 ? 2 : 1) void kv_atten
         attend_part<T, F, DIM, 1, kShareWaves, false>(p, own_places, blockIdx.x - shared_groups);
 }
 
-// Joins a row's few splits, its own and those of the shared tokens `s`, a
-// wavefront a row: a lane has a split's maximum and sum, then DIM / 64 values of the
-// row.  (With a workgroup to each row, prompts' many rows take three times as long.)
-constexpr int kFewSplits = 16;
+// Joins the few splits of rows, their own and those of the shared tokens `s`, a
+// wavefront for four neighbouring rows: sixteen lanes a row have a split's
+// maximum and sum each, then a lane has DIM / 64 values of each row, and the rows' loads
+// are in flight together.  (With a workgroup to each row, the 40096 rows of twelve prompts
+// took 120 us.)
+constexpr int kFewSplits = 16, kJoinRows = 4;
 template <class T, int DIM, int R, int RW>
 __global__ __launch_bounds__(kShareWaves * 64) void kv_join_rows_kernel(Attend p, int64_t places, Attend s,
                                                                         int64_t shared_places) {
@@ -954,47 +956,78 @@ __global__ __launch_bounds__(kShareWaves * 64) void kv_join_rows_kernel(Attend p
     const int64_t place = blockIdx.x / c.heads;
     const int head = (int)(blockIdx.x - place * c.heads);
     Tile t;
-    const int r = (int)blockIdx.y * kShareWaves + wave;
+    const int r = ((int)blockIdx.y * kShareWaves + wave) * kJoinRows;  // (all of one wavefront's RW rows)
     if (!tile_of<R>(p, place, t) || r >= p.rows || t.r0 + r >= t.rows) return;
-    const int token = (t.r0 + r) / p.group;
-    const int in_group = t.r0 + r - token * p.group;
+    int rows = t.rows - t.r0 - r;
+    rows = rows < p.rows - r ? rows : p.rows - r;
+    rows = rows < kJoinRows ? rows : kJoinRows;
     const int r0 = t.r0 + r / RW * RW, last = (r0 + RW < t.rows ? r0 + RW : t.rows) - 1;
     const int chunks = span_of(p, t.first + r0 / p.group, t.first + last / p.group, t.len).count();
     int splits = chunks > p.split_chunks ? (chunks + p.split_chunks - 1) / p.split_chunks : 1;
     splits = splits < p.splits ? splits : p.splits;
-    const Partial in = partial_at<DIM>(p, places, (place * c.heads + head) * p.splits);
-    const int row = (t.start + token) * p.group + in_group, shared_r = row % s.rows;
-    const Partial also = partial_at<DIM>(s, shared_places, ((int64_t)(row / s.rows) * c.heads + head) * s.splits);
     const int all = splits + s.splits;
-    const bool own = lane < splits;
-    const float* ml = own ? in.ml + (lane * p.rows + r) * 2 : also.ml + ((lane - splits) * s.rows + shared_r) * 2;
-    const float m = lane < all ? ml[0] : -__builtin_inff(), ls = lane < all ? ml[1] : 0.0f;
-    const float base = finite_base(wave_max(m));
-    const float l = ls == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(m - base) * ls;
-    const float sum = gemvdev::segment_sum<64>(l);
+    const Partial in = partial_at<DIM>(p, places, (place * c.heads + head) * p.splits);
+    // row j's place in the call, and among the rows over the shared tokens
+    const auto token_of = [&](int j) { return (t.r0 + r + j) / p.group; };
+    const auto shared_row = [&](int j) {
+        const int token = token_of(j);
+        return (t.start + token) * p.group + (t.r0 + r + j - token * p.group);
+    };
+    const auto shared_at = [&](int row) {
+        return partial_at<DIM>(s, shared_places, ((int64_t)(row / s.rows) * c.heads + head) * s.splits);
+    };
+    const int j = lane >> 4, i = lane & 15;
+    float m = -__builtin_inff(), ls = 0.0f;
+    if (j < rows && i < all) {
+        const int row = shared_row(j);
+        const float* ml = i < splits ? in.ml + (i * p.rows + r + j) * 2
+                                     : shared_at(row).ml + ((i - splits) * s.rows + row % s.rows) * 2;
+        m = ml[0];
+        ls = ml[1];
+    }
+    float top = m;
+    top = fmaxf(top, gemvdev::dpp<gemvdev::kDppSwapAdjacent>(top));
+    top = fmaxf(top, gemvdev::dpp<gemvdev::kDppSwapPairs>(top));
+    top = fmaxf(top, gemvdev::dpp<gemvdev::kDppHalfRowMirror>(top));
+    top = fmaxf(top, gemvdev::dpp<gemvdev::kDppRowMirror>(top));
+    const float l = ls == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(m - finite_base(top)) * ls;
+    const float sum = gemvdev::segment_sum<16>(l);
     // (over the sum before they meet the rows: a result is within V's range, its
     // multiple need not be; a split in which the row sees nothing adds nothing,
     // whatever its row holds)
     const float weight = ls == 0.0f ? -1.0f : l * (sum == 0.0f ? 0.0f : 1.0f / sum);
-    piece o = 0.0f;
-    for (int i = 0; i < all; i += 4) {  // four rows' loads in flight; those behind the last repeat it
-        piece x[4];
+    const float* own[kJoinRows];
+    const float* also[kJoinRows];
+    piece o[kJoinRows];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int n = i + k < all ? i + k : all - 1;
-            const float* from = n < splits ? in.rows + ((int64_t)n * p.rows + r) * DIM
-                                           : also.rows + ((int64_t)(n - splits) * s.rows + shared_r) * DIM;
-            x[k] = reinterpret_cast<const piece*>(from)[lane];
-        }
+    for (int k = 0; k < kJoinRows; ++k) {
+        const int n = k < rows ? k : rows - 1;  // (those that are not there repeat the last, and are not stored)
+        const int row = shared_row(n);
+        own[k] = in.rows + (int64_t)(r + n) * DIM + lane * kPer;
+        also[k] = shared_at(row).rows + (int64_t)(row % s.rows) * DIM + lane * kPer;
+        o[k] = 0.0f;
+    }
+    for (int n = 0; n < all; ++n) {
+        piece x[kJoinRows];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float w = gemvdev::f32_of(__builtin_amdgcn_readlane(__builtin_bit_cast(uint32_t, weight), i + k));
-            if (i + k < all && w != -1.0f) o += x[k] * w;
+        for (int k = 0; k < kJoinRows; ++k)
+            x[k] = *reinterpret_cast<const piece*>(n < splits ? own[k] + (int64_t)n * p.rows * DIM
+                                                              : also[k] + (int64_t)(n - splits) * s.rows * DIM);
+#pragma unroll
+        for (int k = 0; k < kJoinRows; ++k) {
+            const float w = gemvdev::f32_of(__builtin_amdgcn_readlane(__builtin_bit_cast(uint32_t, weight), 16 * k + n));
+            if (w != -1.0f) o[k] += x[k] * w;
         }
     }
-    uint16_t* dst = p.O + ((int64_t)t.start + token) * p.ldo + (int64_t)(head * p.group + in_group) * DIM + lane * kPer;
 #pragma unroll
-    for (int d = 0; d < kPer; ++d) dst[d] = fp8dev::narrow(T{}, o[d]);
+    for (int k = 0; k < kJoinRows; ++k) {
+        if (k >= rows) break;
+        const int token = token_of(k);
+        uint16_t* dst = p.O + ((int64_t)t.start + token) * p.ldo +
+                        (int64_t)(head * p.group + (t.r0 + r + k - token * p.group)) * DIM + lane * kPer;
+#pragma unroll
+        for (int d = 0; d < kPer; ++d) dst[d] = fp8dev::narrow(T{}, o[k][d]);
+    }
 }
 
 // Joins the splits of a row, a workgroup a row (R: rows of a place, RW: of one

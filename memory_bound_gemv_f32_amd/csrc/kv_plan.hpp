@@ -186,12 +186,31 @@ struct SharedMapping {
     int chunks;
     Mapping shared, own;
 };
+// Taken together the shared tokens cost a join, and save reading them for each
+// sequence: from 16 MiB a byte of each key and value and sequence on.  Measured, us
+// without and with, 8 heads of 128, single tokens: 4 sequences behind 2048 12.5 and
+// 12.7, behind 4096 16.8 and 13.0; 8 behind 1024 12.3 and 14.9, behind 2048 16.5 and 15.3;
+// 64 behind 256 13.3 and 16.9, behind 512 17.7 and 16.5; of 256, 4 behind 2048 23.2 and 15.0.
+// Prompts, whose rows fill the matrix cores by themselves, gain where the sequences
+// are many: 4 of up to 60 tokens behind 4096 51 and 57, 12 behind 1024 54 and 62, behind 4096
+// 169 and 118; 8 of up to 150 behind 4096 177 and 133.
+constexpr int64_t kWorthSharing = 1 << 24, kManySequences = 8, kManyTokens = 1 << 15;
+constexpr bool worth_sharing(int heads, int dim, int sequences, bool one_each, int64_t shared, int64_t rows_each) {
+    if (sequences < 2 || shared < kChunk) return false;
+    if (!one_each && sequences < kManySequences) return false;
+    if (rows_each > 32) return sequences * shared >= kManyTokens;
+    return sequences * shared >= kWorthSharing / ((int64_t)heads * dim);
+}
 inline SharedMapping map_both(int q_heads, int heads, int dim, int rows, int sequences, bool one_each,
                               int64_t capacity, int window, int sinks, int shared) {
     SharedMapping s{};
     const int64_t there = shared < capacity ? shared : capacity;
-    if (sequences > 1) s.chunks = (int)(there / kChunk);
-    if (s.chunks > 0) s.shared = map_shared(q_heads, heads, dim, rows, s.chunks);
+    const int64_t group = q_heads / heads;
+    const int64_t rows_each = one_each ? group : sequences > 0 ? ceil_div(rows * group, sequences) : 0;
+    if (worth_sharing(heads, dim, sequences, one_each, there, rows_each)) {
+        s.chunks = (int)(there / kChunk);
+        s.shared = map_shared(q_heads, heads, dim, rows, s.chunks);
+    }
     s.own = map_attend(q_heads, heads, dim, rows, sequences, one_each, capacity, window, sinks, s.chunks);
     if (s.chunks > 0 && s.own.waves_share == 8) s.own.waves_share = 4;  // (as the shared tokens' wavefronts)
     return s;

@@ -44,12 +44,33 @@ def shared_problem(lens, new, shared, page_size, heads, dim, form, seed=0, paddi
     return batch, cache
 
 
-def check(lens, new, shared, page_size=64, heads=2, group=4, dim=128, form=INT8, dtype=BF16, window=0, sinks=0, seed=0,
-          one_each=None, padding=0, scale=None):
+def taken_together(cache, q_heads, rows, sequences, width, one_each, shared, window=0, sinks=0):
+    """Whether the library takes the shared tokens for all rows together: then its
+    workspace is not the one without them, at one width of the table or another
+    (the two can be alike at one by chance)."""
+    def size(width, n):
+        return lg.kv_attend_workspace_size(cache, q_heads, rows, sequences, width, one_each=one_each, window=window,
+                                           sinks=sinks, shared=n)
+    return any(size(w, shared) != size(w, 0) for w in (width, width + 3, 2 * width, 8 * width))
+
+
+def enough_heads(sequences, shared, dim):
+    """Key/value heads with which sharing is worth while for single tokens."""
+    heads = 1
+    while sequences * shared * dim * heads < 1 << 24:
+        heads *= 2
+    return heads
+
+
+def check(lens, new, shared, page_size=64, heads=None, group=1, dim=128, form=INT8, dtype=BF16, window=0, sinks=0, seed=0,
+          one_each=None, padding=0, scale=None, together=True):
+    heads = enough_heads(len(lens), shared, dim) if heads is None else heads
     batch, cache = shared_problem(lens, new, shared, page_size, heads, dim, form, seed, padding)
     plain = PlainCache(cache)
     Q = values(seed + 7, batch.rows, heads * group, dim, dtype, 0.2)
     one_each = all(m == 1 for m in new) and not padding if one_each is None else one_each
+    assert together == taken_together(cache, heads * group, batch.rows, len(lens), batch.table.shape[1], one_each, shared,
+                                      window, sinks)
     tensors = batch.tensors(not one_each)
     out = torch.full_like(Q, 3.0)
     got = lg.gemv_kv_attend(Q, cache, *tensors, window=window, sinks=sinks, shared=shared, out=out, scale=scale)
@@ -66,97 +87,130 @@ def check(lens, new, shared, page_size=64, heads=2, group=4, dim=128, form=INT8,
 @pytest.mark.parametrize("dtype", [F16, BF16])
 @pytest.mark.parametrize("dim", [64, 128, 256])
 def test_one_token_each(dim, dtype, form):
-    for n, (lens, shared) in enumerate([([100, 90], 64), ([200, 150, 130], 127), ([700, 650, 641, 655], 640),
-                                        ([300] * 9, 256), ([1000, 400, 999], 330), ([65, 65], 65)]):
-        check(lens, [1] * len(lens), shared, [16, 32, 64, 128, 256][n % 5], 1 + n % 2, [1, 4, 5, 8, 3, 16][n], dim, form, dtype, seed=n)
+    """Every head size, type and page size; shared tokens that end inside a page, a
+    block and a chunk; row tiles of 16 and of 32 for the batch."""
+    for n, (lens, shared, group) in enumerate([([700, 650, 641, 655], 640, 1), ([600] * 9, 513, 1), ([1000, 990, 999, 1001], 983, 5),
+                                               ([513, 600, 513, 700, 520, 600], 512, 4), ([530] * 20, 527, 1)]):
+        check(lens, [1] * len(lens), shared, [16, 32, 64, 128, 256][n], group=group, dim=dim, form=form, dtype=dtype, seed=n)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("group", [17, 32, 40])
+def test_wide_groups(dim, group):
+    """Query heads of one key/value head that fill one row tile or several by
+    themselves: the own tokens go to other kernels."""
+    sequences = 64 if group > 32 else 8
+    check([540 + n % 7 for n in range(sequences)], [1] * sequences, 512, 64, group=group, dim=dim, form=E4M3, dtype=F16,
+          heads=2 if group > 32 else 16, together=sequences * 512 * dim * 16 >= 1 << 24 or group > 32)
 
 
 @pytest.mark.parametrize("dim", [64, 128, 256])
 @pytest.mark.parametrize("form", [INT8, E4M3])
-def test_prompts(dim, form):
-    for n, (lens, new, shared) in enumerate([([200, 150], [20, 3], 128), ([400, 390, 330, 385], [70, 1, 8, 64], 300),
-                                             ([150, 150, 150], [5, 0, 22], 100), ([300] * 6, [40] * 6, 256)]):
-        check(lens, new, shared, [32, 16, 64, 128][n], 2, [4, 2, 8, 1][n], dim, form, F16, seed=n)
+def test_few_new_tokens(dim, form):
+    for n, (new, group) in enumerate([([1, 3, 2, 1, 4, 1, 2, 5], 2), ([1, 0, 3, 1, 2, 2, 1, 0, 7], 4), ([2] * 12, 1)]):
+        lens = [600 + (5 * b) % 60 for b in range(len(new))]
+        check(lens, new, 580, [32, 16, 128][n], group=group, dim=dim, form=form, dtype=F16, seed=n)
 
 
-@pytest.mark.parametrize("rows", [2, 5, 9, 17, 33, 64, 70])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_prompts(dim):
+    """Prompts of many sequences, whose own rows fill their tiles."""
+    rng = np.random.default_rng(dim)
+    new = [int(x) for x in rng.integers(10, 40, 64)]
+    lens = [512 + m + int(x) for m, x in zip(new, rng.integers(0, 90, 64))]
+    check(lens, new, 512, 64, heads=1, group=2, dim=dim, form=E4M3, dtype=BF16)
+    check([4100 + 30 * b for b in range(9)], [30, 1, 9, 0, 40, 22, 30, 17, 40], 4096, 128, heads=2, group=2, dim=dim, form=INT8,
+          dtype=F16, window=[0, 1000, 4000][dim // 128], sinks=5)
+
+
+@pytest.mark.parametrize("rows", [4, 5, 9, 17, 33, 64, 70])
 def test_rows(rows):
     """Row tiles of every kind, full and not."""
     for group in (1, 4, 7):
-        check([260 + 7 * (i % 5) for i in range(rows)], [1] * rows, 256, 64, 1, group, 128, INT8, BF16, seed=rows)
+        check([560 + 7 * (i % 5) for i in range(rows)], [1] * rows, 512, 64, group=group, seed=rows)
 
 
 def test_long_shared():
-    """Several splits of the shared tokens and of the own ones."""
-    check([5000, 4500, 4100], [1, 1, 1], 4096, 128, 1, 4, 128, E4M3, BF16)
-    check([9000, 8300], [3, 1], 8192, 256, 1, 2, 64, INT8, F16)
-    check([4000, 3900, 3999, 3950], [30, 20, 10, 40], 3900, 16, 1, 2, 128, INT8, F16)
+    """Several splits of the shared tokens, few and many, and of the own ones."""
+    check([5000, 4500, 4100, 4200], [1, 1, 1, 1], 4096, 128, 8, 4, 128, E4M3, BF16)
+    check([9000, 8300], [1, 1], 8192, 256, 16, 2, 64, INT8, F16)
+    check([70000, 66000], [1, 1], 65536, 256, 2, 2, 64, INT8, F16)
+    check([14000, 33000, 33010, 33100], [1, 1, 1, 1], 13000, 64, 4, 2, 128, INT8, F16)
+    check([2600 + n for n in range(80)], [1] * 80, 2500, 16, 8, 8, 64, INT8, F16)
 
 
 def test_windows():
     """Windows that see all, a part or nothing of the shared tokens, with and
     without first tokens that stay visible."""
-    for n, (window, sinks) in enumerate([(16, 0), (16, 4), (64, 70), (200, 0), (300, 1), (10000, 4), (500, 1000), (1, 0)]):
-        for lens, new in (([400, 330, 500], [1, 1, 1]), ([400, 330, 500], [30, 20, 90])):
-            check(lens, new, 320, [16, 64][n % 2], 2, 3, 128, [INT8, E4M3][n % 2], BF16, window, sinks, seed=n)
+    for n, (window, sinks) in enumerate([(16, 0), (16, 4), (64, 70), (200, 0), (500, 1), (10000, 4), (700, 1000), (1, 0)]):
+        for lens, new in (([900, 830, 1000, 890], [1] * 4), ([900, 830, 1000, 890] * 2, [3, 2, 9, 1] * 2)):
+            check(lens, new, 820, [16, 64][n % 2], group=2, form=[INT8, E4M3][n % 2], window=window, sinks=sinks, seed=n)
 
 
 def test_rows_inside_the_shared_tokens():
     """Sequences that end within the shared tokens see their own part of them."""
-    check([300, 40, 1, 200], [1, 1, 1, 1], 256, 64)
-    check([300, 64, 70, 200, 256], [20, 64, 6, 150, 1], 256, 32)
-    check([0, 300, 280], [0, 4, 2], 256, 64)                # an empty first sequence, whose pages are there
-    check([0, 300, 280], [0, 4, 2], 256, 64, window=100, sinks=5)
+    check([600, 40, 1, 500], [1, 1, 1, 1], 512, 64)
+    check([600, 64, 70, 400, 512, 300, 514, 10], [4, 6, 1, 3, 1, 0, 2, 10], 512, 32)
+    check([0, 600, 580, 590, 600, 601, 602, 603], [0, 4, 2, 1, 1, 1, 1, 1], 512, 64)  # an empty first sequence, whose pages are there
+    check([0, 600, 580, 590, 600, 601, 602, 603], [0, 4, 2, 1, 1, 1, 1, 1], 512, 64, window=200, sinks=5)
 
 
 def test_padding_rows_stay():
-    check([300, 290], [4, 3], 256, 64, padding=9)
-    check([300, 290], [1, 1], 256, 64, padding=30)
+    check([600, 590] * 4, [4, 3] * 4, 512, 64, padding=9)
+    check([600, 590] * 4, [1, 1] * 4, 512, 64, padding=30)
 
 
 def test_negative_and_zero_scale():
-    check([300, 290, 270], [1, 1, 1], 256, 64, scale=-0.05)
-    check([300, 290, 270], [1, 1, 1], 256, 64, scale=0.0)
+    check([600, 590, 570, 580], [1, 1, 1, 1], 512, 64, scale=-0.05)
+    check([600, 590, 570, 580], [1, 1, 1, 1], 512, 64, scale=0.0)
+
+
+def test_too_little_to_share():
+    """Where little is shared, or nothing, the call is the one without it."""
+    for lens, new, shared in (([300, 290], [1, 1], 256), ([700], [1], 640), ([400, 330], [30, 7], 320), ([90] * 20, [1] * 20, 63)):
+        batch, cache, Q, tensors = check(lens, new, shared, heads=2, group=4, together=False)
+        assert torch.equal(lg.gemv_kv_attend(Q, cache, *tensors, shared=shared), lg.gemv_kv_attend(Q, cache, *tensors))
 
 
 def test_missing_pages():
     """Shared tokens whose page is not there are not seen."""
-    batch, cache = shared_problem([400, 390, 350], [1, 1, 1], 320, 32, 2, 128, INT8)
+    batch, cache = shared_problem([600, 590, 570, 599], [1] * 4, 512, 32, 64, 128, INT8)
+    assert taken_together(cache, 64, 4, 4, batch.table.shape[1], True, 512)
     for bad in (-1, batch.pages, 1 << 30):
         batch.table[:, 3] = bad
-        Q = values(1, 3, 8, 128, BF16)
-        got = lg.gemv_kv_attend(Q, cache, *batch.tensors(False), shared=320)
+        Q = values(1, 4, 64, 128, BF16)
+        got = lg.gemv_kv_attend(Q, cache, *batch.tensors(False), shared=512)
         assert_close(got, *attend(f64(Q), PlainCache(cache), batch, 128 ** -0.5, dtype=BF16))
 
 
 def test_more_shared_than_the_table_holds():
-    batch, cache = shared_problem([256, 256], [1, 1], 256, 64, 2, 128, INT8)
-    Q = values(1, 2, 8, 128, BF16)
+    batch, cache = shared_problem([512] * 4, [1] * 4, 512, 64, 64, 128, INT8)
+    Q = values(1, 4, 64, 128, BF16)
     got = lg.gemv_kv_attend(Q, cache, *batch.tensors(False), shared=1 << 30)
     assert_close(got, *attend(f64(Q), PlainCache(cache), batch, 128 ** -0.5, dtype=BF16))
 
 
 def test_hidden_blocks_that_are_not_finite():
     """A NaN scale reaches the rows that see its block, and no others."""
-    batch, cache = shared_problem([400, 150, 390], [1, 1, 1], 384, 64, 1, 128, E4M3)
-    page = int(batch.table[0, 3])
-    cache.k_scale[page, 0, 1] = float("nan")        # tokens 208 to 223
-    Q = values(2, 3, 4, 128, F16)
-    got = lg.gemv_kv_attend(Q, cache, *batch.tensors(False), shared=384)
-    assert torch.isnan(got[0]).all() and torch.isnan(got[2]).all()
+    batch, cache = shared_problem([800, 350, 790, 700], [1] * 4, 512, 64, 64, 128, E4M3)
+    page = int(batch.table[0, 6])
+    cache.k_scale[page, :, 1] = float("nan")        # tokens 400 to 415
+    Q = values(2, 4, 64, 128, F16)
+    got = lg.gemv_kv_attend(Q, cache, *batch.tensors(False), shared=512)
+    assert torch.isnan(got[0]).all() and torch.isnan(got[2:]).all()
     want, bound = attend(f64(Q), PlainCache(cache), batch, 128 ** -0.5, dtype=F16)
     assert_close(got[1], want[1], bound[1])
-    cache.k_scale[page, 0, 1] = 1.0
-    hidden = PlainCache(cache)  # (the window of 100 hides the block: its V scale has no part in the bound)
-    cache.v_scale[page, 0, 1] = float("inf")
-    got = lg.gemv_kv_attend(Q, cache, *batch.tensors(False), shared=384, window=100)
-    assert_close(got, *attend(f64(Q), hidden, batch, 128 ** -0.5, 100, 0, dtype=F16))
+    cache.k_scale[page, :, 1] = 1.0
+    hidden = PlainCache(cache)  # (the window of 200 hides the block: its V scale has no part in the bound)
+    cache.v_scale[page, :, 1] = float("inf")
+    got = lg.gemv_kv_attend(Q, cache, *batch.tensors(False), shared=512, window=200)
+    assert_close(got, *attend(f64(Q), hidden, batch, 128 ** -0.5, 200, 0, dtype=F16))
 
 
 def test_a_row_does_not_depend_on_the_others():
     """A row's bits are the same whatever the other rows hold, and from call to
     call."""
-    batch, cache, Q, tensors = check([700, 650, 660, 690], [1, 1, 1, 1], 640, heads=1)
+    batch, cache, Q, tensors = check([700, 650, 660, 690], [1, 1, 1, 1], 640)
     first = lg.gemv_kv_attend(Q, cache, *tensors, shared=640)
     assert torch.equal(first, lg.gemv_kv_attend(Q, cache, *tensors, shared=640))
     other = Q.clone()
@@ -167,26 +221,38 @@ def test_a_row_does_not_depend_on_the_others():
 
 
 def test_workspace_and_graph():
-    batch, cache, Q, tensors = check([700, 650, 660, 690], [1, 1, 1, 1], 640, heads=2)
-    width = batch.table.shape[1]
-    need = lg.kv_attend_workspace_size(cache, 8, 4, 4, width, shared=640)
-    assert need > 0
-    guard = torch.full((need + 256,), 77, dtype=torch.uint8, device="cuda")
+    for lens, new in (([700, 650, 660, 690], [1] * 4), ([700, 650, 660, 690] * 2, [3, 1, 2, 1] * 2)):
+        batch, cache, Q, tensors = check(lens, new, 640)
+        one_each, heads = tensors[2] is None, cache.heads
+        need = lg.kv_attend_workspace_size(cache, heads, batch.rows, len(lens), batch.table.shape[1], one_each=one_each, shared=640)
+        assert need > 0
+        guard = torch.full((need + 256,), 77, dtype=torch.uint8, device="cuda")
+        want = lg.gemv_kv_attend(Q, cache, *tensors, shared=640)
+        got = lg.gemv_kv_attend(Q, cache, *tensors, shared=640, workspace=guard[:need])
+        assert torch.equal(got, want) and (guard[need:] == 77).all()
+        with pytest.raises(lg.GemvError):
+            lg.gemv_kv_attend(Q, cache, *tensors, shared=640, workspace=guard[:need - 16])
+        out = torch.empty_like(Q)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            lg.gemv_kv_attend(Q, cache, *tensors, shared=640, out=out, workspace=guard[:need])
+        for n in range(3):
+            Q.copy_(values(n, batch.rows, heads, 128, BF16))
+            out.zero_()
+            guard.fill_(255)  # (nothing of an earlier call's, NaN as numbers)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, lg.gemv_kv_attend(Q, cache, *tensors, shared=640)), n
+
+
+def test_other_stream():
+    batch, cache, Q, tensors = check([700, 650, 660, 690], [1, 1, 1, 1], 640)
     want = lg.gemv_kv_attend(Q, cache, *tensors, shared=640)
-    got = lg.gemv_kv_attend(Q, cache, *tensors, shared=640, workspace=guard[:need])
-    assert torch.equal(got, want) and (guard[need:] == 77).all()
-    with pytest.raises(lg.GemvError):
-        lg.gemv_kv_attend(Q, cache, *tensors, shared=640, workspace=guard[:need - 16])
-    out = torch.empty_like(Q)
-    graph = torch.cuda.CUDAGraph()
-    with torch.cuda.graph(graph):
-        lg.gemv_kv_attend(Q, cache, *tensors, shared=640, out=out, workspace=guard[:need])
-    for n in range(3):
-        Q.copy_(values(n, 4, 8, 128, BF16))
-        out.zero_()
-        graph.replay()
-        torch.cuda.synchronize()
-        assert torch.equal(out, lg.gemv_kv_attend(Q, cache, *tensors, shared=640)), n
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    got = lg.gemv_kv_attend(Q, cache, *tensors, shared=640, stream=s)
+    s.synchronize()
+    assert torch.equal(got, want)
 
 
 def test_a_step_of_a_model():
@@ -194,19 +260,20 @@ def test_a_step_of_a_model():
     rotary positions, the append and the attention behind a shared prefix, against
     the same in 64 bits with the library's roundings between the operators."""
     from q4_helpers import product, rotary
-    heads, group, dim, hidden, page, prefix = 2, 4, 64, 256, 16, 200
+    heads, group, dim, hidden, page, prefix = 8, 2, 64, 256, 16, 4100
     g = torch.Generator().manual_seed(3)
     width = (heads * group + 2 * heads) * dim
     W = torch.randint(0, 256, (width, hidden // 2), generator=g, dtype=torch.uint8).cuda()
     scale = (torch.rand(width, hidden // 32, generator=g) * 0.01).cuda()
-    frequency, magnitude = lg.rotary_frequencies(dim, 10000.0, factor=2.0, original=128)
+    frequency, magnitude = lg.rotary_frequencies(dim, 10000.0, factor=2.0, original=2048)
     weight = [(1 + 0.1 * torch.randn(dim, generator=g)).cuda() for _ in range(2)]
-    lens, new = [prefix + 30, prefix + 9, prefix + 20], [1, 1, 1]
+    lens, new = [prefix + n for n in (30, 9, 20, 8, 30, 17, 1, 11)], [1] * 8
     for prompt in (False, True):
         if prompt:
-            new = [20, 1, 9]
+            new = [20, 1, 9, 3, 30, 2, 1, 4]
         batch, cache = shared_problem(lens, new, prefix, page, heads, dim, INT8, seed=4)
         table, seq_lens, starts = batch.tensors(prompt)
+        assert taken_together(cache, heads * group, batch.rows, 8, table.shape[1], not prompt, prefix)
         x = torch.randn(batch.rows, hidden, generator=g).cuda()
         qkv = lg.gemv_q4(W, scale, x, group=32)
         assert_close(qkv, *product(W, scale, x, None, None, 32, F32))
