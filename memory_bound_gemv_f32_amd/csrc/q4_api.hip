@@ -60,22 +60,42 @@ gemv_status_t tile(Product& p, int group, hipStream_t stream) {
     return launch(fn, grid, W * 64, lds, argv, stream);
 }
 
+template <class T, int RT, int NT, int W>
+gemv_status_t wide(Product& p, int group, hipStream_t stream) {
+    int row_tiles = (int)ceil_div(p.M, 16 * RT * W);
+    void* argv[] = {&p, &row_tiles};
+    const dim3 grid((unsigned)(row_tiles * ceil_div(p.T, 16 * NT)));
+    const int lds = 2 * 16 * NT * 256 + 16 * RT * W * 64;
+    const void* fn = group == 32   ? (const void*)&q4dev::q4_wide_kernel<T, 0, RT, NT, W>
+                     : group == 64 ? (const void*)&q4dev::q4_wide_kernel<T, 1, RT, NT, W>
+                                   : (const void*)&q4dev::q4_wide_kernel<T, 2, RT, NT, W>;
+    return launch(fn, grid, W * 64, lds, argv, stream);
+}
+
 // Which kernel.  Few vectors read W straight into registers, in as many rows to a
 // workgroup as leave two of them to a compute unit at most (X, which each
-// of them reads whole, is what wider row tiles save); past that the tiles, whose X goes
-// through LDS, the larger once it fills three quarters of the places for it.  Measured,
-// us at vectors x rows x K, bf16, groups of 128 (16 rows | 32 rows | 64 rows | tile of
-// 64 x 64 | 128 x 128):
-//   1 x 4096 x 4096        5.3 |  7.3 | 11.8
-//   1 x 14336 x 4096      13.0 | 11.3 | 13.0
-//   16 x 4096 x 4096       7.8 |  8.9 | 12.5
-//   16 x 14336 x 4096     21.7 | 15.2 | 13.5
-//   32 x 14336 x 4096          | 27.6 | 24.8 | 31.5
-//   64 x 4096 x 4096           | 15.9 | 13.3 | 32.2
-//   64 x 14336 x 4096          | 44.8 | 45.7 | 33.2
-//   256 x 4096 x 4096                         | 32.9 |  72.9
-//   512 x 14336 x 4096                        | 121.7 | 110.4
-//   1024 x 14336 x 4096                       | 236.5 | 213.3
+// of them reads whole, is what wider row tiles save: of more than 8 vectors they are wide as soon as
+// most units have one); past that the tiles, whose X goes
+// through LDS.  Measured, us at vectors x rows x K, bf16, groups of 128 (16 rows | 32
+// rows | 64 rows | tile of 64 x 64):
+//   1 x 4096 x 4096        5.7 |  7.2 | 11.6 | 29.8
+//   1 x 14336 x 4096      13.3 | 11.5 | 12.1
+//   8 x 14336 x 4096      17.4 | 12.9 | 12.6
+//   16 x 4096 x 4096       7.8 |  9.0 | 12.5 | 30.1
+//   16 x 14336 x 4096     22.5 | 15.4 | 13.0 | 30.2
+//   24 x 14336 x 4096          | 25.6 | 23.6 | 30.6
+//   64 x 14336 x 4096          | 47.2 | 45.9 | 32.1
+//   128 x 4096 x 4096          | 28.3 | 24.5 | 31.2
+//   256 x 4096 x 4096          | 52.9 | 45.7 | 31.4
+// and of tiles 64 x 64 | 128 x 128 through registers | 256 x 64 | 256 x 112 | 256 x
+// 128 straight into LDS, where every unit's first tile takes some 18 us, and each
+// 5.5 us for 16 vectors and 25 besides:
+//   512 x 4096 x 4096     42.5 |  86.9 |  60.1 |  81.0 |  88.5
+//   1024 x 4096 x 4096    82.1 |  92.7 |  66.4 |  84.3 |  90.1
+//   2000 x 4096 x 4096   163.2 | 113.7 | 102.7 | 126.4 |  95.9
+//   512 x 14336 x 4096   132.0 | 111.6 |  99.5 | 125.6 |  94.4
+//   1024 x 14336 x 4096  246.6 | 206.8 | 180.4 | 192.3 | 143.4
+//   2000 x 14336 x 4096  503.1 | 388.1 | 314.0 | 267.3 | 276.6
 constexpr int64_t kUnits = 256, kEnoughTiles = 384;
 constexpr int64_t kMostStaged = 150 * 1024;  // bytes of LDS for vectors
 constexpr int kMostOffset = 1 << 22;         // pitch with which a tile's rows are 32-bit offsets apart
@@ -94,16 +114,29 @@ gemv_status_t mapped(Product& p, int group, hipStream_t stream) {
     const int64_t tokens = ceil_div(p.T, 16);
     const bool far = p.ldq >= kMostOffset || p.lds >= kMostOffset || p.ldz >= kMostOffset || p.ldx >= kMostOffset;
     if (ceil_div(p.M, 16) * tokens <= kUnits) return few<T, 1, 1, 8, kParts ? 1 : 4, false>(p, group, stream);
-    if (ceil_div(p.M, 32) * tokens < 2 * kUnits) return few<T, 2, 1, 8, kParts ? 1 : 4, false>(p, group, stream);
-    if (far || ceil_div(p.M, 64) * tokens < 2 * kUnits) {
-        if (group == 32 || kParts) return few<T, 4, 1, 8, 1, false>(p, group, stream);  // (more would not fit the registers)
-        return few<T, 4, 1, 8, 4, false>(p, group, stream);
+    const bool wide_rows = !kParts && p.T > 8 && 4 * ceil_div(p.M, 64) * tokens >= 3 * kUnits;
+    if (!wide_rows && ceil_div(p.M, 32) * tokens < 2 * kUnits) return few<T, 2, 1, 8, kParts ? 1 : 4, false>(p, group, stream);
+    if (far || ceil_div(p.M, 64) * tokens <= 2 * kUnits) {
+        if constexpr (!kParts)
+            if (group != 32) return few<T, 4, 1, 8, 4, false>(p, group, stream);
+        return few<T, 4, 1, 8, 1, false>(p, group, stream);  // (more would not fit the registers)
     }
-    if (ceil_div(p.M, 128) * ceil_div(p.T, 128) < kEnoughTiles) return tile<T, 1, 4, 4>(p, group, stream);
-    if constexpr (kParts)
+    if constexpr (kParts) {
+        if (ceil_div(p.M, 128) * ceil_div(p.T, 128) < kEnoughTiles) return tile<T, 1, 4, 4>(p, group, stream);
         return tile<T, 3, 4, 4>(p, group, stream);
-    else
+    } else {
+        if (ceil_div(p.M, 64) * ceil_div(p.T, 64) <= 2 * kUnits) return tile<T, 1, 4, 4>(p, group, stream);
+        // (straight into LDS: whole chunks and aligned pieces)
+        if (p.K % q4dev::kChunk == 0 && aligned(p.Q, 16) && p.ldq % 16 == 0 && aligned(p.X, 16) && p.ldx % 8 == 0) {
+            // a compute unit's tiles, and what one of them takes
+            const auto cost = [&](int nt) { return ceil_div(ceil_div(p.M, 256) * ceil_div(p.T, 16 * nt), kUnits) * (2 * nt + 9); };
+            if (cost(8) <= cost(7) && cost(8) <= cost(4)) return wide<T, 4, 8, 4>(p, group, stream);
+            if (cost(7) <= cost(4)) return wide<T, 4, 7, 4>(p, group, stream);
+            return wide<T, 4, 4, 4>(p, group, stream);
+        }
+        if (ceil_div(p.M, 128) * ceil_div(p.T, 128) < kEnoughTiles) return tile<T, 1, 4, 4>(p, group, stream);
         return tile<T, 2, 8, 4>(p, group, stream);
+    }
 }
 
 template <class T>

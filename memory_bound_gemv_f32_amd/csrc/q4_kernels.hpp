@@ -9,6 +9,7 @@
 #pragma once
 
 #include "fp8_device.hpp"
+#include "fp8_kernels.hpp"
 
 namespace q4dev {
 
@@ -168,10 +169,15 @@ __device__ __forceinline__ Vec8<TF32> operand_of(TF32, quad lo, quad hi) {
 
 // A uniform address that the compiler keeps in scalar registers: loads add the lanes'
 // 32-bit offsets to it, where it would else keep a 64-bit address for each of them.
-__device__ __forceinline__ const uint8_t* scalar_here(const uint8_t* p) {
-    asm volatile("" : "+s"(p));
-    return p;
+// (It names global memory: loads from anywhere are counted as LDS's too, and every
+// wait for LDS would be one for them.)
+using global_bytes = const uint8_t __attribute__((address_space(1)))*;
+__device__ __forceinline__ global_bytes scalar_here(const uint8_t* p) {
+    global_bytes g = (global_bytes)p;
+    asm volatile("" : "+s"(g));
+    return g;
 }
+using global_quad = const quad_any __attribute__((address_space(1)))*;
 __device__ __forceinline__ uint32_t offset_here(uint32_t v) {
     asm volatile("" : "+v"(v));
     return v;
@@ -235,17 +241,16 @@ struct Narrow<2> {
     using type = uint16_t;
 };
 template <int N>
-__device__ __forceinline__ void load_words(const uint8_t* p, typename Narrow<N>::type (&v)[(N + 3) / 4]) {
+__device__ __forceinline__ void load_words(global_bytes p, typename Narrow<N>::type (&v)[(N + 3) / 4]) {
     if constexpr (N == 1) {
         v[0] = *p;
         return;
     }
-    struct __attribute__((packed, aligned(1))) Words {
-        typename Narrow<N>::type v[(N + 3) / 4];
-    };
-    const Words w = *reinterpret_cast<const Words*>(p);
+    typedef typename Narrow<N>::type Word;
+    typedef Word Words __attribute__((ext_vector_type((N + 3) / 4), aligned(1)));
+    const Words w = *(const Words __attribute__((address_space(1)))*)p;
 #pragma unroll
-    for (int i = 0; i < (N + 3) / 4; ++i) v[i] = w.v[i];
+    for (int i = 0; i < (N + 3) / 4; ++i) v[i] = w[i];
 }
 template <class T, int G, int U>
 struct RawScales {
@@ -277,8 +282,8 @@ __device__ __forceinline__ RawScales<T, G, U> load_scales(const Product& p, int6
     const uint8_t* z = p.zero + m * p.ldz + g0;
     R r;
     if (whole) {
-        load_words<R::N * T::bytes>(reinterpret_cast<const uint8_t*>(s), r.s);
-        load_words<R::N>(z, r.z);
+        load_words<R::N * T::bytes>((global_bytes)s, r.s);
+        load_words<R::N>((global_bytes)z, r.z);
         return r;
     }
 #pragma unroll
@@ -304,6 +309,16 @@ __device__ __forceinline__ RawScales<T, G, U> load_scales(const Product& p, int6
 template <class O>
 __device__ __forceinline__ void put(const Product& p, int64_t at, float v) {
     static_cast<typename O::storage*>(p.Y)[at] = fp8dev::narrow(O{}, v);
+}
+// f with the type of Y.
+template <class F>
+__device__ __forceinline__ void with_type(const Product& p, F f) {
+    if (p.y_type == 0)
+        f(TF32{});
+    else if (p.y_type == 1)
+        f(TF16{});
+    else
+        f(TBF16{});
 }
 __device__ __forceinline__ void store(const Product& p, int t, int m, float v) {
     const int64_t at = t * p.ldy + m;
@@ -579,21 +594,21 @@ __global__ __launch_bounds__(W * 64, 2) void q4_tile_kernel(Product p, int row_t
     quad next[RT];
     R then[RT];
     const auto fetch = [&](int c) {
-        const uint8_t* xc = scalar_here(x0 + (int64_t)c * (kChunk * T::bytes));
+        const global_bytes xc = scalar_here(x0 + (int64_t)c * (kChunk * T::bytes));
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
             const int t = first + i * (W * 4), last = p.T - 1 - t0;
             const uint32_t at = (uint32_t)(t < last ? t : last) * ((uint32_t)p.ldx * T::bytes) + piece * 8 * T::bytes;
 #pragma unroll
-            for (int h = 0; h < T::bytes / 2; ++h) ahead[i].v[h] = *reinterpret_cast<const quad_any*>(xc + offset_here(at + 16 * h));
+            for (int h = 0; h < T::bytes / 2; ++h) ahead[i].v[h] = *(global_quad)(xc + offset_here(at + 16 * h));
         }
         const int g0 = 4 * c >> G;
-        const uint8_t* qc = scalar_here(q0 + (int64_t)c * (kChunk / 2));
-        const uint8_t* sc = scalar_here(s0 + (int64_t)g0 * T::bytes);
-        const uint8_t* zc = scalar_here(z0 + g0);
+        const global_bytes qc = scalar_here(q0 + (int64_t)c * (kChunk / 2));
+        const global_bytes sc = scalar_here(s0 + (int64_t)g0 * T::bytes);
+        const global_bytes zc = scalar_here(z0 + g0);
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
-            next[i] = *reinterpret_cast<const quad_any*>(qc + offset_here(q_at[i]));
+            next[i] = *(global_quad)(qc + offset_here(q_at[i]));
             R raw;
             load_words<R::N * T::bytes>(sc + offset_here(s_at[i]), raw.s);
             load_words<R::N>(zc + offset_here(z_at[i]), raw.z);
@@ -722,19 +737,224 @@ __global__ __launch_bounds__(W * 64, 2) void q4_tile_kernel(Product p, int row_t
         }
         __syncthreads();
     }
+    with_type(p, [&](auto type) {
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            const int row = row0 + (wave * RT + i) * 16 + r;
+            if (row >= p.M) continue;
+            const float add = p.bias ? p.bias[row] : 0.0f;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int t = t0 + 16 * n + 4 * g + e;
+                    if (t < p.T) put<decltype(type)>(p, t * p.ldy + row, acc[i][n][e] + add);
+                }
+        }
+    });
+}
+
+// ---------------------------------------------------------------------------
+// very many vectors: X straight into LDS
+//
+// As above, but a wavefront takes 16·RT rows with RT = 4, so that what it reads of X
+// from LDS serves twice as many products, and X goes to LDS without passing
+// registers, which hold the sums (whole chunks and aligned pieces only).  X then lies
+// there in its own order, and the weights come out in that.
+//
+// With groups of 128 a chunk has one scale, and the order in which its columns are
+// taken is free: step j takes columns 32·g + 8·j .. +7 from the lanes' group g,
+// those that the lane has loaded.
+// ---------------------------------------------------------------------------
+
+// Eight columns in their order.  fp16: a value between zero bytes is q·2^-24, and
+// times 2^15 less zero·2^-9 all exact: the weights in units of 2^9, which the scale
+// takes (kUnit).
+template <class MT>
+constexpr float kUnit = 1.0f;
+template <>
+constexpr float kUnit<TF16> = 512.0f;
+__device__ __forceinline__ uint32_t ordered_offset_of(TF16, uint32_t zero) {
+    const _Float16 z = (_Float16)((float)zero * -0x1p-9f);
+    return __builtin_bit_cast(uint32_t, f16x2{z, z});
+}
+__device__ __forceinline__ float ordered_offset_of(TBF16, uint32_t zero) { return offset_of(TBF16{}, zero); }
+__device__ __forceinline__ quad ordered8(TF16, uint32_t w, uint32_t offset, uint32_t) {
+    const uint32_t even = w & 0x0f0f0f0fu, odd = w >> 4 & 0x0f0f0f0fu;
+    const f16x2 by{(_Float16)0x1p15f, (_Float16)0x1p15f};
+    quad v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t pair = __builtin_amdgcn_perm(odd, even, 0x0c040c00u + 0x00010001u * i);
+        v[i] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(__builtin_bit_cast(f16x2, pair), by,
+                                                                      __builtin_bit_cast(f16x2, offset)));
+    }
+    return v;
+}
+__device__ __forceinline__ quad ordered8(TBF16, uint32_t w, float offset, uint32_t exponent) {
+    uint32_t a[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t p = pair_of(w, i, exponent);
+        a[i] = __builtin_bit_cast(uint32_t, half_minus<0>(p, offset));
+        a[i + 4] = __builtin_bit_cast(uint32_t, half_minus<1>(p, offset));
+    }
+    quad v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __builtin_amdgcn_perm(a[2 * i + 1], a[2 * i], 0x07060302u);
+    return v;
+}
+
+template <class T, int G, int RT, int NT, int W>
+__global__ __launch_bounds__(W * 64, 2) void q4_wide_kernel(Product p, int row_tiles) {
+    using R = RawScales<T, G, 1>;
+    constexpr int BN = 16 * NT, BM = 16 * RT * W, kStage = BN * 256;
+    constexpr int kLoads = BN * 16 / (W * 64);  // of X, for each wavefront and chunk
+    static_assert(BN * 16 % (W * 64) == 0 && RT == 4, "whole loads, and a lane for each row of a wavefront");
+    extern __shared__ __align__(16) uint8_t lds[];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int r = lane & 15, g = lane >> 4;
+    const int tiles = gridDim.x, per = tiles / 8, id = blockIdx.x;
+    const int tile = id < per * 8 ? id % 8 * per + id / 8 : id;
+    const int token_tiles = tiles / row_tiles;
+    const int row0 = tile / token_tiles * BM, t0 = tile % token_tiles * BN;
+    const int chunks = p.K / kChunk;
+    const int64_t first_row = row0 + wave * RT * 16 < p.M ? row0 + wave * RT * 16 : p.M - 1;
+    const int left = p.M - 1 - (int)first_row;
+    const uint32_t own = lane < left ? lane : left;
+    const uint32_t s_at = own * (uint32_t)p.lds * T::bytes, z_at = own * (uint32_t)p.ldz;
+    const uint8_t* q0 = p.Q + first_row * p.ldq;
+    const uint8_t* s0 = static_cast<const uint8_t*>(p.scale) + first_row * p.lds * T::bytes;
+    const uint8_t* z0 = p.zero + first_row * p.ldz;
+    const uint8_t* x0 = static_cast<const uint8_t*>(p.X) + t0 * p.ldx * T::bytes;
+    // load i of a wavefront brings four vectors; a lane's slot is lane % 16, the piece
+    // there the slot ^ the vector's last four bits.  Of W it brings 16 rows of four
+    // pieces.
+    uint32_t x_at[kLoads], q_at[RT];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+        const int t = (i * W + wave) * 4 + g, last = p.T - 1 - t0;
+        x_at[i] = (uint32_t)(t < last ? t : last) * (uint32_t)(p.ldx * T::bytes) + 16 * (r ^ (t & 15));
+    }
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
-        const int row = row0 + (wave * RT + i) * 16 + r;
-        if (row >= p.M) continue;
-        const float add = p.bias ? p.bias[row] : 0.0f;
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int t = t0 + 16 * n + 4 * g + e;
-                if (t < p.T) store(p, t, row, acc[i][n][e] + add);
-            }
+        const int n = 16 * i + (lane >> 2);
+        q_at[i] = (uint32_t)(n < left ? n : left) * (uint32_t)p.ldq + 16 * ((lane ^ (lane >> 3)) & 3);
     }
+    const uint32_t lds_at = (uint32_t)(uintptr_t)lds;
+    const uint32_t own_rows = 2 * kStage + wave * (RT * 1024);
+    R then;
+    const auto fetch_x = [&](int c) {
+        const uint8_t* xc = x0 + (int64_t)c * (kChunk * T::bytes);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            fp8dev::lds_load16(xc, x_at[i], lds_at + (c & 1) * kStage + (i * W + wave) * 1024);
+    };
+    const auto fetch_w = [&](int c) {
+        const uint8_t* qc = q0 + (int64_t)c * (kChunk / 2);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) fp8dev::lds_load16(qc, q_at[i], lds_at + own_rows + i * 1024);
+        const int g0 = 4 * c >> G;
+        load_words<R::N * T::bytes>(scalar_here(s0 + (int64_t)g0 * T::bytes) + offset_here(s_at), then.s);
+        load_words<R::N>(scalar_here(z0 + g0) + offset_here(z_at), then.z);
+    };
+    f32x4 acc[RT][NT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) acc[i][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    fetch_x(0);
+    fetch_w(0);
+    const uint32_t exponent = exponent_of_1024();
+    constexpr int kSteps = G == 0 ? 1 : 2;
+    for (int c = 0; c < chunks; ++c) {
+        const uint8_t* stage = lds + (c & 1) * kStage;
+        fp8dev::wait_loads<0>();
+        quad w[RT];
+        R s[RT];
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            w[i] = *reinterpret_cast<const quad*>(lds + own_rows + i * 1024 + r * 64 + 16 * (g ^ (r >> 1 & 3)));
+            const int from = 4 * (16 * i + r);
+#pragma unroll
+            for (int e = 0; e < R::kWords; ++e) s[i].s[e] = __builtin_amdgcn_ds_bpermute(from, then.s[e]);
+#pragma unroll
+            for (int e = 0; e < R::kZeros; ++e) s[i].z[e] = __builtin_amdgcn_ds_bpermute(from, then.z[e]);
+        }
+        fp8dev::change_over();
+        if (c + 1 < chunks) fetch_x(c + 1);
+        stage += r * 256;
+        if constexpr (G < 2) {
+#pragma unroll
+            for (int i = 0; i < RT; ++i) w[i] = transposed(w[i]);
+        }
+#pragma unroll
+        for (int j0 = 0; j0 < 4; j0 += kSteps) {
+            __builtin_amdgcn_sched_barrier(0);
+            quad b[RT][kSteps];
+            float by[RT];
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+                by[i] = s[i].scale(j0) * kUnit<T>;
+                const auto offset = ordered_offset_of(T{}, s[i].zero(p, j0));
+#pragma unroll
+                for (int e = 0; e < kSteps; ++e) b[i][e] = ordered8(T{}, w[i][j0 + e], offset, exponent);
+            }
+            if (j0 == 0 && c + 1 < chunks) {  // (the rows are in registers)
+                __builtin_amdgcn_sched_barrier(0);
+                fp8dev::wait_lds();
+                fetch_w(c + 1);
+            }
+            quad v[2][kSteps];
+            f32x4 d[2][RT];
+            const auto read = [&](int n, quad (&to)[kSteps]) {
+#pragma unroll
+                for (int e = 0; e < kSteps; ++e) {
+                    const int piece = G == 2 ? 4 * g + j0 + e : 4 * (j0 + e) + g;
+                    to[e] = *reinterpret_cast<const quad*>(stage + n * 4096 + 16 * (piece ^ r));
+                }
+            };
+            read(0, v[0]);
+#pragma unroll
+            for (int n = 0; n <= NT; ++n) {
+                __builtin_amdgcn_sched_barrier(0);
+                if (n + 1 < NT) read(n + 1, v[(n + 1) & 1]);
+#pragma unroll
+                for (int i = 0; i < RT; ++i) {
+                    if (n > 0) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            acc[i][n - 1][e] = __builtin_fmaf(d[(n - 1) & 1][i][e], by[i], acc[i][n - 1][e]);
+                        asm volatile("" : "+v"(acc[i][n - 1]));
+                    }
+                    if (n < NT) {
+                        d[n & 1][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                        for (int e = 0; e < kSteps; ++e)
+                            d[n & 1][i] = gemvdev::mma_16x16x32(T{}, v[n & 1][e], b[i][e], d[n & 1][i]);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    fp8dev::wait_loads<0>();
+    with_type(p, [&](auto type) {
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            const int row = row0 + (wave * RT + i) * 16 + r;
+            if (row >= p.M) continue;
+            const float add = p.bias ? p.bias[row] : 0.0f;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int t = t0 + 16 * n + 4 * g + e;
+                    if (t < p.T) put<decltype(type)>(p, t * p.ldy + row, acc[i][n][e] + add);
+                }
+        }
+    });
 }
 
 }  // namespace q4dev

@@ -64,6 +64,17 @@ def test_many_vectors(dtype):
         check(M, K, nvec, (32, 64, 128)[n % 3], dtype, out_dtype=(dtype, F32)[n % 2], zero=n % 2 == 0, bias=n % 2 == 0, seed=n)
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_very_many_vectors(dtype, group):
+    """Tiles of 256 rows, of 64, 112 and 128 vectors, the last ones not full; the
+    same rows and vectors where they are not aligned, or the last columns no chunk."""
+    for n, (M, K, nvec, kw) in enumerate([(2100, 256, 1100, {}), (4090, 384, 1101, {}), (8000, 128, 1000, {}),
+                                          (2100, 256, 1100, dict(pad=1, shift=3)), (2100, 300, 1100, {}),
+                                          (2100, 256, 1100, dict(pad=16, shift=16))]):
+        check(M, K, nvec, group, dtype, out_dtype=(dtype, F32)[n % 2], zero=n % 2 == 0, bias=n % 3 == 0, seed=n, **kw)
+
+
 @pytest.mark.parametrize("dtype", [F32, F16, BF16])
 def test_layouts(dtype):
     """Rows apart and unaligned, outputs that are columns of a wider matrix."""
