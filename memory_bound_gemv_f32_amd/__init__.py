@@ -742,8 +742,9 @@ def rotary_frequencies(dim: int, base: float = 10000.0, *, factor: float = 1.0, 
     are mixed linearly in i, and the magnitude is 1 + 0.1·ln(factor)."""
     import math
     torch = _torch()
-    if dim < 0 or dim % 2 or base <= 0 or not factor >= 1 or original < 0 or not 0 < slow < fast:
-        raise ValueError("dim must be even, base positive, factor at least 1 and 0 < slow < fast")
+    if dim < 0 or dim % 2 or base <= 0 or not factor >= 1 or original < 0 or not 0 < slow < fast \
+            or (original and base <= 1):
+        raise ValueError("dim must be even, base positive (above 1 with original), factor at least 1 and 0 < slow < fast")
     i = torch.arange(dim // 2, dtype=torch.float64)
     frequency = base ** (-2.0 * i / max(dim, 1))
     magnitude = 1.0

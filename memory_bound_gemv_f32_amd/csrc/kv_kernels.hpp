@@ -394,12 +394,13 @@ __device__ __forceinline__ quad load_once(const uint8_t* p) {
 __device__ __forceinline__ float finite_base(float m) { return m == -__builtin_inff() ? 0.0f : m; }
 // How far a row's largest score, as a power of two, may pass the base of its
 // exponents before that follows: prompts, whose vector ALUs are the bound, save
-// the rescaling (2160 tokens over up to 4096, 164 us against 175 with 0); single
+// the rescaling (2160 tokens over up to 4096, 164 us against 175 with 0; 942 over 4000
+// shared ones 166 and 175); single
 // tokens take the same time with 0 (1 x 131071 51.3 and 51.5), and the largest
 // weight is then 1, which fp16 holds exactly (4 with a window of 512, fp16
 // results: error 2.15e-4 against 2.21e-4, of which the result's rounding is 2.06e-4).
-template <int WS>
-constexpr float kSlack = WS == 1 ? 8.0f : 0.0f;
+template <int WS, bool SHARED>
+constexpr float kSlack = WS == 1 || SHARED ? 8.0f : 0.0f;
 // A row's unit in its largest term when it is set, and the largest term in that
 // unit that it is kept for (fp16 ends at 2^16; the factor of 4 is for terms past
 // 2^127, which a caller's scales can make).
@@ -768,7 +769,7 @@ __device__ __forceinline__ void attend_part(const Attend& p, int64_t places, int
                 // has grown past it by kSlack: then most chunks leave it, and o and
                 // l with it, as they are, and no weight passes 2^kSlack
                 const float most = max_of_groups(top);
-                const bool higher = most > m[i] + kSlack<WS>;
+                const bool higher = most > m[i] + kSlack<WS, SHARED>;
                 const float to = higher ? most : m[i];
                 const float base = finite_base(to);
                 // the largest term of the lane's block (a scale that is not finite
@@ -930,6 +931,13 @@ __global__ __launch_bounds__(kWavesOf<WS> * 64, DIM <= 128 ? 2 : 1) void kv_atte
 // 100 tokens behind 2000: 19.3 us in two, 13.0 in one; 64 of up to 1000 behind 8192: 49
 // and 48.  In turns, the longer workgroups of the first part end late: 16 behind 65536
 // take 68 us instead of 55).
+//
+// The shared part is bound by the vector ALUs and by what two wavefronts a SIMD leave
+// unhidden of the steps' latency: 942 tokens of 32 heads over 4000 151 us, 410 TFLOP/s, 64 % of the
+// cycles with a vector or matrix instruction; 64 and 16 single tokens, whose shared workgroups
+// have a few steps each, 43 and 50 us with their own tokens.  K brought straight to
+// LDS a chunk ahead, and Q in registers then, change nothing or cost 9 %; wavefronts with rows of their
+// own, which do not fit the registers with masks and without, likewise.
 template <class T, class F, int DIM, int RT>
 __global__ __launch_bounds__(kShareWaves * 64, DIM <= 128 ? 2 : 1) void kv_attend_shared_kernel(
     Attend s, int64_t shared_places, Attend p, int64_t own_places) {

@@ -395,6 +395,15 @@ __device__ __forceinline__ void multiply(const Product& p, f32x4 (&acc)[RT][NT],
 // STAGED (where the vectors fit): they are brought to LDS once for the workgroup, in
 // the order that the weights come out in; an fp32 vector as three, of its parts,
 // whose sums are added at the end.
+//
+// Bound by the memory's latency: nearly all of a wavefront's share is one batch, so
+// a call is a launch, a load and a join.  1 x 4096 x 4096 fp16 4.6 us (1.9 TB/s), 16
+// x 14336 x 4096 bf16 12.5 (2.5), fp32 1 x 4096 x 11008 with groups of 32 10.9 (2.7).
+// A lane's 16 bytes are in another row than its neighbours', which costs the first
+// cache four accesses for one; loaded one behind the other and passed on through LDS
+// they take a quarter of the accesses and the same time or more (16 x 14336: 13.8).
+// X of 16 vectors staged whole, as the fp32 parts are, leaves one workgroup to a compute
+// unit (19.7).
 template <class T, int G, int RT, int NT, int W, int U, bool STAGED>
 __global__ __launch_bounds__(W * 64) void q4_few_kernel(Product p) {
     using MT = typename Operand<T>::type;
@@ -550,6 +559,10 @@ __global__ __launch_bounds__(W * 64) void q4_few_kernel(Product p) {
 // LDS.  A vector's 256 bytes of a chunk are 16 slots; slot s holds piece
 // s ^ (vector % 16), so that 16 lanes that want the same piece of 16 neighbouring
 // vectors find it in 16 different slots.
+//
+// Bound by the vector ALUs (widening a weight for 128 vectors, and an fp32 multiply-add
+// for each sum and group), which the matrix cores wait for: 500 x 4096 x 4096, 64 x 64,
+// 42 us (390 TFLOP/s); 2000 x 14336 x 4096, 128 x 128, 388 (605).
 // ---------------------------------------------------------------------------
 template <class T, int G, int RT, int NT, int W>
 __global__ __launch_bounds__(W * 64, 2) void q4_tile_kernel(Product p, int row_tiles) {
@@ -758,9 +771,22 @@ __global__ __launch_bounds__(W * 64, 2) void q4_tile_kernel(Product p, int row_t
 // very many vectors: X straight into LDS
 //
 // As above, but a wavefront takes 16·RT rows with RT = 4, so that what it reads of X
-// from LDS serves twice as many products, and X goes to LDS without passing
+// from LDS serves twice as many products, and X and W go to LDS without passing
 // registers, which hold the sums (whole chunks and aligned pieces only).  X then lies
-// there in its own order, and the weights come out in that.
+// there in its own order, and the weights come out in that.  A row's scale and
+// zero are loaded by one lane and passed to the four that want them.
+//
+// Two workgroups of four wavefronts share a compute unit, each with its own
+// barriers: while one widens, the other multiplies (one workgroup of eight, whose
+// wavefronts all wait for the slowest at each chunk: 322 us and 319, with a third fewer
+// wavefront cycles spent waiting).  X's two stages and the one of W, which is in
+// registers before the next is brought, are 80 KiB, half of a unit's LDS.
+//
+// 2000 x 14336 x 4096, groups of 64: 284 us, 827 TFLOP/s (the library's product of
+// bf16 weights, with nothing to widen or scale: 202).  The vector ALUs issue 5.4 instructions
+// to a product (2.4 widen, 2 scale), 66 % of the issue slots and 41 % of the matrix
+// cores' cycles are taken, and the clock falls as either rises: 2.06 GHz here, 1.97 with 112
+// vectors to a tile, whose rounds come out even.
 //
 // With groups of 128 a chunk has one scale, and the order in which its columns are
 // taken is free: step j takes columns 32·g + 8·j .. +7 from the lanes' group g,

@@ -111,6 +111,7 @@ __global__ __launch_bounds__(kWaves * 64) void rotary_kernel(Rotary p) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, in = lane % L;
     const int row = (int)blockIdx.x * kWaves + wave;
     if (row >= p.batch.total) return;
+    if (p.batch.starts != nullptr && row >= kvdev::start_of(p.batch, p.batch.count)) return;  // padding, which is not read
     const int half = p.dim / 2;
     int slot[N];
 #pragma unroll
@@ -156,7 +157,7 @@ __global__ __launch_bounds__(kWaves * 64) void rotary_kernel(Rotary p) {
     else
         b = kvdev::sequence_of(p.batch, row, 1, 1, 0);
     const int start = kvdev::start_of(p.batch, b), stop = kvdev::start_of(p.batch, b + 1);
-    if (row < start || row >= stop) return;  // padding
+    if (row < start || row >= stop) return;
     const int position = p.batch.lens[b] - (stop - row);
     for (int i = lane; i < p.pairs; i += 64) {
         float s, c;
