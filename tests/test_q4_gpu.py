@@ -154,6 +154,45 @@ def test_not_finite(dtype):
         assert not np.isfinite(y[:, 7]).any()
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_large_tiles_at_their_edges(dtype, group):
+    """Very many vectors: whole numbers are exact with every zero; what is not finite
+    reaches its own results; the same bits on every call and when captured."""
+    M, K, nvec = 2100, 256, 1100
+    groups = K // group
+    g = torch.Generator().manual_seed(group)
+    Q = torch.randint(0, 256, (M, K // 2), generator=g, dtype=torch.uint8).cuda()
+    scale = torch.exp2(torch.randint(-2, 3, (M, groups), generator=g).float()).to(dtype).cuda()
+    z = torch.randint(0, 256, (M, groups), generator=g, dtype=torch.uint8).cuda()
+    X = torch.randint(-3, 4, (nvec, K), generator=g).to(dtype).cuda()
+    for zero in (None, z):
+        y = lg.gemv_q4(Q, scale, X, zero=zero, group=group)
+        assert np.array_equal(f64(y), product(Q, scale, X, None, zero, group, F32)[0]), zero is None
+    wide = torch.full((nvec, M + 20), 7.0, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lg.gemv_q4(Q, scale, X, None, wide[:, 9:M + 9], zero=z, group=group)
+    for n in range(3):
+        X.copy_(torch.randint(-3, 4, (nvec, K), generator=g).to(dtype))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(wide[:, 9:M + 9], lg.gemv_q4(Q, scale, X, zero=z, group=group)), n
+    assert (wide[:, :9] == 7).all() and (wide[:, M + 9:] == 7).all()
+    Q[:, 35] = 0x99  # columns 70 and 71
+    z[:, 70 // group] = 3
+    X[1, 70], X[1098, 70] = float("inf"), float("nan")
+    scale[7, -1], scale[2099, 0] = float("inf"), float("nan")
+    y = f64(lg.gemv_q4(Q, scale, X, zero=z, group=group))
+    want = product(Q, scale, X, None, z, group, F32)[0]
+    plain = np.ones(y.shape, dtype=bool)
+    plain[1] = plain[1098] = plain[:, 7] = plain[:, 2099] = False
+    assert (y == want)[plain].all()
+    ordinary = [m for m in range(M) if m not in (7, 2099)]
+    assert np.isposinf(y[1, ordinary]).all() and np.isnan(y[1098]).all() and np.isnan(y[:, 2099]).all()
+    assert not np.isfinite(y[np.abs(want[:, 7]) != 0, 7]).any()
+
+
 def test_nan_with_low_bits_only():
     X = torch.zeros(1, 32)
     X.view(torch.int32)[0, 4] = 0x7f800001
