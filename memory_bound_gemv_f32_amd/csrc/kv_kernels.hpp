@@ -929,13 +929,13 @@ __global__ __launch_bounds__(kWavesOf<WS> * 64, DIM <= 128 ? 2 : 1) void kv_atte
 // each sequence's rows over its own (own_places: 0 where another launch has these):
 // one launch, whose second part starts as the first runs out (4 sequences of up to
 // 100 tokens behind 2000: 19.3 us in two, 13.0 in one; 64 of up to 1000 behind 8192: 49
-// and 48.  In turns, the longer workgroups of the first part end late: 16 behind 65536
+// and 48, the shared ones in 512 workgroups.  In turns, the longer workgroups of the first part end late: 16 behind 65536
 // take 68 us instead of 55).
 //
 // The shared part is bound by the vector ALUs and by what two wavefronts a SIMD leave
 // unhidden of the steps' latency: 942 tokens of 32 heads over 4000 151 us, 410 TFLOP/s, 64 % of the
 // cycles with a vector or matrix instruction; 64 and 16 single tokens, whose shared workgroups
-// have a few steps each, 43 and 50 us with their own tokens.  K brought straight to
+// have a few steps each, 37 and 50 us with their own tokens.  K brought straight to
 // LDS a chunk ahead, and Q in registers then, change nothing or cost 9 %; wavefronts with rows of their
 // own, which do not fit the registers with masks and without, likewise.
 template <class T, class F, int DIM, int RT>

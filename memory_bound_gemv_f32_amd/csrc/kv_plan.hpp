@@ -77,9 +77,10 @@ constexpr int64_t kOwnSlots = 1024, kLeastLongSplit = 4;
 constexpr int64_t kMostTiles = 0x7fffffff;
 constexpr int64_t kLeastSplit = 8, kOneRoundSplit = 32, kSplit = 12, kSlots = 512, kMostWorkgroups = 8192;
 
-
-// Cuts a mapping's chunks into splits.
-inline void cut(Mapping& m, int heads, int dim, int64_t chunks) {
+// Cuts a mapping's chunks into splits; where they fit `slots` in splits of at most
+// one_round, so.
+inline void cut(Mapping& m, int heads, int dim, int64_t chunks, int64_t slots = kSlots,
+                int64_t one_round = kOneRoundSplit) {
     if (m.places * heads > kMostTiles) {  // (launchable refuses it; the products below would overflow)
         m.splits = 1;
         m.split_chunks = (int)chunks;
@@ -90,8 +91,8 @@ inline void cut(Mapping& m, int heads, int dim, int64_t chunks) {
     // (a chunk of dim 256 takes long: 1 x 28767 tokens, one head, 23.6 us in splits of
     // 8 chunks, 19.5 of 4; 4 x 4000, 4 heads, 20.8 and 16.6)
     const int64_t least = own || dim > 128 ? kLeastLongSplit : kLeastSplit;
-    int64_t each = ceil_div(all, own ? kOwnSlots : kSlots);
-    each = !own && each > kOneRoundSplit ? kSplit : each < least ? least : each;
+    int64_t each = ceil_div(all, own ? kOwnSlots : slots);
+    each = !own && each > one_round ? kSplit : each < least ? least : each;
     if (each < ceil_div(all, kMostWorkgroups)) each = ceil_div(all, kMostWorkgroups);
     if (each < ceil_div(chunks, kMaxSplits)) each = ceil_div(chunks, kMaxSplits);
     // (a single split would save little)
@@ -132,8 +133,15 @@ inline Mapping map_attend(int q_heads, int heads, int dim, int rows, int sequenc
     return m;
 }
 
-// The rows of the whole batch over `chunks` chunks that all its sequences share.
-inline Mapping map_shared(int q_heads, int heads, int dim, int rows, int64_t chunks) {
+// The rows of the whole batch over `chunks` chunks that all its sequences share.  Their
+// splits are alike, and each leaves a partial result of all rows, so they are one
+// round of workgroups, however long (16384 tokens, 8 heads of 4 query heads, with own
+// tokens up to 1000, us with splits of 12 past 32 chunks and without: 96 sequences 110
+// and 86, 300 sequences 312 and 226).  many_own: the sequences' own tokens have a
+// workgroup for every other slot; then the shared ones leave them these, while their
+// splits stay at 32 chunks or less (64 sequences: 4096 tokens 44 and 42, 8192 48 and 40; 16384, of
+// 64 chunks, 64 and 77).
+inline Mapping map_shared(int q_heads, int heads, int dim, int rows, int64_t chunks, bool many_own) {
     Mapping m;
     const int64_t all_rows = (int64_t)rows * (q_heads / heads);
     m.waves_share = 4;
@@ -141,7 +149,8 @@ inline Mapping map_shared(int q_heads, int heads, int dim, int rows, int64_t chu
     m.group_rows = 16 * m.row_tiles;
     m.places = ceil_div(all_rows, m.group_rows);
     m.place_rows = all_rows < m.group_rows ? (int)all_rows : m.group_rows;
-    cut(m, heads, dim, chunks);
+    const bool half = many_own && m.places * heads <= kSlots / 2 * kOneRoundSplit / (chunks > 0 ? chunks : 1);
+    cut(m, heads, dim, chunks, half ? kSlots / 2 : kSlots, chunks);
     m.waves_share = 4;  // (one kernel takes them and the sequences' own tokens)
     // Many rows fill the GPU by themselves, and every split costs a start and an end of
     // its own, and a write and a read of all rows (3768 rows, 8 heads, over 4000 tokens:
@@ -209,10 +218,13 @@ inline SharedMapping map_both(int q_heads, int heads, int dim, int rows, int seq
     const int64_t rows_each = one_each ? group : sequences > 0 ? ceil_div(rows * group, sequences) : 0;
     if (worth_sharing(heads, dim, sequences, one_each, there, rows_each)) {
         s.chunks = (int)(there / kChunk);
-        s.shared = map_shared(q_heads, heads, dim, rows, s.chunks);
     }
     s.own = map_attend(q_heads, heads, dim, rows, sequences, one_each, capacity, window, sinks, s.chunks);
-    if (s.chunks > 0 && s.own.waves_share == 8) s.own.waves_share = 4;  // (as the shared tokens' wavefronts)
+    if (s.chunks > 0) {
+        if (s.own.waves_share == 8) s.own.waves_share = 4;  // (as the shared tokens' wavefronts)
+        const bool many_own = s.own.waves_share == 4 && s.own.places * heads * s.own.splits >= kSlots / 2;
+        s.shared = map_shared(q_heads, heads, dim, rows, s.chunks, many_own);
+    }
     return s;
 }
 // Whether one launch takes both parts.
