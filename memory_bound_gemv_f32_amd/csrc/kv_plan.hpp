@@ -227,11 +227,11 @@ inline SharedMapping map_both(int q_heads, int heads, int dim, int rows, int seq
     }
     return s;
 }
-// Whether one launch takes both parts.
+// Whether one launch takes both parts, and whether the launches hold them and their join.
 constexpr bool together(const SharedMapping& s) { return s.own.waves_share == 4 && s.own.row_tiles == 1; }
 constexpr bool launchable(const SharedMapping& s, int heads) {
     return launchable(s.own, heads) &&
-           (s.chunks == 0 || (launchable(s.shared, heads) &&
+           (s.chunks == 0 || (launchable(s.shared, heads) && s.own.places * heads * kShareWaves * 64 <= 0xffffffff &&
                               (s.own.places * s.own.splits + s.shared.places * s.shared.splits) * heads *
                                       kShareWaves * 64 <= 0xffffffff));
 }

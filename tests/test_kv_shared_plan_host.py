@@ -129,3 +129,17 @@ def test_sharing_where_it_pays(shim):
     assert chunks(4, 4096) == 64 and chunks(4, 4032) == 0
     assert chunks(64, 256) == 4 and chunks(1, 1 << 20) == 0 and chunks(300, 63) == 0
     assert chunks(4, 8192, 200) == 0 and chunks(12, 4000, 1000) == 62
+
+
+def test_no_launch_is_larger_than_the_runtime_takes(shim):
+    """Where the parts are launched the join is too: a thread of every tile's
+    workgroup is counted in 32 bits."""
+    for rows in (1000, 30000, 65500, 120000):
+        for dim in (64, 128, 256):
+            for heads in (8, 4096, 8192, 32768):
+                args = (heads, heads, dim, rows, rows // 33, 0, 1 << 20, 0, 0, 1 << 16)
+                chunks, prefix, own, _, launchable, *_ = mapping(shim, *args)
+                assert chunks > 0
+                if launchable:
+                    assert own["places"] * heads * 256 < 1 << 32, args
+                    assert prefix["places"] * heads * prefix["splits"] * 256 < 1 << 32, args
