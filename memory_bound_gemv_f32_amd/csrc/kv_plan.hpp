@@ -231,7 +231,7 @@ inline SharedMapping map_both(int q_heads, int heads, int dim, int rows, int seq
 constexpr bool together(const SharedMapping& s) { return s.own.waves_share == 4 && s.own.row_tiles == 1; }
 constexpr bool launchable(const SharedMapping& s, int heads) {
     return launchable(s.own, heads) &&
-           (s.chunks == 0 || (launchable(s.shared, heads) && s.own.places * heads * kShareWaves * 64 <= 0xffffffff &&
+           (s.chunks == 0 || (launchable(s.shared, heads) &&
                               (s.own.places * s.own.splits + s.shared.places * s.shared.splits) * heads *
                                       kShareWaves * 64 <= 0xffffffff));
 }
