@@ -202,13 +202,18 @@ struct SharedMapping {
 // 64 behind 256 13.3 and 16.9, behind 512 17.7 and 16.5; of 256, 4 behind 2048 23.2 and 15.0.
 // Prompts, whose rows fill the matrix cores by themselves, gain where the sequences
 // are many: 4 of up to 60 tokens behind 4096 51 and 57, 12 behind 1024 54 and 62, behind 4096
-// 169 and 118; 8 of up to 150 behind 4096 177 and 133.
-constexpr int64_t kWorthSharing = 1 << 24, kManySequences = 8, kManyTokens = 1 << 15;
-constexpr bool worth_sharing(int heads, int dim, int sequences, bool one_each, int64_t shared, int64_t rows_each) {
+// 169 and 118; 8 of up to 150 behind 4096 177 and 133.  Of shared tokens that a window
+// hides in part each sequence reads the rest only, and at another place: it takes eight
+// times as many of these (64 single tokens behind 4096, windows of 512 17 and 24, of 1024 22
+// and 26, of 2048 44 and 27; 64 prompts of up to 60, of 1024 108 and 143, of 2048 182 and
+// 186, of 4096 behind 16384 331 and 273).
+constexpr int64_t kWorthSharing = 1 << 24, kManySequences = 8, kManyTokens = 1 << 15, kHidden = 8;
+constexpr bool worth_sharing(int heads, int dim, int sequences, bool one_each, int64_t shared, int64_t seen,
+                             int64_t rows_each) {
     if (sequences < 2 || shared < kChunk) return false;
     if (!one_each && sequences < kManySequences) return false;
-    if (rows_each > 32) return sequences * shared >= kManyTokens;
-    return sequences * shared >= kWorthSharing / ((int64_t)heads * dim);
+    const int64_t tokens = seen < shared ? sequences * seen / kHidden : sequences * shared;
+    return tokens >= (rows_each > 32 ? kManyTokens : kWorthSharing / ((int64_t)heads * dim));
 }
 inline SharedMapping map_both(int q_heads, int heads, int dim, int rows, int sequences, bool one_each,
                               int64_t capacity, int window, int sinks, int shared) {
@@ -216,9 +221,8 @@ inline SharedMapping map_both(int q_heads, int heads, int dim, int rows, int seq
     const int64_t there = shared < capacity ? shared : capacity;
     const int64_t group = q_heads / heads;
     const int64_t rows_each = one_each ? group : sequences > 0 ? ceil_div(rows * group, sequences) : 0;
-    if (worth_sharing(heads, dim, sequences, one_each, there, rows_each)) {
-        s.chunks = (int)(there / kChunk);
-    }
+    const int64_t seen = window > 0 ? (int64_t)window + sinks : there;
+    if (worth_sharing(heads, dim, sequences, one_each, there, seen, rows_each)) s.chunks = (int)(there / kChunk);
     s.own = map_attend(q_heads, heads, dim, rows, sequences, one_each, capacity, window, sinks, s.chunks);
     if (s.chunks > 0) {
         if (s.own.waves_share == 8) s.own.waves_share = 4;  // (as the shared tokens' wavefronts)

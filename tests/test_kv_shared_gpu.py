@@ -120,7 +120,7 @@ def test_prompts(dim):
     lens = [512 + m + int(x) for m, x in zip(new, rng.integers(0, 90, 64))]
     check(lens, new, 512, 64, heads=1, group=2, dim=dim, form=E4M3, dtype=BF16)
     check([4100 + 30 * b for b in range(9)], [30, 1, 9, 0, 40, 22, 30, 17, 40], 4096, 128, heads=2, group=2, dim=dim, form=INT8,
-          dtype=F16, window=[0, 1000, 4000][dim // 128], sinks=5)
+          dtype=F16, window=[0, 1000, 4000][dim // 128], sinks=5, together=dim == 64)
 
 
 @pytest.mark.parametrize("rows", [4, 5, 9, 17, 33, 64, 70])
@@ -144,7 +144,22 @@ def test_windows():
     without first tokens that stay visible."""
     for n, (window, sinks) in enumerate([(16, 0), (16, 4), (64, 70), (200, 0), (500, 1), (10000, 4), (700, 1000), (1, 0)]):
         for lens, new in (([900, 830, 1000, 890], [1] * 4), ([900, 830, 1000, 890] * 2, [3, 2, 9, 1] * 2)):
-            check(lens, new, 820, [16, 64][n % 2], group=2, form=[INT8, E4M3][n % 2], window=window, sinks=sinks, seed=n)
+            check(lens, new, 820, [16, 64][n % 2], group=2, form=[INT8, E4M3][n % 2], window=window, sinks=sinks, seed=n,
+                  together=window + sinks >= 820)
+
+
+@pytest.mark.parametrize("new,window,sinks,form", [([1] * 16, 1100, 0, INT8), ([3, 2, 9, 1] * 4, 1024, 5, E4M3),
+                                                   ([3, 2, 9, 1] * 4, 1400, 70, INT8), ([1] * 16, 90, 1300, E4M3)])
+def test_windows_over_much(new, window, sinks, form):
+    """Windows that hide a part of many shared tokens, and leave enough of them to
+    take together; a first sequence shorter than the window."""
+    lens = [40 if max(new) == 1 else 1900, 1510, 1760, 1530, 1600, 1501, 2700, 1640] + [1900, 1510, 700, 1530] * 2
+    check(lens, new, 1500, 64, heads=64, form=form, window=window, sinks=sinks)
+
+
+def test_windows_of_prompts():
+    check([4510 + 7 * b for b in range(64)], [b % 10 + 15 for b in range(64)], 4500, 64, heads=1, group=2, dim=64, form=E4M3,
+          window=4200, sinks=5)
 
 
 def test_rows_inside_the_shared_tokens():
@@ -152,7 +167,7 @@ def test_rows_inside_the_shared_tokens():
     check([600, 40, 1, 500], [1, 1, 1, 1], 512, 64)
     check([600, 64, 70, 400, 512, 300, 514, 10], [4, 6, 1, 3, 1, 0, 2, 10], 512, 32)
     check([0, 600, 580, 590, 600, 601, 602, 603], [0, 4, 2, 1, 1, 1, 1, 1], 512, 64)  # an empty first sequence, whose pages are there
-    check([0, 600, 580, 590, 600, 601, 602, 603], [0, 4, 2, 1, 1, 1, 1, 1], 512, 64, window=200, sinks=5)
+    check([0, 600, 580, 590, 600, 601, 602, 603], [0, 4, 2, 1, 1, 1, 1, 1], 512, 64, window=200, sinks=5, together=False)
 
 
 def test_padding_rows_stay():

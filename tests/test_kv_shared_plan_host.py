@@ -123,12 +123,16 @@ def test_the_library_reports_the_same_workspace(shim):
 def test_sharing_where_it_pays(shim):
     """Single tokens from 16 MiB of keys over all sequences on, prompts of few
     sequences not."""
-    def chunks(sequences, shared, rows=None, heads=8, dim=128):
+    def chunks(sequences, shared, rows=None, heads=8, dim=128, window=0, sinks=0):
         rows = sequences if rows is None else rows
-        return mapping(shim, 4 * heads, heads, dim, rows, sequences, int(rows == sequences), shared + 1024, 0, 0, shared)[0]
+        return mapping(shim, 4 * heads, heads, dim, rows, sequences, int(rows == sequences), shared + 1024, window, sinks,
+                       shared)[0]
     assert chunks(4, 4096) == 64 and chunks(4, 4032) == 0
     assert chunks(64, 256) == 4 and chunks(1, 1 << 20) == 0 and chunks(300, 63) == 0
     assert chunks(4, 8192, 200) == 0 and chunks(12, 4000, 1000) == 62
+    # windows that hide a part
+    assert chunks(64, 4096, window=2048) == 64 and chunks(64, 4096, window=2047) == 0
+    assert chunks(64, 4096, window=2000, sinks=48) == 64 and chunks(4, 4096, window=5000) == 64
 
 
 def test_no_launch_is_larger_than_the_runtime_takes(shim):
