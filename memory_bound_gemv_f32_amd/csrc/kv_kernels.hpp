@@ -884,6 +884,17 @@ __device__ __forceinline__ void attend_part(const Attend& p, int64_t places, int
         if (wave != 0) return;
     }
 
+    // (a row without a position sees nothing, but min_pos is that of the rows that have
+    // one, and the chunks before it were taken without masks for all rows of the tile; the
+    // join leaves out what a sum of 0 stands beside)
+    if constexpr (SHARED) {
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            if (pos[i] >= 0) continue;
+            m[i] = -__builtin_inff();
+            l[i] = 0.0f;
+        }
+    }
     // (the unit over the sum before o meets either: the result is within V's
     // range, o in V's unit need not be)
     float result[RT];

@@ -170,6 +170,32 @@ def test_rows_inside_the_shared_tokens():
     check([0, 600, 580, 590, 600, 601, 602, 603], [0, 4, 2, 1, 1, 1, 1, 1], 512, 64, window=200, sinks=5, together=False)
 
 
+@pytest.mark.parametrize("form", [INT8, E4M3])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_rows_that_see_nothing(dim, form):
+    """Empty slots of a batch, the first among them, and rows in front of their
+    sequence's first token give exactly 0, beside rows that see every shared token;
+    row tiles of 16 and of 32, and prompts."""
+    for n, (lens, new, group) in enumerate([
+            ([600, 0, 590, 580], [1] * 4, 1), ([0, 600, 0, 590], [1] * 4, 5), ([0] * 3 + [600] * 17, [1] * 20, 2),
+            ([600, 3, 590, 0, 700, 650, 1, 680], [2, 5, 1, 2, 1, 3, 4, 1], 2),
+            ([0, 600, 590, 580, 570, 0, 700, 650], [1, 6, 1, 2, 1, 3, 4, 1], 4)]):
+        check(lens, new, 513 + n, [16, 32, 64, 128, 256][n], group=group, dim=dim, form=form, dtype=[F16, BF16][n % 2], seed=n)
+    lens, new = [540 + b for b in range(64)], [20 + b % 11 for b in range(64)]
+    for b in (0, 5, 6, 40):
+        lens[b] = b % 3
+    check(lens, new, 512, 64, heads=1, group=2, dim=dim, form=form, dtype=F16)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_scales_do_not_reach_rows_that_see_nothing(dim):
+    batch, cache = shared_problem([600, 0, 590, 580], [1] * 4, 512, 64, enough_heads(4, 512, dim), dim, E4M3)
+    cache.k_scale[int(batch.table[0, 2]), :, 1] = float("nan")
+    Q = values(5, 4, cache.heads, dim, BF16)
+    got = lg.gemv_kv_attend(Q, cache, *batch.tensors(False), shared=512)
+    assert (got[1] == 0).all() and torch.isnan(got[[0, 2, 3]]).all()
+
+
 def test_padding_rows_stay():
     check([600, 590] * 4, [4, 3] * 4, 512, 64, padding=9)
     check([600, 590] * 4, [1, 1] * 4, 512, 64, padding=30)
