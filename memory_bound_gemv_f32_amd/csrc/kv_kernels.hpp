@@ -580,6 +580,9 @@ __device__ __forceinline__ void attend_part(const Attend& p, int64_t places, int
         max_pos = __builtin_amdgcn_readfirstlane(wave_max_int(most));
         min_pos = 0x7ffffffe - __builtin_amdgcn_readfirstlane(wave_max_int(most_left));
         min_pos = max_pos < 0 ? -1 : min_pos;
+        // (what lies behind the last token that a row sees need not have been written: a
+        // byte there may be NaN, which no weight of 0 takes away)
+        t.len = max_pos + 1 < t.len ? max_pos + 1 : t.len;
     }
     const Span span = span_of(p, min_pos, max_pos, t.len);
     const int begin = p.splits == 1 ? 0 : split * p.split_chunks;

@@ -196,6 +196,31 @@ def test_scales_do_not_reach_rows_that_see_nothing(dim):
     assert (got[1] == 0).all() and torch.isnan(got[[0, 2, 3]]).all()
 
 
+@pytest.mark.parametrize("lens,new", [([601, 590, 570, 599], [1] * 4), ([0, 130, 100, 90], [1] * 4), ([17, 1, 0, 16], [1] * 4),
+                                      ([601, 590, 570, 599, 33, 40, 500, 0], [3, 2, 5, 1, 9, 4, 1, 0]), ([70 - b for b in range(20)], [1] * 20)])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_bytes_past_the_lengths(dim, lens, new):
+    """Sequences that all end within the shared tokens: what lies behind the longest
+    in its pages, NaN among it, does not matter."""
+    shared, longest = 640, max(lens)
+    batch, cache = shared_problem(lens, new, shared, 64, enough_heads(len(lens), shared, dim), dim, E4M3)
+    batch.table[:] = batch.table[0]
+    k, v = cache.k.view(torch.uint8), cache.v.view(torch.uint8)
+    for at in range(longest, shared):
+        page, i = int(batch.table[0, at // 64]), at % 64
+        k[page, :, i] = 0xff if at % 2 else 0x7f
+        v[page, :, i // 16, :, i % 16] = 0x7f if at % 3 else 0xff
+        if at % 16 == 0:  # (blocks that nothing was written to)
+            cache.k_scale[page, :, i // 16] = float("nan")
+            cache.v_scale[page, :, i // 16] = float("inf")
+    Q = values(3, batch.rows, cache.heads * 2, dim, F16)
+    one_each = max(new) == 1
+    assert taken_together(cache, cache.heads * 2, batch.rows, len(lens), batch.table.shape[1], one_each, 1 << 30)
+    for window in (0, 50):
+        got = lg.gemv_kv_attend(Q, cache, *batch.tensors(not one_each), window=window, shared=1 << 30)
+        assert_close(got, *attend(f64(Q), PlainCache(cache), batch, dim ** -0.5, window, dtype=F16))
+
+
 def test_padding_rows_stay():
     check([600, 590] * 4, [4, 3] * 4, 512, 64, padding=9)
     check([600, 590] * 4, [1, 1] * 4, 512, 64, padding=30)
