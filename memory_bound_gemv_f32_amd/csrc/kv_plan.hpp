@@ -207,11 +207,30 @@ struct SharedMapping {
 // times as many of these (64 single tokens behind 4096, windows of 512 17 and 24, of 1024 22
 // and 26, of 2048 44 and 27; 64 prompts of up to 60, of 1024 108 and 143, of 2048 182 and
 // 186, of 4096 behind 16384 331 and 273).
+//
+// Prompts that fill the GPU by themselves widen no less behind shared tokens (both ways
+// for each 32 rows), and lose a partial result of each row, written and read.  The plain call
+// takes a step for each 1024 of its workgroups or part of them, this one grows with the rows,
+// so they are taken together up to three quarters of the first step; behind many
+// tokens, where the join is little, always; and behind fewer where each prompt has at most
+// two workgroups' rows, which it seldom fills.  Measured, us without and with, e4m3, dim 128:
+// 16 prompts of 4 query heads, 600 | 700 | 800 | 1000 | 1150 | 1600 | 4200 workgroups, behind
+// 4096 200 and 148 | 193 and 168 | 190 and 191 | 190 and 222 | 185 and 246 | 352 and 361 | 827
+// and 964, behind 8192 385 and 240 | 363 and 278 | 363 and 321 | 364 and 374 | 362 and 423 | 672
+// and 618 | 1606 and 1646; 64 of 512 tokens behind 1024 1012 and 1763.  Of 34 | 48 | 63 | 98 |
+// 116 rows, 256 or 64 of them, behind 4096 465 and 285 | 470 and 371 | 595 and 501 | 298 and
+// 221 | 298 and 247, behind 1024 139 and 144 | 143 and 181 | 192 and 246.  (Of dim 256 the same
+// within a fifth either way.)
 constexpr int64_t kWorthSharing = 1 << 24, kManySequences = 8, kManyTokens = 1 << 15, kHidden = 8;
-constexpr bool worth_sharing(int heads, int dim, int sequences, bool one_each, int64_t shared, int64_t seen,
-                             int64_t rows_each) {
+constexpr int64_t kFewWorkgroups = kOwnSlots * 3 / 4, kLong = 4096, kVeryLong = 8192;
+// plain: the mapping of the call without shared tokens
+constexpr bool worth_sharing(const Mapping& plain, int heads, int dim, int sequences, bool one_each, int64_t shared,
+                             int64_t seen, int64_t rows_each) {
     if (sequences < 2 || shared < kChunk) return false;
     if (!one_each && sequences < kManySequences) return false;
+    if (plain.waves_share == 1 && plain.places * heads > kFewWorkgroups &&
+        shared < (rows_each > 2 * plain.group_rows ? kVeryLong : kLong))
+        return false;
     const int64_t tokens = seen < shared ? sequences * seen / kHidden : sequences * shared;
     return tokens >= (rows_each > 32 ? kManyTokens : kWorthSharing / ((int64_t)heads * dim));
 }
@@ -222,13 +241,13 @@ inline SharedMapping map_both(int q_heads, int heads, int dim, int rows, int seq
     const int64_t group = q_heads / heads;
     const int64_t rows_each = one_each ? group : sequences > 0 ? ceil_div(rows * group, sequences) : 0;
     const int64_t seen = window > 0 ? (int64_t)window + sinks : there;
-    if (worth_sharing(heads, dim, sequences, one_each, there, seen, rows_each)) s.chunks = (int)(there / kChunk);
+    s.own = map_attend(q_heads, heads, dim, rows, sequences, one_each, capacity, window, sinks);
+    if (!worth_sharing(s.own, heads, dim, sequences, one_each, there, seen, rows_each)) return s;
+    s.chunks = (int)(there / kChunk);
     s.own = map_attend(q_heads, heads, dim, rows, sequences, one_each, capacity, window, sinks, s.chunks);
-    if (s.chunks > 0) {
-        if (s.own.waves_share == 8) s.own.waves_share = 4;  // (as the shared tokens' wavefronts)
-        const bool many_own = s.own.waves_share == 4 && s.own.places * heads * s.own.splits >= kSlots / 2;
-        s.shared = map_shared(q_heads, heads, dim, rows, s.chunks, many_own);
-    }
+    if (s.own.waves_share == 8) s.own.waves_share = 4;  // (as the shared tokens' wavefronts)
+    const bool many_own = s.own.waves_share == 4 && s.own.places * heads * s.own.splits >= kSlots / 2;
+    s.shared = map_shared(q_heads, heads, dim, rows, s.chunks, many_own);
     return s;
 }
 // Whether one launch takes both parts, and whether the launches hold them and their join.

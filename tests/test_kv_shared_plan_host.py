@@ -135,6 +135,19 @@ def test_sharing_where_it_pays(shim):
     assert chunks(64, 4096, window=2000, sinks=48) == 64 and chunks(4, 4096, window=5000) == 64
 
 
+def test_prompts_that_fill_the_gpu_are_not_taken_together(shim):
+    """Behind few shared tokens they take longer together (measured beside the rule);
+    behind many, or with few rows each, they do not."""
+    def chunks(sequences, new, shared, group=4, heads=8, dim=128):
+        return mapping(shim, group * heads, heads, dim, sequences * new, sequences, 0, shared + new + 64, 0, 0, shared)[0]
+    for sequences, new, shared, group in ((16, 1000, 4096, 4), (64, 512, 1024, 1), (12, 150, 4096, 4), (64, 128, 4096, 4),
+                                          (256, 48, 1024, 1), (1000, 34, 512, 1), (16, 100, 2048, 4)):
+        assert chunks(sequences, new, shared, group) == 0, (sequences, new, shared, group)
+    for sequences, new, shared, group in ((12, 80, 4096, 4), (16, 1000, 16384, 4), (256, 48, 4096, 1), (64, 49, 4096, 2),
+                                          (16, 100, 2048, 1), (16, 256, 4096, 1)):
+        assert chunks(sequences, new, shared, group) == shared // 64, (sequences, new, shared, group)
+
+
 def test_no_launch_is_larger_than_the_runtime_takes(shim):
     """Where the parts are launched the join is too: a thread of every tile's
     workgroup is counted in 32 bits."""
