@@ -577,7 +577,8 @@ gemv_status_t gemv_kv_attend_bf16(const gemv_kv_cache_t *cache, const uint16_t *
  * same one or a copy: how many of the tokens are taken together is the
  * library's choice.)  shared == 0 computes what gemv_kv_attend_* does.  Other
  * arguments, results and errors are gemv_kv_attend_*'s, also for a negative
- * `shared`; the workspace has its own size. */
+ * `shared`; the workspace has its own size, at most 2^30 bytes or what
+ * gemv_kv_attend_* needs for the same sizes, whichever is more. */
 gemv_status_t gemv_kv_attend_shared_workspace_size(int q_heads, int heads, int dim,
                                                    int rows, int sequences,
                                                    int one_each, int table_width,

@@ -17,7 +17,7 @@ using kvdev::TF16;
 using kvdev::TF32;
 using kvplan::capacity_of;
 using kvplan::map_attend;
-using kvplan::map_both;
+using kvplan::map_call;
 using kvplan::Mapping;
 using kvplan::SharedMapping;
 using kvplan::workspace_of;
@@ -190,7 +190,7 @@ gemv_status_t attend(const gemv_kv_cache_t* cache, const uint16_t* Q, int ldq, u
     if (rows == 0 || p.batch.count == 0) return GEMV_SUCCESS;
     if (Q == nullptr || O == nullptr || !aligned(Q, 2) || !aligned(O, 2)) return GEMV_ERROR_INVALID_VALUE;
     const int64_t capacity = capacity_of(batch->table_width, cache->page_size);
-    const SharedMapping m = map_both(q_heads, p.cache.heads, cache->dim, rows, p.batch.count,
+    const SharedMapping m = map_call(q_heads, p.cache.heads, cache->dim, rows, p.batch.count,
                                      batch->starts == nullptr, capacity, window, sinks, shared);
     if (!kvplan::launchable(m, p.cache.heads)) return GEMV_ERROR_INVALID_VALUE;
     const size_t need = workspace_of(m, p.cache.heads, cache->dim);
@@ -227,7 +227,7 @@ extern "C" gemv_status_t gemv_kv_attend_shared_workspace_size(int q_heads, int h
         return GEMV_ERROR_INVALID_VALUE;
     size_t need = 0;
     if (rows > 0 && sequences > 0) {
-        const SharedMapping m = map_both(q_heads, heads, dim, rows, sequences, one_each != 0,
+        const SharedMapping m = map_call(q_heads, heads, dim, rows, sequences, one_each != 0,
                                          capacity_of(table_width, page_size), window, sinks, shared);
         if (!kvplan::launchable(m, heads)) return GEMV_ERROR_INVALID_VALUE;
         need = workspace_of(m, heads, dim);

@@ -262,5 +262,16 @@ inline size_t workspace_of(const SharedMapping& s, int heads, int dim) {
     return s.chunks == 0 ? workspace_of(s.own, heads, dim)
                          : partials_of(s.own, heads, dim) + partials_of(s.shared, heads, dim);
 }
+// The mapping of a call: shared tokens are taken together where that pays and fits.
+// Both parts leave partial results of all rows, where the plain call leaves those of few or
+// none, so theirs are 1 GiB at most (8192 single tokens of 32 query heads of 256 take half
+// of it); and what the plain call's launches hold is never refused.
+constexpr size_t kMostShared = (size_t)1 << 30;
+inline SharedMapping map_call(int q_heads, int heads, int dim, int rows, int sequences, bool one_each,
+                              int64_t capacity, int window, int sinks, int shared) {
+    const SharedMapping s = map_both(q_heads, heads, dim, rows, sequences, one_each, capacity, window, sinks, shared);
+    if (s.chunks == 0 || (launchable(s, heads) && workspace_of(s, heads, dim) <= kMostShared)) return s;
+    return map_both(q_heads, heads, dim, rows, sequences, one_each, capacity, window, sinks, 0);
+}
 
 }  // namespace kvplan

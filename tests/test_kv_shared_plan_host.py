@@ -148,6 +148,54 @@ def test_prompts_that_fill_the_gpu_are_not_taken_together(shim):
         assert chunks(sequences, new, shared, group) == shared // 64, (sequences, new, shared, group)
 
 
+def workspace(q_heads, heads, dim, rows, sequences, one_each, width, page, window, sinks, shared):
+    """Bytes of a call with and without shared tokens; None where it is refused."""
+    out = []
+    for n in (shared, 0):
+        size = ctypes.c_size_t()
+        status = lg.gemv_kv_attend_shared_workspace_size(q_heads, heads, dim, rows, sequences, one_each, width, page, window,
+                                                         sinks, n, ctypes.byref(size))
+        out.append(size.value if status == 0 else None)
+    return out
+
+
+def test_the_workspace_is_bounded():
+    """However many rows, heads and sequences there are: 1 GiB, or what the call needs
+    without shared tokens."""
+    for args in ((32, 8, 128, 64000, 32, 0, 1024, 64, 0, 0, 16384), (32, 8, 128, 128000, 64, 0, 300, 64, 0, 0, 16384),
+                 (1, 1, 64, 1 << 22, 1 << 17, 0, 2000, 64, 0, 0, 100000), (64, 1, 256, 1 << 18, 1 << 18, 1, 5000, 64, 0, 0, 300000),
+                 (128, 128, 256, 100000, 3000, 0, 5000, 64, 0, 0, 300000)):
+        with_shared, without = workspace(*args)
+        assert without is not None and with_shared <= max(1 << 30, without), args
+    rng = random.Random(6)
+    for _ in range(20000):
+        heads, group = rng.choice((1, 2, 8, 32, 128)), rng.choice((1, 2, 4, 8, 16, 40))
+        sequences = int(2 ** rng.uniform(1, 18))
+        rows = sequences * int(2 ** rng.uniform(0, 11))
+        if rows * heads * group >= 1 << 31:
+            continue
+        with_shared, without = workspace(heads * group, heads, rng.choice((64, 128, 256)), rows, sequences,
+                                         int(rows == sequences and rng.random() < 0.5), int(2 ** rng.uniform(0, 16)), 64,
+                                         rng.choice((0, 0, 5000)), 0, int(2 ** rng.uniform(6, 22)))
+        assert with_shared is None or with_shared <= max(1 << 30, without)
+        assert (with_shared is None) == (without is None)
+
+
+def test_no_call_is_refused_for_its_shared_tokens():
+    """Up to the sizes that the call takes without them."""
+    for dim in (64, 128, 256):
+        for log2 in (28, 29):
+            for sequences in (8, 1 << 16, 1 << 20):
+                for q_heads, heads in ((1, 1), (32, 8), (64, 64)):
+                    if sequences * heads > 1 << 22:
+                        continue
+                    rows = (1 << log2) // q_heads
+                    if rows < sequences:
+                        continue
+                    with_shared, without = workspace(q_heads, heads, dim, rows, sequences, 0, 1 << 20, 64, 0, 0, 1 << 20)
+                    assert with_shared is not None and without is not None, (dim, log2, sequences, q_heads, heads)
+
+
 def test_no_launch_is_larger_than_the_runtime_takes(shim):
     """Where the parts are launched the join is too: a thread of every tile's
     workgroup is counted in 32 bits."""
