@@ -739,7 +739,9 @@ def rotary_frequencies(dim: int, base: float = 10000.0, *, factor: float = 1.0, 
     without ``original`` every frequency is divided by it.  With the original
     context's length, a pair that turns more than ``fast`` times within it keeps its
     frequency, one that turns less than ``slow`` times is divided, those between
-    are mixed linearly in i, and the magnitude is 1 + 0.1·ln(factor)."""
+    are mixed linearly in i (from the i that turns ``fast`` times, rounded down, to
+    the one that turns ``slow`` times, rounded up, whether the head has those pairs
+    or not), and the magnitude is 1 + 0.1·ln(factor)."""
     import math
     torch = _torch()
     if dim < 0 or dim % 2 or base <= 0 or not factor >= 1 or original < 0 or not 0 < slow < fast \
@@ -752,8 +754,10 @@ def rotary_frequencies(dim: int, base: float = 10000.0, *, factor: float = 1.0, 
         # the i at which a pair turns so many times
         def place(turns):
             return dim / 2 * math.log(original / (2 * math.pi * turns)) / math.log(base)
-        low, high = max(math.floor(place(fast)), 0), min(math.ceil(place(slow)), dim // 2 - 1)
-        divided = torch.clamp((i - low) / max(high - low, 1e-3), 0.0, 1.0)
+        # (not cut to the head's pairs, where a long context's last ones still turn often:
+        # that would bend the line between)
+        low, high = math.floor(place(fast)), math.ceil(place(slow))
+        divided = torch.clamp((i - low) / max(high - low, 1), 0.0, 1.0)
         frequency = frequency * (1 - divided) + frequency / factor * divided
         magnitude = 1.0 + 0.1 * math.log(factor)
     elif factor > 1:
