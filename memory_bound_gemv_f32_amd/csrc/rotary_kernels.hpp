@@ -172,9 +172,9 @@ __global__ __launch_bounds__(kWaves * 64) void rotary_kernel(Rotary p) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const bool turned = slot[n] + i < p.pairs;
-            const f32x2 t = turns[wave][turned ? slot[n] + i : 0];
-            c[n][i] = turned ? t[0] : 1.0f;
-            s[n][i] = turned ? t[1] : 0.0f;
+            const f32x2 t = turns[wave][turned ? slot[n] + i : 0];  // (else unused)
+            c[n][i] = t[0];
+            s[n][i] = t[1];
         }
     // a part's weights stay in registers while its heads last
     float wu[N][V], wv[N][V];
@@ -225,8 +225,13 @@ __global__ __launch_bounds__(kWaves * 64) void rotary_kernel(Rotary p) {
             float lo[V], hi[V];
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                lo[i] = __builtin_fmaf(u[n][i], c[n][i], -(v[n][i] * s[n][i]));
-                hi[i] = __builtin_fmaf(v[n][i], c[n][i], u[n][i] * s[n][i]);
+                // (a pair that is not turned is kept, not multiplied by 1 and 0: an infinity
+                // or NaN would reach its neighbour)
+                const bool turned = slot[n] + i < p.pairs;
+                const float a = __builtin_fmaf(u[n][i], c[n][i], -(v[n][i] * s[n][i]));
+                const float b = __builtin_fmaf(v[n][i], c[n][i], u[n][i] * s[n][i]);
+                lo[i] = turned ? a : u[n][i];
+                hi[i] = turned ? b : v[n][i];
             }
             if (p.interleaved || slot[n] >= p.pairs) {
                 float y[2 * V];

@@ -129,6 +129,34 @@ def test_norm_edges():
     assert torch.isnan(y[3, 0]).any() and torch.isnan(y[4, 1]).all()
 
 
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dim,pairs", [(128, 32), (64, 8), (100, 30), (66, 0), (258, 100)])
+def test_values_that_are_not_rotated_stay(dim, pairs, interleaved, dtype):
+    """Behind the rotated ones every value is the input's own, whatever it and
+    its neighbours are: infinities, NaN, zeros of both signs."""
+    at = 2 * pairs
+    x = torch.randn(5, 3, dim, generator=torch.Generator().manual_seed(dim))
+    odd = torch.tensor([float("inf"), 0.0, 1.5, float("nan"), -0.0, -1.0, -float("inf"), -0.0, 0.0, -2.0])
+    for row in range(5):
+        for i, v in enumerate(odd.roll(row)):
+            x[row, :, at + (3 * i + row) % (dim - at)] = v
+    x = x.to(dtype).cuda()
+    lens = torch.tensor([9], dtype=torch.int32, device="cuda")
+    starts = torch.tensor([0, 5], dtype=torch.int32, device="cuda")
+    frequency = torch.rand(pairs, generator=torch.Generator().manual_seed(1)).cuda()
+    y, k = lg.gemv_rotary(x, x, frequency, lens, starts, interleaved=interleaved, magnitude=1.25, k_dtype=F32)
+    for out, same in ((y, x), (k, x.float())):
+        nan = torch.isnan(same[:, :, at:])
+        assert torch.equal(torch.isnan(out[:, :, at:]), nan)
+        kind = torch.int32 if out.dtype == F32 else torch.int16
+        bits = [t[:, :, at:].contiguous().view(kind)[~nan] for t in (out, same)]
+        assert torch.equal(*bits)
+    if pairs:
+        want, bound = rotary(x[:, :, :at], np.arange(4, 9), frequency, None, 1e-6, 1.25, interleaved, dtype)
+        assert_close(y[:, :, :at], want, bound)
+
+
 def test_frequencies():
     f, m = lg.rotary_frequencies(64, 10000.0)
     assert m == 1.0 and torch.equal(f.cpu(), (10000.0 ** (-torch.arange(32).double() / 32)).float())
