@@ -458,8 +458,8 @@ typedef struct {
  * overlap any part's x or y.  weight: dim fp32 values, or NULL: no norm.
  * dim is even and at most GEMV_ROTARY_MAX_DIM, pairs at most dim / 2;
  * frequency: `pairs` fp32 values (NULL where pairs is 0), finite.
- * The angle is worked out in 64 bits and keeps fp32's bits of its place in the
- * turn at every position; squares, products and sums are fp32, and a value is
+ * The angle is worked out in 64 bits and its place in the turn keeps more than fp32's
+ * bits at every position (of frequencies up to 2^70); squares, products and sums are fp32, and a value is
  * rounded to y_dtype once.  Rows from starts[sequences] on are neither read nor
  * written.
  * Errors: GEMV_ERROR_INVALID_VALUE for sizes that are not as above, another

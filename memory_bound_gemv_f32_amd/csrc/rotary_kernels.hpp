@@ -41,16 +41,40 @@ struct Rotary {
     int each;             // steps of a wavefront
 };
 
-// The angle of a position in half turns, in [-1, 1].  frequency/π and its
-// product with the position are each held as a sum of two 64-bit numbers (whole
-// turns may take 30 of a number's 53 bits), so at every position what is lost is the rounding
-// to fp32 at the end.
-__device__ __forceinline__ float half_turns(int position, float frequency) {
-    constexpr double kInvPi = 0.31830988618379067, kInvPiRest = -1.9678676675182486e-17;  // 1/π
+// The place of a position's angle in its turn, in half turns, in [-1, 1]: as an fp32
+// number, and in radians what that leaves out.  Whole turns of the frequency change nothing, as
+// positions are whole numbers, so they are taken out before the product with the position.
+// 1/π is a sum of three 64-bit numbers and every product keeps what it rounds off, so the
+// place has more than fp32's bits at every position, of frequencies up to 2^70.
+struct Place {
+    float at, rest;
+};
+// (Products that are taken apart below must be rounded, not passed on unrounded into a
+// multiply-add.)
+__device__ __forceinline__ double less_turns(double v) {
+#pragma clang fp contract(off)
+    return v - 2.0 * __builtin_rint(0.5 * v);
+}
+// a + b rounded, and what that rounds off.
+__device__ __forceinline__ double sum_of(double a, double b, double& off) {
+#pragma clang fp contract(off)
+    const double s = a + b, t = s - a;
+    off = (a - (s - t)) + (b - t);
+    return s;
+}
+__device__ __forceinline__ Place place_of(int position, float frequency) {
+#pragma clang fp contract(off)
+    constexpr double kInvPi = 0.31830988618379067, kSecond = -1.9678676675182486e-17, kThird = -1.0721436282893004e-33;
     const double f = frequency, n = position;
-    const double by = f * kInvPi, by_rest = __builtin_fma(f, kInvPi, -by) + f * kInvPiRest;
+    const double first = f * kInvPi, second = f * kSecond;
+    double off1, off2;
+    double by = sum_of(less_turns(first), less_turns(__builtin_fma(f, kInvPi, -first)), off1);
+    by = sum_of(by, less_turns(second), off2);
+    const double by_rest = off1 + off2 + (__builtin_fma(f, kSecond, -second) + f * kThird);
     const double a = n * by, a_rest = __builtin_fma(n, by, -a) + n * by_rest;
-    return (float)(a - 2.0 * __builtin_rint(0.5 * a) + a_rest);
+    const double place = less_turns(less_turns(a) + a_rest);
+    const float at = (float)place;
+    return Place{at, (float)(place - at) * 3.14159265f};
 }
 
 // N values of a type: as loaded, widened, and stored.
@@ -160,9 +184,12 @@ __global__ __launch_bounds__(kWaves * 64) void rotary_kernel(Rotary p) {
     if (row < start || row >= stop) return;
     const int position = p.batch.lens[b] - (stop - row);
     for (int i = lane; i < p.pairs; i += 64) {
+        const Place place = place_of(position, p.frequency[i]);
         float s, c;
-        sincospif(half_turns(position, p.frequency[i]), &s, &c);
-        turns[wave][i] = f32x2{c * p.magnitude, s * p.magnitude};
+        sincospif(place.at, &s, &c);
+        // (turned on by the little that is left: its square is below fp32's bits)
+        const float cosine = __builtin_fmaf(-s, place.rest, c), sine = __builtin_fmaf(c, place.rest, s);
+        turns[wave][i] = f32x2{cosine * p.magnitude, sine * p.magnitude};
     }
     // (a wavefront's own: its LDS accesses are in order)
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");

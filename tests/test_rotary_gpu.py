@@ -3,6 +3,8 @@ bits (needs a GPU)."""
 
 from __future__ import annotations
 
+from fractions import Fraction
+
 import numpy as np
 import pytest
 import torch
@@ -73,6 +75,29 @@ def test_far_positions():
     mantissas), a rounding of 64 bits' turns would not."""
     for lens in ([131071, 1 << 20], [1 << 24, (1 << 24) + 1], [(1 << 31) - 1, (1 << 30) + 12345]):
         check(lens, [3, 2], 4, 2, 64, F32, 32)
+
+
+PI = Fraction("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899862803482534211706798214808651")
+
+
+def test_large_frequencies():
+    """Frequencies far above 1, and positions up to an int's end: the angle keeps fp32's
+    bits of its place in the turn (against whole numbers, with 100 digits of pi)."""
+    pairs = 24
+    frequency = torch.tensor([1.7 ** (3 * i) * (1 + 0.01 * i) for i in range(pairs)])  # to 2^52
+    for length in (3, 1000, (1 << 20) + 7, (1 << 31) - 1):
+        x = torch.zeros(2, 1, 2 * pairs)
+        x[:, :, :pairs] = 1.0
+        y, _ = lg.gemv_rotary(x.cuda(), None, frequency.cuda(), torch.tensor([length], dtype=torch.int32, device="cuda"),
+                              torch.tensor([0, 2], dtype=torch.int32, device="cuda"))
+        for row in range(2):
+            for i in range(pairs):
+                turns = (length - 2 + row) * Fraction(float(frequency[i])) / (2 * PI)
+                place = 2 * np.pi * float(turns - round(turns))
+                # the angle's place rounded to fp32, a sine or cosine within two steps, two products and a sum
+                bound = (np.pi + 2 + 3) * 2.0 ** -24
+                got = [float(y[row, 0, i]), float(y[row, 0, i + pairs])]
+                assert abs(got[0] - np.cos(place)) <= bound and abs(got[1] - np.sin(place)) <= bound, (length, row, i)
 
 
 def test_batches():
