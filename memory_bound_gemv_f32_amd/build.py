@@ -23,7 +23,7 @@ SOURCES = [CSRC / "gemv_api.hip", CSRC / "fp8_api.hip", CSRC / "kv_api.hip", CSR
 HEADERS = [CSRC / "gemv_plan.hpp", CSRC / "gemv_device.hpp",
            CSRC / "gemv_kernels.hpp", CSRC / "gemv_launch.hpp",
            CSRC / "fp8_device.hpp", CSRC / "fp8_kernels.hpp",
-           CSRC / "kv_kernels.hpp", CSRC / "kv_plan.hpp", CSRC / "q4_kernels.hpp",
+           CSRC / "kv_kernels.hpp", CSRC / "kv_plan.hpp", CSRC / "q4_kernels.hpp", CSRC / "q4_plan.hpp",
            CSRC / "rotary_kernels.hpp", ROOT / "include" / "gemv.h"]
 LIBRARY = PACKAGE / "libgemv.so"
 ARCH = "gfx950"

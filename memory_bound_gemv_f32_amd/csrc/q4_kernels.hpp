@@ -10,6 +10,7 @@
 
 #include "fp8_device.hpp"
 #include "fp8_kernels.hpp"
+#include "q4_plan.hpp"
 
 namespace q4dev {
 
@@ -24,9 +25,8 @@ using fp8dev::TF32;
 using fp8dev::u32x2;
 using fp8dev::widen;
 
-constexpr int kChunk = 128;      // columns of a step: 16 bytes to a lane
-constexpr int kBlock = 32;       // columns of a matrix-core step
-constexpr int kNoZero = 8;       // the zero of weights without zeros
+using q4plan::kChunk;
+constexpr int kNoZero = 8;  // the zero of weights without zeros
 
 struct Product {
     const uint8_t* Q;
@@ -290,7 +290,7 @@ __device__ __forceinline__ RawScales<T, G, U> load_scales(const Product& p, int6
     for (int i = 0; i < R::kWords; ++i) r.s[i] = 0;
 #pragma unroll
     for (int i = 0; i < R::kZeros; ++i) r.z[i] = 0;
-    const int left = (((p.K + kBlock - 1) / kBlock + (1 << G) - 1) >> G) - g0;  // groups from g0 on
+    const int left = q4plan::groups_of(p.K, G) - g0;  // groups from g0 on
 #pragma unroll
     for (int i = 0; i < R::N; ++i) {
         const int at = i < left ? i : left - 1;  // (those behind repeat the last, and become 0)
@@ -459,7 +459,7 @@ __global__ __launch_bounds__(W * 64) void q4_few_kernel(Product p) {
     };
     // a vector's (or part's) line in LDS: whole chunks and 16 bytes, so that lines
     // start in other banks
-    const int pitch = chunks * kChunk * 2 + 16;
+    const int pitch = STAGED ? chunks * kChunk * 2 + 16 : 0;
     const uint8_t* line = lds + (r < PER * p.T ? r : PER * p.T - 1) * pitch + 16 * g;
     struct Parts {
         quad part[PARTS];

@@ -200,6 +200,31 @@ def test_nan_with_low_bits_only():
     assert torch.isnan(lg.gemv_q4(Q, torch.ones(16, 1, device="cuda"), X.cuda(), group=32)).all()
 
 
+@pytest.mark.parametrize("dtype,group", [(BF16, 128), (F16, 32), (F32, 64)])
+@pytest.mark.parametrize("K", [2 ** 31 - 1, 2 ** 31 - 128])
+def test_rows_up_to_an_int(K, dtype, group):
+    """The longest rows: all zero but for whole numbers at the start, the middle and the
+    end, so the result is exact."""
+    g = torch.Generator().manual_seed(K % 1000 + group)
+    M, groups = 2, -(-K // group)
+    Q = torch.zeros(M, -(-K // 2), dtype=torch.uint8, device="cuda")
+    scale = torch.ones(M, groups, dtype=dtype, device="cuda")
+    X = torch.zeros(1, K, dtype=dtype, device="cuda")
+    want = np.zeros((1, M))
+    for at in (0, 2 ** 30 - 50, (K - 201) // 2 * 2):
+        n = min(300, K - at)
+        codes = torch.randint(0, 256, (M, -(-n // 2)), generator=g, dtype=torch.uint8)
+        Q[:, at // 2:at // 2 + codes.shape[1]] = codes.cuda()
+        for part in range(at // group, min((at + n - 1) // group + 1, groups)):
+            scale[:, part] = 2.0 ** (part % 3)
+        x = torch.randint(-3, 4, (n,), generator=g)
+        X[0, at:at + n] = x.to(dtype).cuda()
+        q = f64(codes).astype(int)
+        w = np.stack((q & 15, q >> 4), 2).reshape(M, -1)[:, :n] - 8
+        want += ((w * 2.0 ** (((at + np.arange(n)) // group) % 3)) @ f64(x))[None]
+    assert np.array_equal(f64(lg.gemv_q4(Q, scale, X, group=group)), want)
+
+
 def test_empty():
     for M, K, nvec in ((0, 64, 3), (5, 64, 0), (5, 0, 3)):
         Q = torch.empty(M, K // 2, dtype=torch.uint8, device="cuda")
