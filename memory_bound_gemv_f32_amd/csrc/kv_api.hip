@@ -145,6 +145,7 @@ gemv_status_t attend(const SharedMapping& m, Attend& p, hipStream_t stream) {
         s.rows = m.shared.place_rows;
         s.capacity = m.chunks * kvplan::kChunk;
         s.shared = 0;
+        s.slack = m.own.waves_share == 1 ? kvdev::kPromptSlack : 0.0f;
         s.partial = p.partial + kvplan::partials_of(m.own, p.cache.heads, DIM) / sizeof(float);
         const gemv_status_t st = walk_shared<T, F, DIM>(m, s, p, stream);
         return st != GEMV_SUCCESS ? st : join<T, DIM, true>(m.own, p, s, m.shared.places, stream);
@@ -210,6 +211,7 @@ gemv_status_t attend(const gemv_kv_cache_t* cache, const uint16_t* Q, int ldq, u
     p.split_chunks = m.own.split_chunks;
     p.rows = m.own.place_rows;
     p.shared = m.chunks;
+    p.slack = 0.0f;
     p.partial = static_cast<float*>(workspace);
     return cache->format == GEMV_KV_E4M3 ? attend_dim<T, E4m3>(cache->dim, m, p, stream)
                                          : attend_dim<T, Int8>(cache->dim, m, p, stream);

@@ -392,15 +392,6 @@ __device__ __forceinline__ quad load_once(const uint8_t* p) {
 // A row that has seen nothing keeps its base at -inf; its exponents are taken
 // against 0.
 __device__ __forceinline__ float finite_base(float m) { return m == -__builtin_inff() ? 0.0f : m; }
-// How far a row's largest score, as a power of two, may pass the base of its
-// exponents before that follows: prompts, whose vector ALUs are the bound, save
-// the rescaling (2160 tokens over up to 4096, 164 us against 175 with 0; 942 over 4000
-// shared ones 166 and 175); single
-// tokens take the same time with 0 (1 x 131071 51.3 and 51.5), and the largest
-// weight is then 1, which fp16 holds exactly (4 with a window of 512, fp16
-// results: error 2.15e-4 against 2.21e-4, of which the result's rounding is 2.06e-4).
-template <int WS, bool SHARED>
-constexpr float kSlack = WS == 1 || SHARED ? 8.0f : 0.0f;
 // A row's unit in its largest term when it is set, and the largest term in that
 // unit that it is kept for (fp16 ends at 2^16; the factor of 4 is for terms past
 // 2^127, which a caller's scales can make).
@@ -445,7 +436,22 @@ struct Attend {
     float* partial;     // see partial_at
     int shared;         // chunks that the batch shares and another launch takes (0: none):
                         // then the results are partial ones, whatever the splits
+    float slack;        // of the rows over shared tokens, see slack_of
 };
+
+// How far a row's largest score, as a power of two, may pass the base of its
+// exponents before that follows: prompts, whose vector ALUs are the bound, save
+// the rescaling (2160 tokens over up to 4096, 164 us against 175 with 0; 942 over 4000
+// shared ones 166 and 175); single
+// tokens take the same time with 0 (1 x 131071 51.3 and 51.5), and the largest
+// weight is then 1, which fp16 holds exactly (4 with a window of 512, fp16
+// results: error 2.15e-4 against 2.21e-4, of which the result's rounding is 2.06e-4).
+// Shared tokens are weighed as the call without them would weigh them.
+constexpr float kPromptSlack = 8.0f;
+template <int WS, bool SHARED>
+__device__ __forceinline__ float slack_of(const Attend& p) {
+    return SHARED ? p.slack : WS == 1 ? kPromptSlack : 0.0f;
+}
 
 // What a row tile sees of the sequence's tokens.
 __device__ __forceinline__ Span span_of(const Attend& p, int min_pos, int max_pos, int len) {
@@ -769,10 +775,10 @@ __device__ __forceinline__ void attend_part(const Attend& p, int64_t places, int
                 // (a lane that sees nothing has top = -inf; ks = 0 would make that a NaN)
                 top = WHOLE || sees != 0 ? top * ks : -__builtin_inff();
                 // the base of the exponents follows the maximum only where that
-                // has grown past it by kSlack: then most chunks leave it, and o and
-                // l with it, as they are, and no weight passes 2^kSlack
+                // has grown past it by the slack: then most chunks leave it, and o and
+                // l with it, as they are, and no weight passes 2^slack
                 const float most = max_of_groups(top);
-                const bool higher = most > m[i] + kSlack<WS, SHARED>;
+                const bool higher = most > m[i] + slack_of<WS, SHARED>(p);
                 const float to = higher ? most : m[i];
                 const float base = finite_base(to);
                 // the largest term of the lane's block (a scale that is not finite

@@ -231,6 +231,36 @@ def test_negative_and_zero_scale():
     check([600, 590, 570, 580], [1, 1, 1, 1], 512, 64, scale=0.0)
 
 
+@pytest.mark.parametrize("dim,group", [(64, 1), (64, 8), (128, 3), (256, 1)])
+def test_the_largest_weight_of_single_tokens_is_whole(dim, group):
+    """Where one shared token has the largest score and the only value, a single
+    token's result is the formula's rounded once: its weight is 1 before the sum, not a
+    number of fp16's 11 bits.  (Scores are whole multiples of a power of two but for the
+    softmax scale's log2(e), 2^-24 of a score of 6 at most; the weight, the sum of some 4000
+    others and the quotient round by 2^-24 a few hundred times.)"""
+    shared, lens = 4096, [4100, 4200, 4130, 4097]
+    heads = enough_heads(4, shared, dim)
+    batch, cache = shared_problem(lens, [1] * 4, shared, 64, heads, dim, INT8)
+    for t in (cache.k, cache.v):
+        t.zero_()
+    for t in (cache.k_scale, cache.v_scale):
+        t.fill_(1.0)
+    value = torch.arange(dim, dtype=torch.int64) % 37 + 91
+    for head in range(heads):  # (behind others that a wavefront weighs before it)
+        at = 64 * (8 * (head % 8) + 4 + head % 4) + head % 64
+        page, i = int(batch.table[0, at // 64]), at % 64
+        cache.k[page, head, i, 0] = 1
+        cache.v[page, head, i // 16, :, i % 16] = value.to(torch.int8).cuda()
+    Q = torch.zeros(4, heads * group, dim, dtype=F16, device="cuda")
+    Q[:, :, 0] = (torch.rand(4, heads * group, generator=torch.Generator().manual_seed(dim)) * 40 + 4).to(F16).cuda()
+    assert taken_together(cache, heads * group, 4, 4, batch.table.shape[1], True, shared)
+    got = f64(lg.gemv_kv_attend(Q, cache, *batch.tensors(False), scale=0.125, shared=shared))
+    e = np.exp(f64(Q)[:, :, :1] * 0.125)
+    want = value.numpy() * e / (e + np.array(lens)[:, None, None] - 1)
+    half_step = 2.0 ** (np.floor(np.log2(want)) - 11)
+    assert (np.abs(got - want) <= half_step + 2.0 ** -16 * want).all()
+
+
 def test_too_little_to_share():
     """Where little is shared, or nothing, the call is the one without it."""
     for lens, new, shared in (([300, 290], [1, 1], 256), ([700], [1], 640), ([400, 330], [30, 7], 320), ([90] * 20, [1] * 20, 63)):
