@@ -200,7 +200,6 @@ __device__ __forceinline__ quad load_end(const uint8_t* row, int64_t at, int64_t
 
 // What a lane loads of a vector for one matrix-core step: columns k .. k+7;
 // those from K on read as zero and are not touched.  Rows are of 32 columns at least.
-constexpr int kLeastColumns = 32;
 template <class T>
 struct Raw8 {
     quad v[T::bytes / 2];

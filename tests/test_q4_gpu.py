@@ -9,6 +9,7 @@ import torch
 
 import memory_bound_gemv_f32_amd as lg
 from q4_helpers import assert_close, f64, product
+from q4_variants import CASES, FAR
 
 pytestmark = pytest.mark.gpu
 
@@ -73,6 +74,22 @@ def test_very_many_vectors(dtype, group):
                                           (2100, 256, 1100, dict(pad=1, shift=3)), (2100, 300, 1100, {}),
                                           (2100, 256, 1100, dict(pad=16, shift=16))]):
         check(M, K, nvec, group, dtype, out_dtype=(dtype, F32)[n % 2], zero=n % 2 == 0, bias=n % 3 == 0, seed=n, **kw)
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("case", range(len(CASES)))
+def test_every_kernel(case, group):
+    """Every kernel that the rule names, of every type and group, at ragged sizes."""
+    dtype, family, M, K, nvec, pad, shift = CASES[case]
+    Q, scale, X, b, z = problem(M, K, nvec, group, dtype, zero=case % 3 != 0, bias=case % 2 == 0, seed=case,
+                                pad=0 if pad >= FAR else pad, shift=shift)
+    if pad >= FAR:
+        wide = torch.zeros(nvec, pad, dtype=dtype, device="cuda")
+        wide[:, :K] = X
+        X = wide[:, :K]
+    out_dtype = (F32, F16, BF16)[(case + group // 32) % 3]
+    y = lg.gemv_q4(Q, scale, X, b, zero=z, group=group, out_dtype=out_dtype)
+    assert_close(y, *product(Q, scale, X, b, z, group, out_dtype), f"{CASES[case]} {group}")
 
 
 @pytest.mark.parametrize("dtype", [F32, F16, BF16])

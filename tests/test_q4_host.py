@@ -147,3 +147,9 @@ def test_kernels_use_no_scratch(kernels):
         waves = max(1, -(-int(f["max_flat_workgroup_size"]) // 256))
         assert int(f["vgpr_count"]) <= 512 // waves, name
         assert int(f["group_segment_fixed_size"]) <= 160 * 1024, name
+
+
+def test_every_family_is_built(kernels):
+    """... and so held to the limits above."""
+    for family in ("q4_short", "q4_few", "q4_tile", "q4_wide", "rotary"):
+        assert any(family in n for n in kernels), family
