@@ -187,6 +187,12 @@ def test_rows_that_see_nothing(dim, form):
     check(lens, new, 512, 64, heads=1, group=2, dim=dim, form=form, dtype=F16)
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_rows_that_see_nothing_behind_many_splits(dim):
+    """The same where a workgroup joins many partial results of a row."""
+    check([35000, 0, 33000, 0], [1] * 4, 32768, 256, 2, 2, dim, INT8, F16)
+
+
 @pytest.mark.parametrize("dim", [64, 128])
 def test_scales_do_not_reach_rows_that_see_nothing(dim):
     batch, cache = shared_problem([600, 0, 590, 580], [1] * 4, 512, 64, enough_heads(4, 512, dim), dim, E4M3)
@@ -277,6 +283,20 @@ def test_missing_pages():
         Q = values(1, 4, 64, 128, BF16)
         got = lg.gemv_kv_attend(Q, cache, *batch.tensors(False), shared=512)
         assert_close(got, *attend(f64(Q), PlainCache(cache), batch, 128 ** -0.5, dtype=BF16))
+
+
+def test_more_rows_than_partial_results_are_kept_of():
+    """Past 1 GiB of them the call is the one without shared tokens."""
+    sequences, heads, group, dim, shared = 33000, 2, 8, 256, 512
+    cache = filled(8 + sequences, heads, dim, 16, E4M3, 1)
+    table = torch.empty(sequences, 33, dtype=torch.int32)
+    table[:, :32] = torch.arange(32) % 8  # (pages may also be named twice)
+    table[:, 32] = torch.arange(sequences) + 8
+    table, lens = table.cuda(), (torch.arange(sequences, dtype=torch.int32) % 16 + 513).cuda()
+    size = [lg.kv_attend_workspace_size(cache, heads * group, sequences, sequences, 33, shared=n) for n in (0, shared)]
+    assert size[0] == size[1] and 8 * sequences * heads * group * dim > 1 << 30
+    Q = torch.randn(sequences, heads * group, dim, device="cuda", dtype=BF16)
+    assert torch.equal(lg.gemv_kv_attend(Q, cache, table, lens, shared=shared), lg.gemv_kv_attend(Q, cache, table, lens))
 
 
 def test_more_shared_than_the_table_holds():
