@@ -570,12 +570,13 @@ gemv_status_t gemv_kv_attend_bf16(const gemv_kv_cache_t *cache, const uint16_t *
 
 /* As gemv_kv_attend_*, for a batch whose sequences begin with the same tokens
  * (a common instruction or document): the first `shared` tokens of every
- * sequence that has them have the same keys and values.  Their tokens are read
- * and multiplied once for the whole batch, from the pages that the first row of
+ * sequence that has them have the same keys and values.  They are taken for the
+ * rows of all sequences together (32 or 16 rows at a time, where each sequence would
+ * read them for its own), from the pages that the first row of
  * the table names, whatever the first sequence's length; a shared token is there
  * where that row has its page.  (The other rows name a page for each shared token as well, the
- * same one or a copy: how many of the tokens are taken together is the
- * library's choice.)  shared == 0 computes what gemv_kv_attend_* does.  Other
+ * same one or a copy: how many of the tokens are taken together, and whether any
+ * are, is the library's choice, by which of the two is faster.)  shared == 0 computes what gemv_kv_attend_* does.  Other
  * arguments, results and errors are gemv_kv_attend_*'s, also for a negative
  * `shared`; the workspace has its own size, at most 2^30 bytes or what
  * gemv_kv_attend_* needs for the same sizes, whichever is more. */

@@ -1004,8 +1004,8 @@ def gemv_kv_attend(Q, cache, table, seq_lens, starts=None, *, scale=None, window
     table, seq_lens and starts as for ``gemv_kv_append``.  scale: 1 / sqrt(dim)
     by default.  window > 0: a token sees the last ``window`` tokens (itself
     among them) and the first ``sinks``.  shared > 0: the first ``shared`` tokens
-    are the same in every sequence, and are read once for the whole batch, from
-    the pages in the table's first row.  Rows of out behind the last start are
+    are the same in every sequence, and are taken for the rows of the whole batch
+    together where that is faster, from the pages in the table's first row.  Rows of out behind the last start are
     left as they were.  workspace: a device tensor of at least
     ``kv_attend_workspace_size(...)`` bytes, allocated here through torch when
     not given."""

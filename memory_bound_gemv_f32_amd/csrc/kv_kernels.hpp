@@ -952,10 +952,11 @@ __global__ __launch_bounds__(kWavesOf<WS> * 64, DIM <= 128 ? 2 : 1) void kv_atte
 // and 48, the shared ones in 512 workgroups.  In turns, the longer workgroups of the first part end late: 16 behind 65536
 // take 68 us instead of 55).
 //
-// The shared part is bound by the vector ALUs and by what two wavefronts a SIMD leave
+// Every 32 rows (16 of dim 256) widen all of the shared K and V for themselves.  So the
+// shared part is bound by the vector ALUs and by what two wavefronts a SIMD leave
 // unhidden of the steps' latency: 942 tokens of 32 heads over 4000 151 us, 410 TFLOP/s, 64 % of the
 // cycles with a vector or matrix instruction; 64 and 16 single tokens, whose shared workgroups
-// have a few steps each, 37 and 50 us with their own tokens.  K brought straight to
+// have a few steps each, 37 and 51 us with their own tokens.  K brought straight to
 // LDS a chunk ahead, and Q in registers then, change nothing or cost 9 %; wavefronts with rows of their
 // own, which do not fit the registers with masks and without, likewise.
 template <class T, class F, int DIM, int RT>

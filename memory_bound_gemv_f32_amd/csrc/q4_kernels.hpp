@@ -395,9 +395,11 @@ __device__ __forceinline__ void multiply(const Product& p, f32x4 (&acc)[RT][NT],
 // the order that the weights come out in; an fp32 vector as three, of its parts,
 // whose sums are added at the end.
 //
-// Bound by the memory's latency: nearly all of a wavefront's share is one batch, so
-// a call is a launch, a load and a join.  1 x 4096 x 4096 fp16 4.6 us (1.9 TB/s), 16
-// x 14336 x 4096 bf16 12.5 (2.5), fp32 1 x 4096 x 11008 with groups of 32 10.9 (2.7).
+// Bound by the latency of this mapping, not by memory: nearly all of a wavefront's share is
+// one batch with nothing in flight behind it, so a call is a launch, a load and a join.
+// 1 x 4096 x 4096 fp16 4.6 us (1.9 TB/s), 16 x 14336 x 4096 bf16 12.5 (2.5), fp32 1 x 4096
+// x 11008 with groups of 32 10.9 (2.7).  With weights that no cache holds the int8 rows of
+// gemv_q8 read twice the bytes of 1 x 14336 x 4096 in 11.0 us, where this takes 12.4.
 // A lane's 16 bytes are in another row than its neighbours', which costs the first
 // cache four accesses for one; loaded one behind the other and passed on through LDS
 // they take a quarter of the accesses and the same time or more (16 x 14336: 13.8).
