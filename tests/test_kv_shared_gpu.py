@@ -361,6 +361,25 @@ def test_workspace_and_graph():
             assert torch.equal(out, lg.gemv_kv_attend(Q, cache, *tensors, shared=640)), n
 
 
+def test_replayed_with_other_lengths():
+    """A captured call whose sequences grow, end and leave their place empty."""
+    for new in ([1] * 8, [3, 1, 2, 1, 1, 4, 1, 1]):
+        batch, cache, Q, tensors = check([700, 650, 660, 690, 680, 645, 641, 700], new, 640, page_size=64)
+        plain, lens = PlainCache(cache), tensors[1]
+        out = torch.empty_like(Q)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            lg.gemv_kv_attend(Q, cache, *tensors, shared=640, out=out)
+        for then in ([700, 0, 660, 690, 0, 645, 641, 1], [0] * 8, [2, 650, 0, 600, 640, 3, 64, 65], [690, 650, 660, 690, 680, 645, 641, 699]):
+            lens.copy_(torch.tensor(then, dtype=torch.int32))
+            batch.lens = then
+            out.fill_(5.0)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert_close(out, *attend(f64(Q), plain, batch, 128 ** -0.5, dtype=BF16), str(then))
+            assert torch.equal(out, lg.gemv_kv_attend(Q, cache, *tensors, shared=640)), then
+
+
 def test_other_stream():
     batch, cache, Q, tensors = check([700, 650, 660, 690], [1, 1, 1, 1], 640)
     want = lg.gemv_kv_attend(Q, cache, *tensors, shared=640)

@@ -217,6 +217,14 @@ def test_nan_with_low_bits_only():
     assert torch.isnan(lg.gemv_q4(Q, torch.ones(16, 1, device="cuda"), X.cuda(), group=32)).all()
 
 
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("M,K,nvec", [((1 << 20) + 77, 40, 2), (33, 70, (1 << 15) + 45), ((1 << 20) + 5, 9, 1)])
+def test_more_than_one_launch_holds(M, K, nvec, dtype):
+    """Rows past 2^20 and vectors past 2^15 go to launches of their own."""
+    for n, (zero, bias) in enumerate([(True, True), (False, False)]):
+        check(M, K, nvec, 32, dtype, out_dtype=(F32, dtype)[n], zero=zero, bias=bias, seed=n)
+
+
 @pytest.mark.parametrize("dtype,group", [(BF16, 128), (F16, 32), (F32, 64)])
 @pytest.mark.parametrize("K", [2 ** 31 - 1, 2 ** 31 - 128])
 def test_rows_up_to_an_int(K, dtype, group):
